@@ -11,8 +11,11 @@ and fails loudly if the library was not built.
 """
 from . import accounting, workloads  # noqa: F401
 from .binding import (  # noqa: F401
-    MOE_BF16, MOE_FP8_E4M3, MoeError, load_library, make_config, moe_combine,
-    moe_dispatch, moe_dispatch_layout, moe_error_string, moe_expert_standin, moe_get_layout,
+    MOE_BF16, MOE_FP8_E4M3, MoeError, load_library, make_config, make_expert_config, moe_combine,
+    moe_combine_backward, moe_dispatch, moe_dispatch_layout, moe_error_string,
+    moe_expert_backward, moe_expert_create, moe_expert_down, moe_expert_gated,
+    moe_expert_read_status, moe_expert_set_wait_limit, moe_expert_standin,
+    moe_expert_workspace_bytes, moe_get_layout,
     moe_handle_create, moe_read_status, moe_recv_rows_max, moe_route_dispatch_layout,
     moe_route_topk, moe_workspace_bytes)
 from .build import build  # noqa: F401

@@ -36,7 +36,9 @@ EXPORTED_SYMBOLS = (
     "moe_dispatch_two_stage", "moe_layout_dispatch_fused", "moe_set_wait_limit",
     "moe_dispatch_tokens", "moe_expert_standin_tokens", "moe_combine_tokens",
     "moe_dispatch_allgather", "moe_layout_tables", "moe_dispatch_fixed_slots",
-    "moe_fixed_slot_rows", "moe_debug_bounds",
+    "moe_fixed_slot_rows", "moe_debug_bounds", "moe_expert_workspace_bytes", "moe_expert_create",
+    "moe_expert_destroy", "moe_expert_gated", "moe_expert_down", "moe_expert_backward",
+    "moe_expert_set_wait_limit", "moe_expert_read_status", "moe_combine_backward",
 )
 
 
@@ -63,6 +65,12 @@ class moe_layout_view_t(ctypes.Structure):
 class moe_recv_meta_t(ctypes.Structure):
     _fields_ = [(n, _c_void_p) for n in (
         "local_expert", "src_rank", "src_token", "slot", "weight")]
+
+
+class moe_expert_config_t(ctypes.Structure):
+    _fields_ = [("num_experts", ctypes.c_int32), ("hidden", ctypes.c_int32),
+                ("inter", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("rows_max", ctypes.c_int64), ("train", ctypes.c_int32)]
 
 
 _lib = None
@@ -150,6 +158,25 @@ def load_library():
         lib.moe_copy_d2h_async.argtypes = [vp, vp, sz, vp]
         lib.moe_error_string.restype = ctypes.c_char_p
         lib.moe_error_string.argtypes = [i32]
+        xcfgp = ctypes.POINTER(moe_expert_config_t)
+        lib.moe_expert_workspace_bytes.restype = sz
+        lib.moe_expert_workspace_bytes.argtypes = [xcfgp]
+        lib.moe_expert_create.restype = i32
+        lib.moe_expert_create.argtypes = [xcfgp, vp, sz, ctypes.POINTER(vp)]
+        lib.moe_expert_destroy.restype = i32
+        lib.moe_expert_destroy.argtypes = [vp]
+        lib.moe_expert_gated.restype = i32
+        lib.moe_expert_gated.argtypes = [vp] * 10
+        lib.moe_expert_down.restype = i32
+        lib.moe_expert_down.argtypes = [vp] * 8
+        lib.moe_expert_backward.restype = i32
+        lib.moe_expert_backward.argtypes = [vp] * 12
+        lib.moe_expert_set_wait_limit.restype = i32
+        lib.moe_expert_set_wait_limit.argtypes = [vp, i64]
+        lib.moe_expert_read_status.restype = i32
+        lib.moe_expert_read_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), vp]
+        lib.moe_combine_backward.restype = i32
+        lib.moe_combine_backward.argtypes = [vp] * 7
         lib.moe_debug_bounds.restype = i32
         lib.moe_debug_bounds.argtypes = []
         _lib = lib
@@ -358,6 +385,134 @@ def moe_expert_standin(h: Handle, recv_x, recv_scale, expert_scale, y, stream=No
 def moe_combine(h: Handle, y, w, out, stream=None) -> None:
     _check("moe_combine", load_library().moe_combine(
         h.ptr, _ptr(y), _ptr(w), _ptr(out), _stream(stream)))
+
+
+def _buf(name: str, t, count: int, size: int, optional: bool = False) -> Optional[int]:
+    """Device pointer of a tensor that must hold `count` elements of `size` bytes."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name}: a tensor is needed")
+    if t.element_size() != size or t.numel() < count:
+        raise ValueError(f"{name}: expected at least {count} elements of {size} bytes, "
+                         f"got {t.numel()} of {t.dtype}")
+    return _ptr(t)
+
+
+def moe_combine_backward(h: Handle, dout, y, w, dy, dw, stream=None) -> None:
+    """Gradients of moe_combine on the last dispatch's layout (see the header)."""
+    c = h.cfg
+    T = c.num_ranks * c.tokens_per_rank
+    _check("moe_combine_backward", load_library().moe_combine_backward(
+        h.ptr, _buf("dout", dout, T * c.hidden, 2), _ptr(y), _buf("w", w, T * c.top_k, 4),
+        _buf("dy", dy, y.numel(), 2), _buf("dw", dw, T * c.top_k, 4), _stream(stream)))
+
+
+def make_expert_config(E: int, H: int, F: int, rows_max: int, dtype: int = MOE_BF16,
+                       train: bool = False) -> moe_expert_config_t:
+    """E experts of hidden width H and inner width F over up to rows_max rows."""
+    return moe_expert_config_t(E, H, F, dtype, rows_max, int(train))
+
+
+def moe_expert_workspace_bytes(cfg: moe_expert_config_t) -> int:
+    return int(load_library().moe_expert_workspace_bytes(ctypes.byref(cfg)))
+
+
+class ExpertHandle:
+    """Owns the C handle of an expert block and keeps its workspace tensor alive."""
+
+    def __init__(self, cfg: moe_expert_config_t, workspace):
+        self.cfg = cfg
+        self.workspace = workspace
+        self.fp8 = cfg.dtype == MOE_FP8_E4M3
+        h = _c_void_p()
+        _check("moe_expert_create", load_library().moe_expert_create(
+            ctypes.byref(cfg), _ptr(workspace), workspace.numel() * workspace.element_size(),
+            ctypes.byref(h)))
+        self._h = h
+
+    @property
+    def ptr(self):
+        return self._h
+
+    def close(self):
+        if self._h:
+            load_library().moe_expert_destroy(self._h)
+            self._h = _c_void_p()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def moe_expert_create(cfg: moe_expert_config_t, workspace=None, device=None) -> ExpertHandle:
+    """Creates a handle; allocates the workspace with torch when none is given."""
+    import torch
+    if workspace is None:
+        nbytes = moe_expert_workspace_bytes(cfg)
+        if nbytes == 0:
+            _check("moe_expert_workspace_bytes", -1)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device or "cuda")
+    return ExpertHandle(cfg, workspace)
+
+
+def _scale(name: str, x: ExpertHandle, t, count: int) -> Optional[int]:
+    if t is None and not x.fp8:
+        return None
+    return _buf(name, t, count // 128, 4)
+
+
+def moe_expert_gated(x: ExpertHandle, expert_offset, inp, inp_scale, w13, w13_scale, hid,
+                     hid_scale=None, gate_up=None, stream=None) -> None:
+    """hid = silu(inp Wg^T) * (inp Wu^T) over the experts' segments (see the header)."""
+    c, elt = x.cfg, 1 if x.fp8 else 2
+    E, H, F, R = c.num_experts, c.hidden, c.inter, c.rows_max
+    _check("moe_expert_gated", load_library().moe_expert_gated(
+        x.ptr, _buf("expert_offset", expert_offset, E + 1, 4), _buf("inp", inp, R * H, elt),
+        _scale("inp_scale", x, inp_scale, R * H), _buf("w13", w13, E * 2 * F * H, elt),
+        _scale("w13_scale", x, w13_scale, E * 2 * F * H // 128), _buf("hid", hid, R * F, elt),
+        _scale("hid_scale", x, hid_scale, R * F),
+        _buf("gate_up", gate_up, R * 2 * F, 2, optional=True), _stream(stream)))
+
+
+def moe_expert_down(x: ExpertHandle, expert_offset, hid, hid_scale, w2, w2_scale, y,
+                    stream=None) -> None:
+    """y = hid W2^T over the experts' segments (see the header)."""
+    c, elt = x.cfg, 1 if x.fp8 else 2
+    E, H, F, R = c.num_experts, c.hidden, c.inter, c.rows_max
+    _check("moe_expert_down", load_library().moe_expert_down(
+        x.ptr, _buf("expert_offset", expert_offset, E + 1, 4), _buf("hid", hid, R * F, elt),
+        _scale("hid_scale", x, hid_scale, R * F), _buf("w2", w2, E * H * F, elt),
+        _scale("w2_scale", x, w2_scale, E * H * F // 128), _buf("y", y, R * H, 2),
+        _stream(stream)))
+
+
+def moe_expert_backward(x: ExpertHandle, expert_offset, inp, gate_up, hid, dy, w13, w2, dx=None,
+                        dw13=None, dw2=None, stream=None) -> None:
+    """Gradients of the gated block; dx, or dw13 and dw2 together, may be left out."""
+    c = x.cfg
+    E, H, F, R = c.num_experts, c.hidden, c.inter, c.rows_max
+    _check("moe_expert_backward", load_library().moe_expert_backward(
+        x.ptr, _buf("expert_offset", expert_offset, E + 1, 4), _buf("inp", inp, R * H, 2),
+        _buf("gate_up", gate_up, R * 2 * F, 2), _buf("hid", hid, R * F, 2),
+        _buf("dy", dy, R * H, 2), _buf("w13", w13, E * 2 * F * H, 2),
+        _buf("w2", w2, E * H * F, 2), _buf("dx", dx, R * H, 2, optional=True),
+        _buf("dw13", dw13, E * 2 * F * H, 2, optional=True),
+        _buf("dw2", dw2, E * H * F, 2, optional=True), _stream(stream)))
+
+
+def moe_expert_set_wait_limit(x: ExpertHandle, cycles: int) -> None:
+    _check("moe_expert_set_wait_limit",
+           load_library().moe_expert_set_wait_limit(x.ptr, int(cycles)))
+
+
+def moe_expert_read_status(x: ExpertHandle, stream=None) -> int:
+    flags = ctypes.c_uint32(0)
+    _check("moe_expert_read_status", load_library().moe_expert_read_status(
+        x.ptr, ctypes.byref(flags), _stream(stream)))
+    return int(flags.value)
 
 
 def moe_read_status(h: Handle, stream=None) -> int:

@@ -796,6 +796,26 @@ int moe_combine_tokens(moe_handle_t h, int64_t token_begin, int64_t token_end, c
   return combine_range(h, token_begin, token_end, y, w, out, stream);
 }
 
+int moe_combine_backward(moe_handle_t h, const void* dout, const void* y, const float* w, void* dy,
+                         float* dw, void* stream) {
+  if (!h || !dout || !y || !w || !dy || !dw) return MOE_ERR_INVALID_ARG;
+  if (!aligned(dout, 16) || !aligned(y, 16) || !aligned(dy, 16)) return MOE_ERR_INVALID_ARG;
+  if (h->dispatch_gen == 0 || h->dispatch_gen != h->layout_gen) return MOE_ERR_STATE;
+  moe::CombineBackwardArgs a{};
+  a.dout = static_cast<const uint16_t*>(dout);
+  a.y = static_cast<const uint16_t*>(y);
+  a.w = w;
+  a.inv = h->inv;
+  a.dy = static_cast<uint16_t*>(dy);
+  a.dw = dw;
+  a.T = h->T;
+  a.rows = h->fixed_rows ? fixed_slot_rows(&h->cfg) : h->rows_max;
+  a.k = h->cfg.top_k;
+  a.H = h->cfg.hidden;
+  a.status = h->status;
+  return cuda_rc(moe::launch_combine_backward(a, h->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
 int moe_expert_standin_tokens(moe_handle_t h, int64_t token_begin, int64_t token_end,
                               const void* recv_x, const float* recv_scale,
                               const float* expert_scale, void* y, void* stream) {

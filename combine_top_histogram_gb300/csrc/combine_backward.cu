@@ -1,0 +1,114 @@
+// combine_backward.cu -- the gradients of the weighted top-k sum.
+//
+// out[g] = sum_j w[g,j] y[inv[g,j]], so with dout[g] the gradient of out[g]
+//   dy[inv[g,j]] = w[g,j] dout[g]            (each receive row has one slot)
+//   dw[g,j]      = <dout[g], y[inv[g,j]]>    (0 for masked and dropped slots)
+//
+// One pass: a CTA takes a token, each thread holds its 16-byte pieces of
+// dout[g] and, for every slot, reads the same pieces of the slot's y row
+// (all slots' loads before the first product), adds their products in fp32
+// and writes the scaled pieces to the slot's dy row. The k sums are then
+// reduced over the CTA in a fixed order (no atomics: the same inputs give the
+// same bits). Bound by HBM: y in, dy out, dout once.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "internal.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 128;
+
+__device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+
+__device__ __forceinline__ uint32_t scale2(uint32_t u, float w) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(__fmul_rn(w, lo_f(u)), __fmul_rn(w, hi_f(u)));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ float dot8(const uint4 a, const uint4 b, float acc) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    acc = __fmaf_rn(lo_f(x[q]), lo_f(y[q]), acc);
+    acc = __fmaf_rn(hi_f(x[q]), hi_f(y[q]), acc);
+  }
+  return acc;
+}
+
+// K slots at a time: K == k for the common k, 8 otherwise (any k).
+template <int K>
+__global__ void __launch_bounds__(kThreads) k_combine_backward(const CombineBackwardArgs p) {
+  __shared__ int rows_buf[2][MOE_MAX_TOPK];
+  __shared__ float w_buf[2][MOE_MAX_TOPK];
+  __shared__ float part[2][kThreads / 32][MOE_MAX_TOPK];
+  const int nvec = p.H >> 3, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int par = 0;
+  pdl_wait();
+  for (long long g = blockIdx.x; g < p.T; g += gridDim.x) {
+    int* rows_s = rows_buf[par];
+    float* w_s = w_buf[par];
+    if (tid < p.k) {
+      const int r = __ldg(p.inv + g * p.k + tid);
+      rows_s[tid] = (r >= 0 && row_ok(r, p.rows, p.status)) ? r : -1;
+      w_s[tid] = __ldg(p.w + g * p.k + tid);
+    }
+    __syncthreads();
+    const uint4* d = reinterpret_cast<const uint4*>(p.dout + g * p.H);
+    for (int j0 = 0; j0 < p.k; j0 += K) {
+      float acc[K];
+#pragma unroll
+      for (int j = 0; j < K; ++j) acc[j] = 0.0f;
+      for (int v = tid; v < nvec; v += kThreads) {
+        const uint4 dv = __ldg(d + v);
+        uint4 yv[K];
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+          const int r = j0 + j < p.k ? rows_s[j0 + j] : -1;
+          yv[j] = r >= 0 ? __ldcs(reinterpret_cast<const uint4*>(p.y + (long long)r * p.H) + v)
+                         : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+          const int r = j0 + j < p.k ? rows_s[j0 + j] : -1;
+          if (r < 0) continue;
+          acc[j] = dot8(dv, yv[j], acc[j]);
+          const float w = w_s[j0 + j];
+          __stcs(reinterpret_cast<uint4*>(p.dy + (long long)r * p.H) + v,
+                 make_uint4(scale2(dv.x, w), scale2(dv.y, w), scale2(dv.z, w), scale2(dv.w, w)));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < K; ++j) {
+        for (int o = 16; o > 0; o >>= 1) acc[j] += __shfl_xor_sync(~0u, acc[j], o);
+        if (lane == 0 && j0 + j < p.k) part[par][warp][j0 + j] = acc[j];
+      }
+    }
+    __syncthreads();
+    if (tid < p.k)
+      p.dw[g * p.k + tid] = rows_s[tid] < 0 ? 0.0f
+                                            : (part[par][0][tid] + part[par][1][tid]) +
+                                                  (part[par][2][tid] + part[par][3][tid]);
+    par ^= 1;  // the other buffers next: these are read until the next token's barriers
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_combine_backward(const CombineBackwardArgs& a, int num_sms, cudaStream_t st) {
+  long long blocks = a.T;
+  const long long cap = (long long)num_sms * 16;
+  if (blocks > cap) blocks = cap;
+  const dim3 grid((unsigned)blocks), block(kThreads);
+  switch (a.k) {
+    case 1: return launch_pdl(k_combine_backward<1>, grid, block, 0, st, a);
+    case 2: return launch_pdl(k_combine_backward<2>, grid, block, 0, st, a);
+    case 4: return launch_pdl(k_combine_backward<4>, grid, block, 0, st, a);
+    default: return launch_pdl(k_combine_backward<8>, grid, block, 0, st, a);
+  }
+}
+
+}  // namespace moe

@@ -183,6 +183,20 @@ struct CombineArgs {
   uint32_t* status;       // MOE_STATUS_BOUNDS (debug bounds checks)
 };
 
+// Gradients of the combine (combine_backward.cu).
+struct CombineBackwardArgs {
+  const uint16_t* dout;   // bf16 [T*H]
+  const uint16_t* y;      // bf16 [rows*H]
+  const float* w;         // [T*k]
+  const int32_t* inv;     // [T*k]
+  uint16_t* dy;           // bf16 [rows*H]
+  float* dw;              // [T*k]
+  long long T;
+  long long rows;         // rows of y and dy
+  int k, H;
+  uint32_t* status;       // MOE_STATUS_BOUNDS (debug bounds checks)
+};
+
 struct StandinArgs {
   const int32_t* inv;      // token-range form: rows of assignments [a0, a1)
   long long a0, a1;
@@ -261,6 +275,7 @@ cudaError_t layout_prepare_all(size_t* layout_dyn_max, size_t* scan_dyn_max);
 cudaError_t launch_dispatch(const DispatchArgs& a, bool fp8, int num_sms, cudaStream_t st);
 cudaError_t launch_tables(const TablesArgs& t, cudaStream_t st);
 cudaError_t launch_combine(const CombineArgs& a, int num_sms, cudaStream_t st);
+cudaError_t launch_combine_backward(const CombineBackwardArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_standin(const StandinArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_standin_tokens(const StandinArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_send_pos(const int32_t* kept_cnt, int32_t* send_pos, int32_t* src_base, int P,

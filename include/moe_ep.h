@@ -392,6 +392,105 @@ int moe_expert_standin_tokens(moe_handle_t h, int64_t token_begin, int64_t token
 int moe_combine_tokens(moe_handle_t h, int64_t token_begin, int64_t token_end, const void *y,
                        const float *w, void *out, void *stream);
 
+/* ---- experts: the gated feed-forward block over the receive segments --------
+ * What runs between dispatch and combine, and its way back. The pages leave
+ * the experts' grouped products out ("per-expert counts for a later grouped
+ * GEMM"); these operators fill that place. For every row r of expert e's
+ * segment [expert_offset[e], expert_offset[e+1]):
+ *   moe_expert_gated     g = x_r Wg^T, u = x_r Wu^T, h_r = g/(1+exp(-g)) * u
+ *   moe_expert_down      y_r = h_r W2^T
+ *   moe_expert_backward  dx_r, and dW13[e], dW2[e] summed over e's rows
+ *   moe_combine_backward dy_r = w[g,j] dout[g], dw[g,j] = <dout[g], y_r>
+ * Layouts (row-major, contiguous): x [rows_max, H]; w13 [E, 2F, H], the F gate
+ * rows before the F up rows; h [rows_max, F]; w2 [E, H, F]; y [rows_max, H].
+ * MOE_BF16: all of them bf16. MOE_FP8_E4M3 (serving): x, h, w13 and w2 are e4m3
+ * codes; x and h carry an fp32 scale for each 128 channels of a row (as
+ * moe_dispatch writes them: x_scale [rows_max, H/128], h_scale
+ * [rows_max, F/128]), the weights one for each 128 x 128 block (w13_scale
+ * [E, 2F/128, H/128], w2_scale [E, H/128, F/128]); a value is code * scale.
+ * moe_expert_gated then quantises h with the dispatch's rule (s = amax/448,
+ * codes e4m3 RNE satfinite of h/s, an all-zero block has s = 0 and zero codes);
+ * y is bf16. Sums are fp32; FP8 sums are exact products of codes added up
+ * within each 128-channel block, then scaled and added in fp32.
+ * expert_offset is int32 [E+1] on the device: the layout's expert_offset of a
+ * compact dispatch (moe_dispatch and its comparators; not the fixed-slot
+ * layout, whose regions it does not describe), or the caller's own
+ * ({0, n} with E = 1 is a dense block). Values outside [0, rows_max] and
+ * descending ends are clamped, so no row outside the buffers is touched. Rows
+ * outside every segment are neither read into a result nor written.
+ * All pointers are device pointers, 16-byte aligned (scales 4-byte). Calls are
+ * asynchronous on `stream`, allocate nothing, can be captured in a CUDA graph,
+ * and on one handle must be ordered on one stream. */
+typedef struct {
+    int32_t num_experts; /* E >= 1, <= MOE_MAX_EXPERTS */
+    int32_t hidden;      /* H, a multiple of 8; of 128 for FP8 */
+    int32_t inter;       /* F, a multiple of 8; of 128 for FP8 */
+    int32_t dtype;       /* MOE_BF16 or MOE_FP8_E4M3 */
+    int64_t rows_max;    /* rows every row buffer holds (moe_recv_rows_max) */
+    int32_t train;       /* 1: the handle also runs moe_expert_backward (MOE_BF16 only) */
+} moe_expert_config_t;
+
+typedef struct moe_expert *moe_expert_t;
+
+/* Bytes of device workspace of a handle (0 if *cfg is invalid): control words
+ * and, for training, the gradient of the pre-activations [rows_max, 2F]. */
+size_t moe_expert_workspace_bytes(const moe_expert_config_t *cfg);
+
+/* Creates a handle over d_workspace (256-byte aligned, the caller's). As
+ * moe_handle_create: a synchronous cudaMemset of the control words on the
+ * current device; outside stream capture. Errors: INVALID_ARG, UNSUPPORTED,
+ * WORKSPACE, CUDA. */
+int moe_expert_create(const moe_expert_config_t *cfg, void *d_workspace, size_t bytes,
+                      moe_expert_t *out);
+int moe_expert_destroy(moe_expert_t x);
+
+/* h = silu(x Wg^T) * (x Wu^T). x_scale, w13_scale and hid_scale are NULL for
+ * bf16. gate_up: NULL, or (bf16) [rows_max, 2F] that receives the
+ * pre-activations g and u, rounded to bf16, for moe_expert_backward.
+ * Errors: INVALID_ARG, CUDA. */
+int moe_expert_gated(moe_expert_t x, const int32_t *expert_offset, const void *in,
+                     const float *in_scale, const void *w13, const float *w13_scale, void *hid,
+                     float *hid_scale, void *gate_up, void *stream);
+
+/* y = h W2^T, bf16 [rows_max, H]. Errors: INVALID_ARG, CUDA. */
+int moe_expert_down(moe_expert_t x, const int32_t *expert_offset, const void *hid,
+                    const float *hid_scale, const void *w2, const float *w2_scale, void *y,
+                    void *stream);
+
+/* The block's gradients from dy [rows_max, H], the inputs of the forward calls
+ * and the kept pre-activations: with dh = dy W2, s = 1/(1+exp(-g)),
+ * dg = dh u s (1 + g (1 - s)) and du = dh g s,
+ *   dx = dg Wg + du Wu           [rows_max, H]
+ *   dw13[e] = [dg du]^T x        [E, 2F, H], summed over e's rows
+ *   dw2[e] = dy^T h              [E, H, F]
+ * all bf16, overwritten (an expert without rows gets zeros). dg and du are
+ * rounded to bf16 between the products, as the tensor cores take them. Needs a
+ * handle with train = 1. dx, or both weight gradients together, may be NULL:
+ * they are then not computed. Errors: INVALID_ARG, STATE (train = 0), CUDA. */
+int moe_expert_backward(moe_expert_t x, const int32_t *expert_offset, const void *in,
+                        const void *gate_up, const void *hid, const void *dy, const void *w13,
+                        const void *w2, void *dx, void *dw13, void *dw2, void *stream);
+
+/* Clock cycles a bounded device wait may last before its kernel gives up
+ * (default 2^32, about two seconds): it then sets MOE_STATUS_TIMEOUT and
+ * leaves with its outputs undefined; the next call works normally. 0 makes
+ * every wait that does not succeed at once give up: for testing that path. */
+int moe_expert_set_wait_limit(moe_expert_t x, int64_t cycles);
+
+/* Reads and clears the handle's device status word (MOE_STATUS_* bits).
+ * Synchronises `stream`. */
+int moe_expert_read_status(moe_expert_t x, uint32_t *flags, void *stream);
+
+/* Gradients of moe_combine on the layout of the last dispatch: for every slot
+ * with inv[g*k+j] >= 0, dy[inv[g*k+j]] = bf16(w[g,j] * dout[g]) and
+ * dw[g,j] = sum_c dout[g,c] * y[inv[g*k+j],c] (fp32); masked and dropped slots
+ * get dw = 0. dout: bf16 [T, H]; y, dy: bf16 rows as moe_combine's y (both
+ * layouts); w, dw: fp32 [T, k]. Rows that no slot names are not written. (The
+ * gradient of a bf16 dispatch is moe_combine with unit weights.)
+ * Errors: INVALID_ARG, STATE, CUDA. */
+int moe_combine_backward(moe_handle_t h, const void *dout, const void *y, const float *w, void *dy,
+                         float *dw, void *stream);
+
 /* Housekeeping (no counterpart on the pages): reads and clears the device
  * status word. Synchronises `stream`: tests and debugging only. *flags
  * receives MOE_STATUS_* bits. */
