@@ -31,6 +31,12 @@ int validate(const moe_expert_config_t* c) {
   // the joint gate and up projection
   if (c->rows_max >= (1ll << 31) - 256 || c->inter > (1 << 29) || c->hidden > (1 << 29))
     return MOE_ERR_UNSUPPORTED;
+  // int32 tile numbers: 128 rows x 128 columns at least, per expert and widest
+  // side of a product
+  const long long wide = (c->hidden > 2ll * c->inter ? c->hidden : 2ll * c->inter) / 128 + 1;
+  if ((c->rows_max / 128 + c->num_experts) * wide >= (1ll << 31) ||
+      wide * wide * c->num_experts >= (1ll << 31))
+    return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

@@ -10,11 +10,14 @@
 //   kDx     dx = [dg du] W13                        A = dgu, B = w13 (N-major)
 //   kDw     dW = a^T b over the segment's rows      A = a (M-major), B = b (N-major)
 //
-// One persistent CTA per SM computes 128 x 256 tiles. One thread copies
-// operand tiles (128 bytes along the contiguous axis, 128-byte swizzle) with
-// TMA into a ring of stages, one thread issues the tcgen05 products into one
-// of two 256-column TMEM accumulators, and eight warps read the other one
-// back, so a tile's epilogue runs beside the next tile's products.
+// One persistent CTA per SM. A CTA computes 128 x 256 tiles, or the two CTAs
+// of a cluster compute 256 x 256 tiles together (CG = 2): each holds its 128
+// rows of A and accumulator and half of B's columns, and the first CTA issues
+// the products of both. One thread per CTA copies operand tiles (128 bytes
+// along the contiguous axis, 128-byte swizzle) with TMA into a ring of stages,
+// one thread issues the tcgen05 products into one of two 256-column TMEM
+// accumulators, and eight warps read the other one back, so a tile's epilogue
+// runs beside the next tile's products.
 // With e4m3 operands the products of one 128-channel block are a partial sum
 // that the eight warps multiply by the row's and the block's fp32 scales and
 // add up in registers: the accumulators then alternate per block.
@@ -36,86 +39,126 @@
 namespace moe {
 namespace {
 
-constexpr int kTileM = 128;
+constexpr int kTileM = 128;            // rows of one CTA's accumulator
 constexpr int kTileN = 256;
 constexpr int kThreads = 384;          // copy, product, TMEM, spare; 8 epilogue warps
 constexpr int kEpiWarp0 = 4;
-constexpr int kStages = 4;
 constexpr int kABytes = kTileM * 128;  // a stage holds 128 bytes of K (or 64 k) per row
-constexpr int kBBytes = kTileN * 128;
-constexpr int kStageBytes = kABytes + kBBytes;
+template <int CG>
+struct Ring {
+  static constexpr int kBRows = kTileN / CG;  // rows (or columns) of B in one CTA
+  static constexpr int kStageBytes = kABytes + kBRows * 128;
+  static constexpr int kStages = CG == 2 ? 6 : 4;
+};
+constexpr int kRingBytes = 192 * 1024;
+static_assert(Ring<1>::kStages * Ring<1>::kStageBytes == kRingBytes, "ring");
+static_assert(Ring<2>::kStages * Ring<2>::kStageBytes == kRingBytes, "ring");
+constexpr int kMaxStages = 6;
 constexpr int kEpiBytes = 8 * 2048;    // 32 rows x 64 bytes per epilogue warp
 constexpr int kGroupM = 8;             // row tiles that share weight tiles in L2
 
 struct Shared {
-  uint64_t full[kStages], empty[kStages];
+  uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t tfull[2], tempty[2], drain;
+  uint64_t tail[kMaxStages];           // kDw, second CTA: its copies of a segment's last block
   uint32_t tmem;
   int abort;
   uint64_t pair[4];                    // the two warps of a lane quarter exchange amax
   float amax[2][2][kTileM];            // [tile parity][half][row]
+  uint64_t sempty[2];                  // the epilogue has read scale[i]
+  float2 scale[2][kTileM];             // FP8: row scale x scales of the tile's two weight blocks
   int off[MOE_MAX_EXPERTS + 1];
   int pre[MOE_MAX_EXPERTS + 1];        // row tiles before expert e
 };
 
-constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kEpiBytes + (int)sizeof(Shared);
+constexpr int kSmemBytes = 1024 + kRingBytes + kEpiBytes + (int)sizeof(Shared);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
 
 struct Tile {
   int e;
-  int row0;     // first row (kDw: first row of the segment)
+  int row0;     // this CTA's first row (kDw: first row of the segment)
   int rows;     // rows of the segment from row0 on (kDw: the reduction length)
-  int m0;       // kDw: first gradient row
+  int m0;       // kDw: this CTA's first gradient row
   int n0;       // first output column
   int kb;       // reduction blocks
 };
 
-// Tile t of the launch. Row tiles of one expert are taken in groups of
-// kGroupM that walk the columns together, so that concurrent CTAs share both
-// operands in L2.
-template <int OP>
-__device__ __forceinline__ bool get_tile(long long t, const ExpertArgs& p, const Shared& s,
-                                         int k_elems, Tile& o) {
-  if (OP == kDw) {
-    const int mt = (p.M + kTileM - 1) / kTileM;
-    const int per = mt * p.nt;
-    if (t >= (long long)per * p.E) return false;
-    o.e = (int)(t / per);
-    const int local = (int)(t - (long long)o.e * per);
-    o.row0 = s.off[o.e];
-    o.rows = s.off[o.e + 1] - o.row0;
-    const int g = local / (kGroupM * p.nt), gs = min(kGroupM, mt - g * kGroupM);
-    const int idx = local - g * kGroupM * p.nt;
-    o.m0 = (g * kGroupM + idx % gs) * kTileM;
-    o.n0 = idx / gs;
-    o.kb = (o.rows + 63) >> 6;
+// The tiles of one CTA (or pair), in order: tile0, tile0 + step, ... of the
+// launch. Row tiles of one expert are taken in groups of kGroupM that walk the
+// columns together, so that concurrent CTAs share both operands in L2. Each
+// role walks for itself; a step costs two divisions and, within an expert or
+// to one of the next few, no search.
+template <int OP, int CG>
+struct Walk {
+  static constexpr int kRows = kTileM * CG;
+  const ExpertArgs& p;
+  const Shared& s;
+  const int k_elems, rank, step, mt_w;
+  int t, e, base, per;  // tile, its expert, the expert's first tile and tiles
+
+  __device__ __forceinline__ Walk(const ExpertArgs& pa, const Shared& sh, int ke, int rk, int tile0,
+                                  int st)
+      : p(pa), s(sh), k_elems(ke), rank(rk), step(st),
+        mt_w(OP == kDw ? (pa.M + kRows - 1) / kRows : 0), t(tile0 - st), e(0), base(0) {
+    per = tiles(0);
+  }
+
+  __device__ __forceinline__ int tiles(int x) const {
+    return (OP == kDw ? mt_w : s.pre[x + 1] - s.pre[x]) * p.nt;
+  }
+
+  __device__ __forceinline__ bool next(Tile& o) {
+    t += step;
+    if (t >= (OP == kDw ? mt_w * p.E : s.pre[p.E]) * p.nt) return false;
+    if (OP == kDw) {
+      if (t - base >= per) {
+        e = t / per;
+        base = e * per;
+      }
+    } else {
+      for (int i = 0; i < 4 && t - base >= per; ++i) {
+        base += per;
+        per = tiles(++e);
+      }
+      if (t - base >= per) {
+        int lo = e, hi = p.E - 1;  // largest e with pre[e] * nt <= t
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (s.pre[mid] * p.nt <= t) lo = mid;
+          else hi = mid - 1;
+        }
+        e = lo;
+        base = s.pre[e] * p.nt;
+        per = tiles(e);
+      }
+    }
+    const int mt = OP == kDw ? mt_w : s.pre[e + 1] - s.pre[e];
+    const uint32_t local = t - base, group = kGroupM * p.nt;
+    const uint32_t g = local / group, idx = local - g * group;
+    const uint32_t gs = min(kGroupM, mt - (int)g * kGroupM);
+    const uint32_t n = gs == kGroupM ? idx / kGroupM : idx / gs;
+    const int m = (int)(g * kGroupM + idx - n * gs) * kRows + rank * kTileM;
+    o.e = e;
+    o.n0 = (int)n;
+    if (OP == kDw) {
+      o.row0 = s.off[e];
+      o.rows = s.off[e + 1] - o.row0;
+      o.m0 = m;
+      o.kb = (o.rows + 63) >> 6;
+    } else {
+      o.row0 = s.off[e] + m;
+      o.rows = s.off[e + 1] - o.row0;
+      o.m0 = 0;
+      o.kb = (p.K + k_elems - 1) / k_elems;
+    }
     return true;
   }
-  if (t >= (long long)s.pre[p.E] * p.nt) return false;
-  int lo = 0, hi = p.E - 1;  // largest e with pre[e] * nt <= t
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if ((long long)s.pre[mid] * p.nt <= t) lo = mid;
-    else hi = mid - 1;
-  }
-  o.e = lo;
-  const long long local = t - (long long)s.pre[lo] * p.nt;
-  const int mt = s.pre[lo + 1] - s.pre[lo];
-  const int g = (int)(local / ((long long)kGroupM * p.nt));
-  const int gs = min(kGroupM, mt - g * kGroupM);
-  const int idx = (int)(local - (long long)g * kGroupM * p.nt);
-  const int m = g * kGroupM + idx % gs;
-  o.row0 = s.off[lo] + m * kTileM;
-  o.rows = s.off[lo + 1] - o.row0;
-  o.m0 = 0;
-  o.n0 = idx / gs;
-  o.kb = (p.K + k_elems - 1) / k_elems;
-  return true;
-}
+};
 
 // The segments and the row tiles before each expert, once per CTA. Offsets
 // are held to [0, rows_max] and to ascending order, so no row index that
 // follows from them leaves a row buffer.
+template <int CG>
 __device__ __forceinline__ void load_segments(const ExpertArgs& p, Shared& s) {
   for (int e = threadIdx.x; e <= p.E; e += kThreads) {
     const long long o = p.offset[e];
@@ -137,7 +180,7 @@ __device__ __forceinline__ void load_segments(const ExpertArgs& p, Shared& s) {
       if (lane == 0) begin = top;
       top = __shfl_sync(~0u, end, 31);
       const int n = e < p.E ? max(end - begin, 0) : 0;
-      const int tiles = (n + kTileM - 1) / kTileM;
+      const int tiles = (n + kTileM * CG - 1) / (kTileM * CG);
       int sum = tiles;
       for (int d = 1; d < 32; d <<= 1) {
         const int v = __shfl_up_sync(~0u, sum, d);
@@ -322,16 +365,27 @@ __device__ __forceinline__ void epilogue_bf16(const ExpertArgs& p, const Tile& t
   }
 }
 
-__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t s) {
-  const uint64_t v = (uint64_t)lo | ((uint64_t)hi << 32);
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(s));
+// An epilogue warp has read accumulator `as`: tells the CTA that issues the
+// products.
+template <int CG>
+__device__ __forceinline__ void release(Shared& s, int as) {
+  if constexpr (CG == 2) mbar_arrive_relaxed(cluster_addr(smem_u32(&s.tempty[as]), 0));
+  else mbar_arrive(smem_u32(&s.tempty[as]));
 }
-__device__ __forceinline__ uint64_t both(float s) {
-  const uint32_t u = __float_as_uint(s);
-  return (uint64_t)u | ((uint64_t)u << 32);
-}
-__device__ __forceinline__ float part(const uint64_t (&acc)[64], int i) {
-  return __uint_as_float((uint32_t)(acc[i >> 1] >> (32 * (i & 1))));
+
+// Rows from `valid` to the next multiple of 16 of a stage's CHUNKS M- or
+// N-major operand pieces (64 lines of 128 bytes each) become zero, for the
+// tensor cores to read. Whole warp.
+template <int CHUNKS>
+__device__ __forceinline__ void clear_rows(uint8_t* stage, int valid, int lane) {
+  uint4* base = reinterpret_cast<uint4*>(stage);
+  const int units = (((valid + 15) & ~15) - valid) * 8;  // 16-byte units of one piece
+  for (int i = lane; i < units * CHUNKS; i += 32) {
+    const int chunk = i / units, r = i - chunk * units;
+    base[chunk * 512 + valid * 8 + r] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_async_smem();
+  __syncwarp();
 }
 
 // With e4m3 operands an epilogue thread holds 128 sums. The CTA launches with
@@ -346,31 +400,151 @@ __device__ __forceinline__ void take_registers() {
   if constexpr (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
 }
 
-template <int OP, bool FP8>
+// The warp that issues the products: its place in the ring of stages and in
+// the two accumulators.
+template <int CG, bool FP8, bool AMN, bool BMN>
+struct Issuer {
+  static constexpr int kStages = Ring<CG>::kStages, kStageBytes = Ring<CG>::kStageBytes;
+  static constexpr uint32_t kIdesc = mma_desc(FP8, AMN, BMN, kTileM * CG, kTileN);
+  // 16 k of bf16 (32 of e4m3): 32 bytes along K, or 16 lines of 128 bytes
+  static constexpr uint64_t kA = (AMN ? 2048 : 32) >> 4, kB = (BMN ? 2048 : 32) >> 4;
+  const uint32_t full0, empty0, tfull0, tempty0, tmem;
+  const uint64_t da0, db0;
+  const WaitCtl& ctl;
+  int st = 0, as = 0;
+  uint32_t ph = 0, aph = 1;
+
+  __device__ __forceinline__ Issuer(Shared& s, uint8_t* smem, uint32_t tm, const WaitCtl& c)
+      : full0(smem_u32(s.full)), empty0(smem_u32(s.empty)), tfull0(smem_u32(s.tfull)),
+        tempty0(smem_u32(s.tempty)), tmem(tm),
+        da0(smem_desc(smem_u32(smem), AMN ? 8192 : 16, 1024)),
+        db0(smem_desc(smem_u32(smem) + kABytes, BMN ? 8192 : 16, 1024)), ctl(c) {}
+
+  // Waits for a stage's operands and, where a sum begins, for its accumulator.
+  __device__ __forceinline__ bool wait(bool begins) {
+    bool ok = mbar_wait<CG == 2>(full0 + st * 8, ph, ctl);
+    if (begins) ok = ok && mbar_wait<CG == 2>(tempty0 + as * 8, aph, ctl);
+    ok = __all_sync(~0u, ok);
+    tc_fence_after();
+    return ok;
+  }
+
+  // The products of the stage, `steps` of 16 k (e4m3: 32); begins, ends: of
+  // the sum in the accumulator.
+  __device__ __forceinline__ void block(bool begins, bool ends, int steps) {
+    const uint32_t d = tmem + as * kTileN;
+    const uint64_t da = da0 + (uint64_t)(st * (kStageBytes >> 4));
+    const uint64_t db = db0 + (uint64_t)(st * (kStageBytes >> 4));
+    if (steps == 4) {
+      tc_mma<CG, FP8, 2>(d, da, db, kA, kB, kIdesc, !begins);
+      tc_mma<CG, FP8, 2>(d, da + 2 * kA, db + 2 * kB, kA, kB, kIdesc, true);
+    } else {
+      for (int k = 0; k < steps; ++k)
+        tc_mma<CG, FP8, 1>(d, da + k * kA, db + k * kB, 0, 0, kIdesc, !begins || k > 0);
+    }
+    if (ends) {
+      tc_commit<CG>(tfull0 + as * 8);
+      as ^= 1;
+      if (as == 0) aph ^= 1;
+    }
+    tc_commit<CG>(empty0 + st * 8);
+    if (++st == kStages) {
+      st = 0;
+      ph ^= 1;
+    }
+  }
+};
+
+// FP8: two warps keep the scales of the next accumulators ready, so that the
+// epilogue warps never wait for memory: for each reduction block the 128 rows'
+// scale times those of the tile's two weight blocks. Thread j of 64 serves
+// rows j and j + 64 and loads four blocks ahead.
+template <int OP, int CG>
+__device__ __forceinline__ void scale_warp(const ExpertArgs& p, Shared& s, const WaitCtl& ctl,
+                                           Walk<OP, CG>& walk, int j) {
+  constexpr int kAhead = 4;
+  int as = 0;
+  uint32_t ph = 1;
+  Tile t;
+  while (walk.next(t)) {
+    // a row past the segment's end takes the scales of the segment's first
+    const float* a0 = p.sa + (long long)(j < t.rows ? t.row0 + j : s.off[t.e]) * t.kb;
+    const float* a1 = p.sa + (long long)(j + 64 < t.rows ? t.row0 + j + 64 : s.off[t.e]) * t.kb;
+    const int blocks = OP == kGated ? 2 * p.F >> 7 : p.N >> 7;
+    const int n0 = OP == kGated ? t.n0 : 2 * t.n0;
+    const int n1 = OP == kGated ? (p.F >> 7) + t.n0 : min(2 * t.n0 + 1, blocks - 1);
+    const float* b0 = p.sb + ((long long)t.e * blocks + n0) * t.kb;
+    const float* b1 = p.sb + ((long long)t.e * blocks + n1) * t.kb;
+    float next[4][kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int k = min(i, t.kb - 1);
+      next[0][i] = __ldg(a0 + k);
+      next[1][i] = __ldg(a1 + k);
+      next[2][i] = __ldg(b0 + k);
+      next[3][i] = __ldg(b1 + k);
+    }
+    for (int kb = 0; kb < t.kb; kb += kAhead) {
+      float now[4][kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int k = min(kb + kAhead + i, t.kb - 1);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) now[q][i] = next[q][i];
+        next[0][i] = __ldg(a0 + k);
+        next[1][i] = __ldg(a1 + k);
+        next[2][i] = __ldg(b0 + k);
+        next[3][i] = __ldg(b1 + k);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (kb + i >= t.kb) break;
+        if (!__all_sync(~0u, mbar_wait<CG == 2>(smem_u32(&s.sempty[as]), ph, ctl))) return;
+        s.scale[as][j] = make_float2(now[0][i] * now[2][i], now[0][i] * now[3][i]);
+        s.scale[as][j + 64] = make_float2(now[1][i] * now[2][i], now[1][i] * now[3][i]);
+        __syncwarp();
+        if ((j & 31) == 0) mbar_arrive(smem_u32(&s.tfull[as]));
+        as ^= 1;
+        if (as == 0) ph ^= 1;
+      }
+    }
+  }
+}
+
+// Two sums at a time (one issue slot for two fused multiply-adds).
+__device__ __forceinline__ void fma2(float2& acc, uint32_t lo, uint32_t hi, float s) {
+  acc = __ffma2_rn(make_float2(__uint_as_float(lo), __uint_as_float(hi)), make_float2(s, s), acc);
+}
+
+template <int OP, bool FP8, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
     k_expert_gemm(const __grid_constant__ CUtensorMap map_a,
                   const __grid_constant__ CUtensorMap map_b, const ExpertArgs p) {
   constexpr bool kAmn = OP == kDw;
   constexpr bool kBmn = OP == kDw || OP == kDgate || OP == kDx;
   constexpr int kElems = FP8 ? 128 : 64;  // reduction elements of one stage
-  constexpr uint32_t kIdesc = mma_desc(FP8, kAmn, kBmn, kTileM, kTileN);
+  constexpr int kStages = Ring<CG>::kStages, kStageBytes = Ring<CG>::kStageBytes;
+  constexpr bool kPair = CG == 2;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint4* epi = reinterpret_cast<uint4*>(smem + kStages * kStageBytes);
-  Shared& s = *reinterpret_cast<Shared*>(smem + kStages * kStageBytes + kEpiBytes);
+  uint4* epi = reinterpret_cast<uint4*>(smem + kRingBytes);
+  Shared& s = *reinterpret_cast<Shared*>(smem + kRingBytes + kEpiBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = kPair ? (int)(blockIdx.x & 1) : 0;  // clusters are pairs of neighbours
 
-  if (warp == 2) tc_alloc(smem_u32(&s.tmem), 512);
+  if (warp == 2) tc_alloc<CG>(smem_u32(&s.tmem), 512);
   if (threadIdx.x == 0) {
     s.abort = 0;
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_u32(&s.full[i]), 1);
+      mbar_init(smem_u32(&s.full[i]), CG);
       mbar_init(smem_u32(&s.empty[i]), 1);
+      mbar_init(smem_u32(&s.tail[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&s.tfull[i]), 1);
-      mbar_init(smem_u32(&s.tempty[i]), 8);
+      mbar_init(smem_u32(&s.tfull[i]), FP8 ? 3 : 1);  // the products, and two scale warps
+      mbar_init(smem_u32(&s.sempty[i]), 8);
+      mbar_init(smem_u32(&s.tempty[i]), 8 * CG);
     }
     for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&s.pair[i]), 2);
     mbar_init(smem_u32(&s.drain), 1);
@@ -379,130 +553,143 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_map(&map_b);
   }
   pdl_wait();  // the segments and the operands come from earlier kernels
-  load_segments(p, s);
+  load_segments<CG>(p, s);
   tc_fence_before();
-  __syncthreads();
+  if constexpr (kPair) cluster_sync();  // both CTAs' barriers exist
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s.tmem;
-  const WaitCtl ctl{&s.abort, p.wait_limit, p.status};
+  const WaitCtl ctl{&s.abort, kPair ? cluster_addr(smem_u32(&s.abort), rank ^ 1) : 0u, p.wait_limit,
+                    p.status};
+  Walk<OP, CG> walk(p, s, kElems, rank, blockIdx.x / CG, gridDim.x / CG);
 
   if (warp < kEpiWarp0) {
     give_registers<FP8>();
     if (warp == 0) {
-      if (lane == 0) {
-        int st = 0, issued = 0;
-        uint32_t ph = 0;
-        bool ok = true;
-        Tile t;
-        for (long long ti = blockIdx.x; ok && get_tile<OP>(ti, p, s, kElems, t); ti += gridDim.x) {
-          const int a_copies =
-              kAmn ? 0 : (min(t.rows, kTileM) + p.a_box - 1) / p.a_box;
-          const uint32_t bytes = kAmn ? kStageBytes : a_copies * p.a_box * 128 + kBBytes;
-          for (int kb = 0; kb < t.kb; ++kb) {
-            if (!mbar_wait(smem_u32(&s.empty[st]), ph ^ 1, ctl)) {
-              ok = false;
-              break;
-            }
-            const uint32_t bar = smem_u32(&s.full[st]);
-            const uint32_t a = smem_u32(smem + st * kStageBytes), b = a + kABytes;
-            mbar_expect(bar, bytes);
-            if constexpr (kAmn) {
-              for (int i = 0; i < 2; ++i)
-                tma_load_2d(a + i * 8192, &map_a, bar, t.m0 + i * 64, t.row0 + kb * 64);
-            } else {
-              for (int i = 0; i < a_copies; ++i)
-                tma_load_2d(a + i * p.a_box * 128, &map_a, bar, kb * kElems, t.row0 + i * p.a_box);
-            }
-            if constexpr (OP == kDw) {
-              for (int i = 0; i < 4; ++i)
-                tma_load_2d(b + i * 8192, &map_b, bar, t.n0 * kTileN + i * 64, t.row0 + kb * 64);
-            } else if constexpr (kBmn) {
-              for (int i = 0; i < 4; ++i)
-                tma_load_3d(b + i * 8192, &map_b, bar, t.n0 * kTileN + i * 64, kb * 64, t.e);
-            } else if constexpr (OP == kGated) {
-              tma_load_3d(b, &map_b, bar, kb * kElems, t.n0 * 128, t.e);
-              tma_load_3d(b + 16384, &map_b, bar, kb * kElems, p.F + t.n0 * 128, t.e);
-            } else {
-              tma_load_3d(b, &map_b, bar, kb * kElems, t.n0 * kTileN, t.e);
-              tma_load_3d(b + 16384, &map_b, bar, kb * kElems, t.n0 * kTileN + 128, t.e);
-            }
-            if (issued < kStages) ++issued;
-            if (++st == kStages) {
-              st = 0;
-              ph ^= 1;
-            }
-          }
-        }
-        // copies in flight land before the CTA ends, also when a wait gave up
-        for (int i = 0; i < issued; ++i) {
-          if (--st < 0) {
-            st = kStages - 1;
-            ph ^= 1;
-          }
-          mbar_drain(smem_u32(&s.full[st]), ph);
-        }
-      }
-      __syncwarp();
-    } else if (warp == 1) {
-      int st = 0, as = 0;
-      uint32_t ph = 0, aph = 0;
+      int st = 0, issued = 0;
+      uint32_t ph = 0;
       bool ok = true;
       Tile t;
-      for (long long ti = blockIdx.x; ok && get_tile<OP>(ti, p, s, kElems, t); ti += gridDim.x) {
-        if (t.kb == 0) continue;
-        for (int kb = 0; kb < t.kb; ++kb) {
-          if (FP8 || kb == 0) {
-            ok = mbar_wait(smem_u32(&s.tempty[as]), aph ^ 1, ctl);
-            tc_fence_after();
-          }
-          ok = ok && mbar_wait(smem_u32(&s.full[st]), ph, ctl);
-          ok = __all_sync(~0u, ok);
+      const uint32_t ring = smem_u32(smem);
+      const uint32_t full0 = smem_u32(s.full), empty0 = smem_u32(s.empty);
+      const uint32_t full0_first = kPair ? cluster_addr(full0, 0) : full0;
+      while (ok && walk.next(t)) {
+        // uniform, and known to be
+        const int blocks = __shfl_sync(~0u, t.kb, 0), e = __shfl_sync(~0u, t.e, 0);
+        const int row0 = __shfl_sync(~0u, t.row0, 0), rows = __shfl_sync(~0u, t.rows, 0);
+        const int m0 = __shfl_sync(~0u, t.m0, 0), n0 = __shfl_sync(~0u, t.n0, 0);
+        // copies cover at least the tile's rows (a pair's always 128)
+        const int a_copies = kAmn ? 0 : kPair ? 1 : (min(rows, kTileM) + p.a_box - 1) / p.a_box;
+        const uint32_t bytes =
+            kAmn || kPair ? kStageBytes : a_copies * p.a_box * 128 + kTileN * 128;
+        for (int kb = 0; kb < blocks; ++kb) {
+          ok = __all_sync(~0u, mbar_wait<kPair>(empty0 + st * 8, ph ^ 1, ctl));
           if (!ok) break;
-          const uint32_t a = smem_u32(smem + st * kStageBytes), b = a + kABytes;
-          int ksteps = 4;
-          if constexpr (OP == kDw) {
-            const int valid = t.rows - kb * 64;
-            if (valid < 64) {  // rows of the next segment: zero them in both operands
-              ksteps = (valid + 15) >> 4;
-              uint4* base = reinterpret_cast<uint4*>(smem + st * kStageBytes);
-              const int lines = ksteps * 16 - valid;
-              for (int i = lane; i < lines * 8 * 6; i += 32) {
-                const int chunk = i / (lines * 8), r = i - chunk * lines * 8;
-                base[chunk * 512 + valid * 8 + r] = make_uint4(0u, 0u, 0u, 0u);
-              }
-              fence_async_smem();
-              __syncwarp();
+          // a pair's copies all arrive at the first CTA's barrier, except
+          // those of a block that the second CTA has to clear rows of first
+          uint32_t bar = full0_first + st * 8;
+          const uint32_t a = ring + st * kStageBytes, b = a + kABytes;
+          if (kPair && OP == kDw && rank == 1 && rows - kb * 64 < 64) {
+            bar = smem_u32(&s.tail[st]);
+            mbar_expect_elected(bar, bytes);
+            bar = cluster_addr(bar, 1);
+          } else if constexpr (kPair) {
+            mbar_expect_relaxed_elected(bar, bytes);
+          } else {
+            mbar_expect_elected(bar, bytes);
+          }
+          if constexpr (kAmn) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              tma_load_2d<CG>(a + i * 8192, &map_a, bar, m0 + i * 64, row0 + kb * 64);
+          } else if constexpr (kPair) {
+            tma_load_2d<CG>(a, &map_a, bar, kb * kElems, row0);
+          } else {
+            for (int i = 0; i < a_copies; ++i)
+              tma_load_2d<CG>(a + i * p.a_box * 128, &map_a, bar, kb * kElems, row0 + i * p.a_box);
+          }
+          // B: 256 columns, or this CTA's 128 of them
+          if constexpr (kBmn) {
+#pragma unroll
+            for (int i = 0; i < 4 / CG; ++i) {
+              const int n = n0 * kTileN + rank * 128 + i * 64;
+              if constexpr (OP == kDw)
+                tma_load_2d<CG>(b + i * 8192, &map_b, bar, n, row0 + kb * 64);
+              else
+                tma_load_3d<CG>(b + i * 8192, &map_b, bar, n, kb * 64, e);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 2 / CG; ++i) {
+              const int half = i + rank;  // kGated: gate columns, then up columns
+              const int n = OP == kGated ? half * p.F + n0 * 128 : n0 * kTileN + half * 128;
+              tma_load_3d<CG>(b + i * 16384, &map_b, bar, kb * kElems, n, e);
             }
           }
-          tc_fence_after();
-          if (lane == 0) {
-            const uint32_t d = tmem + as * kTileN;
-            uint64_t da = kAmn ? smem_desc(a, 8192, 1024) : smem_desc(a, 16, 1024);
-            uint64_t db = kBmn ? smem_desc(b, 8192, 1024) : smem_desc(b, 16, 1024);
-            for (int k = 0; k < ksteps; ++k) {
-              tc_mma<FP8>(d, da, db, kIdesc, (FP8 ? 0 : kb) > 0 || k > 0);
-              // 16 k of bf16 (32 of e4m3): 32 bytes along K, or 16 lines of 128 bytes
-              da += (kAmn ? 2048 : 32) >> 4;
-              db += (kBmn ? 2048 : 32) >> 4;
-            }
-            tc_commit(smem_u32(&s.empty[st]));
-            if (FP8 || kb == t.kb - 1) tc_commit(smem_u32(&s.tfull[as]));
-          }
-          __syncwarp();
+          if (issued < kStages) ++issued;
           if (++st == kStages) {
             st = 0;
             ph ^= 1;
           }
-          if (FP8 || kb == t.kb - 1) {
-            as ^= 1;
-            if (as == 0) aph ^= 1;
-          }
         }
       }
-      if (lane == 0) {  // products in flight end before TMEM is freed
-        tc_commit(smem_u32(&s.drain));
-        mbar_drain(smem_u32(&s.drain), 0);
+      // copies in flight land before the CTA (the pair) ends, also when a wait
+      // gave up
+      for (int i = 0; i < (rank == 0 ? issued : 0); ++i) {
+        if (--st < 0) {
+          st = kStages - 1;
+          ph ^= 1;
+        }
+        mbar_drain(smem_u32(&s.full[st]), ph);
       }
+      __syncwarp();
+    } else if (kPair && warp == 1 && rank == 1) {
+      // The second CTA issues no products. In kDw it clears its rows past a
+      // segment's end and then arrives at the first CTA's barrier.
+      if constexpr (OP == kDw) {
+        int st = 0;
+        uint32_t phases = 0;  // bit i: parity of tail[i]'s next phase
+        bool ok = true;
+        Tile t;
+        while (ok && walk.next(t)) {
+          st = (st + t.kb) % kStages;
+          const int valid = t.rows & 63;
+          if (valid == 0) continue;
+          const int last = st == 0 ? kStages - 1 : st - 1;
+          ok = __all_sync(~0u,
+                          mbar_wait<kPair>(smem_u32(&s.tail[last]), (phases >> last) & 1, ctl));
+          if (!ok) break;
+          clear_rows<2 + 4 / CG>(smem + last * kStageBytes, valid, lane);
+          if (lane == 0) mbar_arrive_release(cluster_addr(smem_u32(&s.full[last]), 0));
+          phases ^= 1u << last;
+        }
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      Issuer<CG, FP8, kAmn, kBmn> io(s, smem, tmem, ctl);
+      bool ok = true;
+      Tile t;
+      while (ok && walk.next(t)) {
+        const int blocks = __shfl_sync(~0u, t.kb, 0);  // uniform, and known to be
+        const int tail = OP == kDw ? __shfl_sync(~0u, t.rows, 0) & 63 : 0;
+        for (int kb = 0; kb < blocks; ++kb) {
+          ok = io.wait(FP8 || kb == 0);
+          if (!ok) break;
+          int steps = 4;
+          if (OP == kDw && tail != 0 && kb == blocks - 1) {
+            // rows of the next segment follow: zero them in both operands
+            steps = (tail + 15) >> 4;
+            clear_rows<2 + 4 / CG>(smem + io.st * kStageBytes, tail, lane);
+          }
+          io.block(FP8 || kb == 0, FP8 || kb == blocks - 1, steps);
+        }
+      }
+      __syncwarp();
+      tc_commit<CG>(smem_u32(&s.drain));  // products in flight end before TMEM is freed
+      mbar_drain(smem_u32(&s.drain), 0);
+      __syncwarp();
+    } else if constexpr (FP8) {
+      scale_warp<OP, CG>(p, s, ctl, walk, (warp - 2) * 32 + lane);
       __syncwarp();
     }
   } else {
@@ -514,10 +701,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t aph = 0, parity = 0;
     bool ok = true;
     Tile t;
-    for (long long ti = blockIdx.x; ok && get_tile<OP>(ti, p, s, kElems, t); ti += gridDim.x) {
+    while (ok && walk.next(t)) {
       if constexpr (!FP8) {
         if (t.kb > 0) {
-          ok = __all_sync(~0u, mbar_wait(smem_u32(&s.tfull[as]), aph, ctl));
+          ok = __all_sync(~0u, mbar_wait<kPair>(smem_u32(&s.tfull[as]), aph, ctl));
           if (!ok) break;
           tc_fence_after();
         }
@@ -525,52 +712,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (t.kb > 0) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&s.tempty[as]));
+          if (lane == 0) release<CG>(s, as);
           as ^= 1;
           if (as == 0) aph ^= 1;
         }
       } else {
         // columns of this thread: kGated 64 of gate and the same 64 of up,
-        // kDown 128 in a row; two groups of 64, one weight block each
+        // kDown 128 in a row of one weight block
         const int r = quarter * 32 + lane;
         const bool mine = r < t.rows;
-        const float* sa = p.sa + ((long long)t.row0 + (mine ? r : 0)) * t.kb;
-        const int blocks = OP == kGated ? 2 * p.F >> 7 : p.N >> 7;
-        const int b0 = OP == kGated ? t.n0 : t.n0 * 2 + half;
-        const int b1 = OP == kGated ? (p.F >> 7) + t.n0 : b0;
-        const float* sb0 = p.sb + ((long long)t.e * blocks + min(b0, blocks - 1)) * t.kb;
-        const float* sb1 = p.sb + ((long long)t.e * blocks + min(b1, blocks - 1)) * t.kb;
         const uint32_t c0 = OP == kGated ? half * 64 : half * 128;
         const uint32_t c1 = OP == kGated ? 128 + half * 64 : half * 128 + 64;
-        uint64_t acc[64];
+        float2 acc[64];
 #pragma unroll
-        for (int i = 0; i < 64; ++i) acc[i] = 0ull;
-        float a_next = __ldg(sa), b0_next = __ldg(sb0), b1_next = __ldg(sb1);
+        for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.0f, 0.0f);
         for (int kb = 0; kb < t.kb; ++kb) {
-          const uint64_t s0 = both(a_next * b0_next), s1 = both(a_next * b1_next);
-          if (kb + 1 < t.kb) {
-            a_next = __ldg(sa + kb + 1);
-            b0_next = __ldg(sb0 + kb + 1);
-            b1_next = __ldg(sb1 + kb + 1);
-          }
-          ok = __all_sync(~0u, mbar_wait(smem_u32(&s.tfull[as]), aph, ctl));
+          ok = __all_sync(~0u, mbar_wait<kPair>(smem_u32(&s.tfull[as]), aph, ctl));
           if (!ok) break;
           tc_fence_after();
           const uint32_t ta = tmem + lanes + as * kTileN;
+          uint32_t v[2][32];
+          tc_ld32(v[0], ta + c0);
+          const float2 sc = s.scale[as][r];
+          const float s0 = OP == kGated || half == 0 ? sc.x : sc.y;
+          const float s1 = OP == kGated ? sc.y : s0;
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            uint32_t v[32];
-            tc_ld32(v, ta + (g < 2 ? c0 : c1) + (g & 1) * 32);
+          for (int g = 0; g < 4; ++g) {  // the next 32 columns load beside this sum
             tc_wait_ld();
-            tc_loaded(v);
-            if (g == 3) {  // all read: the accumulator may be overwritten
+            tc_loaded(v[g & 1]);
+            if (g < 3) {
+              tc_ld32(v[(g + 1) & 1], ta + (g < 1 ? c0 + 32 : g < 2 ? c1 : c1 + 32));
+            } else {  // all read: the accumulator and the scales may be overwritten
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive(smem_u32(&s.tempty[as]));
+              if (lane == 0) {
+                release<CG>(s, as);
+                mbar_arrive(smem_u32(&s.sempty[as]));
+              }
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              fma2(acc[g * 16 + i], v[2 * i], v[2 * i + 1], g < 2 ? s0 : s1);
+              fma2(acc[g * 16 + i], v[g & 1][2 * i], v[g & 1][2 * i + 1], g < 2 ? s0 : s1);
           }
           as ^= 1;
           if (as == 0) aph ^= 1;
@@ -585,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t o[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              o[i] = bf16x2(part(acc, g * 32 + 2 * i), part(acc, g * 32 + 2 * i + 1));
+              o[i] = bf16x2(acc[g * 16 + i].x, acc[g * 16 + i].y);
             put_store(buf, lane, o, static_cast<uint16_t*>(p.out) + row * p.N + c, p.N, rows,
                       p.N - c);
           }
@@ -595,14 +777,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           // and the one of the other half
           float h[64], m = 0.0f;
 #pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            h[i] = silu(part(acc, i)) * part(acc, 64 + i);
-            m = fmaxf(m, fabsf(h[i]));
+          for (int i = 0; i < 32; ++i) {
+            h[2 * i] = silu(acc[i].x) * acc[32 + i].x;
+            h[2 * i + 1] = silu(acc[i].y) * acc[32 + i].y;
+            m = fmaxf(m, fmaxf(fabsf(h[2 * i]), fabsf(h[2 * i + 1])));
           }
           s.amax[parity][half][r] = m;
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&s.pair[quarter]));
-          ok = __all_sync(~0u, mbar_wait(smem_u32(&s.pair[quarter]), parity, ctl));
+          ok = __all_sync(~0u, mbar_wait<kPair>(smem_u32(&s.pair[quarter]), parity, ctl));
           if (!ok) break;
           m = fmaxf(m, s.amax[parity][half ^ 1][r]);
           parity ^= 1;  // the other buffer next: this one is read until then
@@ -637,9 +820,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  if constexpr (kPair) cluster_sync();  // neither CTA's memory is used any more
+  else __syncthreads();
   tc_fence_after();
-  if (warp == 2) tc_dealloc(tmem, 512);
+  if (warp == 2) tc_dealloc<CG>(tmem, 512);
 }
 
 // ---- host side -------------------------------------------------------------
@@ -680,9 +864,10 @@ cudaError_t make_map(CUtensorMap* m, const void* base, bool fp8, long long cols,
   return rc == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int OP, bool FP8>
+template <int OP, bool FP8, int CG>
 cudaError_t launch(const ExpertArgs& p, const void* a, const void* b, int num_sms,
                    cudaStream_t st) {
+  constexpr int kRows = kTileM * CG;
   CUtensorMap ma, mb;
   cudaError_t e;
   if (OP == kDw) {
@@ -697,24 +882,66 @@ cudaError_t launch(const ExpertArgs& p, const void* a, const void* b, int num_sm
     }
   }
   if (e != cudaSuccess) return e;
-  // Row tiles are at most one per 128 rows plus one per segment.
+  // Row tiles are at most one per kRows rows plus one per segment.
   const long long segments = p.E < p.rows_max ? p.E : p.rows_max;
-  const long long tiles = OP == kDw ? (long long)((p.M + kTileM - 1) / kTileM) * p.nt * p.E
-                                    : (p.rows_max / kTileM + segments) * p.nt;
-  const int grid = (int)(tiles < num_sms ? tiles : num_sms);
-  return launch_pdl(k_expert_gemm<OP, FP8>, dim3(grid), dim3(kThreads), kSmemBytes, st, ma, mb, p);
+  const long long tiles = OP == kDw ? (long long)((p.M + kRows - 1) / kRows) * p.nt * p.E
+                                    : (p.rows_max / kRows + segments) * p.nt;
+  const long long most = num_sms / CG;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((tiles < most ? tiles : most) * CG));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CG == 2 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, k_expert_gemm<OP, FP8, CG>, ma, mb, p);
+}
+
+// Whether pairs of CTAs share 256-row tiles: each then writes and reads a
+// third less of its shared memory per product, but an expert's last tile
+// wastes up to 255 rows instead of 127. By average rows per expert (the host
+// knows no others). Measured at E = 32, H = 4096, F = 2048, bf16, us alone /
+// paired: kGated 192 / 192 at 128 rows, 221 / 194 at 192, 401 / 381 at 512,
+// 734 / 663 at 1024; kDgate 120 / 138 at 128, 163 / 160 at 256; kDx 175 / 179
+// at 128, 251 / 230 at 256; kDw, where the rows are the reduction axis and the
+// epilogue of a short sum weighs more, 480 / 498 at 512, 757 / 737 at 1024.
+// e4m3 (H = 7168) does not gain: 961 / 1158 at 512 rows, where an accumulator
+// is handed back and forth between the two CTAs for each 128 channels.
+bool use_pair(ExpertOp op, bool fp8, const ExpertArgs& p) {
+  if (fp8) return false;
+  return p.rows_max >= (op == kDw ? 768ll : 192ll) * p.E;
+}
+
+template <int OP, bool FP8>
+cudaError_t launch(bool pair, const ExpertArgs& p, const void* a, const void* b, int num_sms,
+                   cudaStream_t st) {
+  return pair ? launch<OP, FP8, 2>(p, a, b, num_sms, st) : launch<OP, FP8, 1>(p, a, b, num_sms, st);
+}
+
+template <int OP, bool FP8, int CG>
+cudaError_t prepare() {
+  const auto kernel = k_expert_gemm<OP, FP8, CG>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess || !FP8) return e;
+  // The register split (4 warps x 56, 8 warps x 224) spends exactly 12 x 168.
+  cudaFuncAttributes attr;
+  e = cudaFuncGetAttributes(&attr, kernel);
+  if (e != cudaSuccess) return e;
+  return attr.numRegs >= 168 ? cudaSuccess : cudaErrorInvalidConfiguration;
 }
 
 template <int OP, bool FP8>
 cudaError_t prepare() {
-  cudaError_t e = cudaFuncSetAttribute(k_expert_gemm<OP, FP8>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-  if (e != cudaSuccess || !FP8) return e;
-  // The register split (4 warps x 56, 8 warps x 224) spends exactly 12 x 168.
-  cudaFuncAttributes attr;
-  e = cudaFuncGetAttributes(&attr, k_expert_gemm<OP, FP8>);
-  if (e != cudaSuccess) return e;
-  return attr.numRegs >= 168 ? cudaSuccess : cudaErrorInvalidConfiguration;
+  const cudaError_t e = prepare<OP, FP8, 1>();
+  return e == cudaSuccess ? prepare<OP, FP8, 2>() : e;
 }
 
 }  // namespace
@@ -735,16 +962,17 @@ cudaError_t launch_expert_gemm(ExpertOp op, bool fp8, const ExpertArgs& args, co
   ExpertArgs p = args;
   p.a_box = 128;
   p.nt = op == kGated ? (p.F + 127) / 128 : (p.N + kTileN - 1) / kTileN;
+  const bool pair = use_pair(op, fp8, p);
   switch (op) {
     case kGated:
-      return fp8 ? launch<kGated, true>(p, a, b, num_sms, st)
-                 : launch<kGated, false>(p, a, b, num_sms, st);
+      return fp8 ? launch<kGated, true>(pair, p, a, b, num_sms, st)
+                 : launch<kGated, false>(pair, p, a, b, num_sms, st);
     case kDown:
-      return fp8 ? launch<kDown, true>(p, a, b, num_sms, st)
-                 : launch<kDown, false>(p, a, b, num_sms, st);
-    case kDgate: return launch<kDgate, false>(p, a, b, num_sms, st);
-    case kDx: return launch<kDx, false>(p, a, b, num_sms, st);
-    default: return launch<kDw, false>(p, a, b, num_sms, st);
+      return fp8 ? launch<kDown, true>(pair, p, a, b, num_sms, st)
+                 : launch<kDown, false>(pair, p, a, b, num_sms, st);
+    case kDgate: return launch<kDgate, false>(pair, p, a, b, num_sms, st);
+    case kDx: return launch<kDx, false>(pair, p, a, b, num_sms, st);
+    default: return launch<kDw, false>(pair, p, a, b, num_sms, st);
   }
 }
 

@@ -26,6 +26,18 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
                : "memory");
 }
 
+// "Elected" wrappers are called by a whole converged warp, with the same
+// arguments in every lane; one lane (always the same) executes them. Written
+// this way, and not inside a branch of one lane, the warp's loop keeps its
+// addresses and descriptors in uniform registers.
+__device__ __forceinline__ void mbar_expect_elected(uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(bytes)
+      : "memory");
+}
+
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -55,23 +67,63 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// What a wait needs to give up: the CTA's abort flag, the clock cycles a wait
-// may last, and the device status word.
+// Address of this CTA's shared-memory location in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Arrivals on a barrier of the cluster (an address from cluster_addr). The
+// relaxed forms order no memory: a release at cluster scope is a memory
+// barrier that waits for the thread's stores (measured: one per stage halved
+// the speed of the paired products). They serve where nothing is written for
+// the other side: announcing copies, and handing back an accumulator whose
+// loads tcgen05.wait::ld and tcgen05.fence have ordered.
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void mbar_expect_relaxed_elected(uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;\n\t}" ::"r"(
+          bar),
+      "r"(bytes)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_release(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+               : "memory");
+}
+
+// What a wait needs to give up: the CTA's abort flag (and its address in the
+// other CTA of a pair, or 0), the clock cycles a wait may last, and the device
+// status word.
 struct WaitCtl {
   volatile int* abort;
+  uint32_t peer_abort;
   long long limit;
   uint32_t* status;
 };
 
 // Waits for the phase of the given parity. False when the wait lasted longer
 // than the limit (then the status bit is set and every other wait of the CTA
-// gives up too) or another wait of the CTA gave up.
+// or the pair gives up too) or another wait gave up.
+template <bool PAIR>
 __device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, const WaitCtl& c) {
   const long long t0 = clock64();
   while (true) {
     if (*c.abort) return false;
     if (clock64() - t0 >= c.limit) {
       *c.abort = 1;
+      if constexpr (PAIR)
+        asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], %1;" ::"r"(c.peer_abort), "r"(1)
+                     : "memory");
       atomicOr(c.status, MOE_STATUS_TIMEOUT);
       return false;
     }
@@ -79,37 +131,46 @@ __device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, co
   }
 }
 
+template <bool PAIR>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const WaitCtl& c) {
   if (mbar_test(bar, parity)) return true;
-  return mbar_wait_slow(bar, parity, c);
+  return mbar_wait_slow<PAIR>(bar, parity, c);
 }
 
-// Waits up to about a second for copies or products in flight, abort flag or
-// not: the way out of a kernel whose waits gave up.
+// Waits for copies or products in flight, abort flag or not, for at most about
+// half a millisecond: the way out of a kernel, where they have landed unless a
+// wait gave up.
 __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
   const long long t0 = clock64();
   while (!mbar_try(bar, parity))
-    if (clock64() - t0 > (1ll << 31)) return;
+    if (clock64() - t0 > (1ll << 20)) return;
 }
 
 // ---- TMA ------------------------------------------------------------------
+// Elected copies of a tile. CG == 2: `bar` is an address in the cluster, in
+// either CTA of the pair.
+#define MOE_TMA(DIM, GROUP, COORDS, ...)                                                          \
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"                           \
+               "@q cp.async.bulk.tensor." DIM GROUP                                               \
+               ".shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, " COORDS     \
+               "], [%2];\n\t}" ::"r"(dst),                                                        \
+               "l"(m), "r"(bar), __VA_ARGS__                                                      \
+               : "memory")
+
+template <int CG>
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x,
                                             int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-      "l"(m), "r"(bar), "r"(x), "r"(y)
-      : "memory");
+  if constexpr (CG == 2) MOE_TMA("2d", ".cta_group::2", "{%3, %4}", "r"(x), "r"(y));
+  else MOE_TMA("2d", "", "{%3, %4}", "r"(x), "r"(y));
 }
 
+template <int CG>
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x,
                                             int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-      "l"(m), "r"(bar), "r"(x), "r"(y), "r"(z)
-      : "memory");
+  if constexpr (CG == 2) MOE_TMA("3d", ".cta_group::2", "{%3, %4, %5}", "r"(x), "r"(y), "r"(z));
+  else MOE_TMA("3d", "", "{%3, %4, %5}", "r"(x), "r"(y), "r"(z));
 }
+#undef MOE_TMA
 
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
@@ -129,44 +190,82 @@ __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
-// Whole warp. 512 columns: the CTA's shared memory keeps any second CTA of
-// these kernels off the SM, so the allocation never waits for one.
+// Whole warp; CG == 2: one warp of each CTA of the pair. 512 columns: the
+// CTA's shared memory keeps any second CTA of these kernels off the SM, so the
+// allocation never waits for one.
+template <int CG>
 __device__ __forceinline__ void tc_alloc(uint32_t smem_dst, uint32_t cols) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst),
-               "r"(cols)
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-}
-
-__device__ __forceinline__ void tc_dealloc(uint32_t tmem, uint32_t cols) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols));
-}
-
-// The barrier completes its pending arrival when every product this thread
-// has issued so far is done (with an implied fence::before_thread_sync).
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-      : "memory");
-}
-
-template <bool FP8>
-__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       bool accumulate) {
-  if constexpr (FP8) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
-        : "memory");
+  if constexpr (CG == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst),
+                 "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
   } else {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
-        : "memory");
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst),
+                 "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
 }
+
+template <int CG>
+__device__ __forceinline__ void tc_dealloc(uint32_t tmem, uint32_t cols) {
+  if constexpr (CG == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols));
+  else
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols));
+}
+
+// Elected. The barrier (CG == 2: the barriers at this offset in both CTAs)
+// gets an arrival when every product that the elected lane has issued so far
+// is done (with an implied fence::before_thread_sync).
+template <int CG>
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster."
+        "b64 [%0], %1;\n\t}" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            bar)
+        : "memory");
+}
+
+// Elected. N products (1 or 2) along the reduction axis, the second with both
+// descriptors advanced; `accumulate`: the first adds to the accumulator (a
+// second always does).
+#define MOE_TC_MMA(GROUP, KIND, SECOND)                                                            \
+  asm volatile("{\n\t.reg .pred p, t, q;\n\t.reg .b64 a, b;\n\t"                                  \
+               "elect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"                          \
+               "setp.eq.b32 t, 0, 0;\n\tadd.u64 a, %1, %5;\n\tadd.u64 b, %2, %6;\n\t"              \
+               "@q tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, p;\n\t"      \
+               SECOND "\n\t}" ::"r"(d),                                                            \
+               "l"(da), "l"(db), "r"(idesc), "r"((uint32_t)accumulate), "l"(step_a), "l"(step_b)   \
+               : "memory")
+#define MOE_TC_MMA_N(GROUP, KIND)                                                                  \
+  do {                                                                                             \
+    if constexpr (N == 2)                                                                          \
+      MOE_TC_MMA(GROUP, KIND, "@q tcgen05.mma.cta_group::" GROUP ".kind::" KIND                    \
+                              " [%0], a, b, %3, t;");                                              \
+    else                                                                                           \
+      MOE_TC_MMA(GROUP, KIND, "");                                                                 \
+  } while (0)
+
+template <int CG, bool FP8, int N>
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t da, uint64_t db, uint64_t step_a,
+                                       uint64_t step_b, uint32_t idesc, bool accumulate) {
+  if constexpr (CG == 2 && FP8) MOE_TC_MMA_N("2", "f8f6f4");
+  else if constexpr (CG == 2) MOE_TC_MMA_N("2", "f16");
+  else if constexpr (FP8) MOE_TC_MMA_N("1", "f8f6f4");
+  else MOE_TC_MMA_N("1", "f16");
+}
+#undef MOE_TC_MMA_N
+#undef MOE_TC_MMA
 
 // 32 consecutive columns of this warp's 32 lanes: v[i] = column i of the
 // thread's lane. Asynchronous until tc_wait_ld.

@@ -40,6 +40,16 @@ FP8_CASES = {
 }
 
 
+# Rows of the buffers past the segments, in multiples of 1 and of the experts:
+# none, a few, and many per expert (the row count that a configuration allows
+# chooses between the products' forms)
+SPARE = {"exact": (0, 0), "spare": (37, 0), "roomy": (37, 1024)}
+
+
+def with_spare(n, counts, spare):
+    return max(1, n + SPARE[spare][0] + SPARE[spare][1] * len(counts))
+
+
 def offsets(counts):
     c = torch.tensor([0] + list(counts), device="cuda").cumsum(0)
     return c.to(torch.int32)
@@ -77,12 +87,12 @@ def untouched(t):
 
 
 @pytest.mark.parametrize("keep", [False, True])
-@pytest.mark.parametrize("spare", [0, 37])
+@pytest.mark.parametrize("spare", SPARE)
 @pytest.mark.parametrize("case", list(BF16_CASES))
 def test_gated_bf16(gpu, case, spare, keep):
     counts, H, F = BF16_CASES[case]
     E, n = len(counts), sum(counts)
-    rows = max(1, n + spare)
+    rows = with_spare(n, counts, spare)
     x, w13 = normal(rows, H), normal(E, 2 * F, H, std=H ** -0.5, seed=1)
     x[n:] = float("nan")  # rows outside every segment
     hid, gu = poisoned(rows, F), poisoned(rows, 2 * F) if keep else None
@@ -98,12 +108,12 @@ def test_gated_bf16(gpu, case, spare, keep):
         assert untouched(gu[n:])
 
 
-@pytest.mark.parametrize("spare", [0, 37])
+@pytest.mark.parametrize("spare", SPARE)
 @pytest.mark.parametrize("case", list(FP8_CASES))
 def test_gated_fp8(gpu, case, spare):
     counts, H, F = FP8_CASES[case]
     E, n = len(counts), sum(counts)
-    rows = max(1, n + spare)
+    rows = with_spare(n, counts, spare)
     x, xs = quant_rows(normal(rows, H))
     x[n:], xs[n:] = 0x7F, float("nan")
     w13, ws = quant_weights(normal(E, 2 * F, H, std=H ** -0.5, seed=1))
@@ -122,12 +132,12 @@ def test_gated_fp8(gpu, case, spare):
     assert untouched(hid[n:]) and untouched(hs[n:])
 
 
-@pytest.mark.parametrize("spare", [0, 37])
+@pytest.mark.parametrize("spare", SPARE)
 @pytest.mark.parametrize("case", list(BF16_CASES))
 def test_down_bf16(gpu, case, spare):
     counts, H, F = BF16_CASES[case]
     E, n = len(counts), sum(counts)
-    rows = max(1, n + spare)
+    rows = with_spare(n, counts, spare)
     hid, w2 = normal(rows, F), normal(E, H, F, std=F ** -0.5, seed=1)
     hid[n:] = float("nan")
     y = poisoned(rows, H)
@@ -138,12 +148,12 @@ def test_down_bf16(gpu, case, spare):
     assert untouched(y[n:])
 
 
-@pytest.mark.parametrize("spare", [0, 37])
+@pytest.mark.parametrize("spare", SPARE)
 @pytest.mark.parametrize("case", list(FP8_CASES))
 def test_down_fp8(gpu, case, spare):
     counts, H, F = FP8_CASES[case]
     E, n = len(counts), sum(counts)
-    rows = max(1, n + spare)
+    rows = with_spare(n, counts, spare)
     hid, hs = quant_rows(normal(rows, F))
     hid[n:], hs[n:] = 0x7F, float("nan")
     w2, ws = quant_weights(normal(E, H, F, std=F ** -0.5, seed=1))
@@ -163,12 +173,12 @@ def backward_inputs(counts, H, F, rows):
                 w2=normal(E, H, F, std=F ** -0.5, seed=5))
 
 
-@pytest.mark.parametrize("spare", [0, 37])
+@pytest.mark.parametrize("spare", SPARE)
 @pytest.mark.parametrize("case", list(BF16_CASES))
 def test_backward(gpu, case, spare):
     counts, H, F = BF16_CASES[case]
     E, n = len(counts), sum(counts)
-    rows = max(1, n + spare)
+    rows = with_spare(n, counts, spare)
     t = backward_inputs(counts, H, F, rows)
     for name in ("x", "gu", "hid", "dy"):
         t[name][n:] = float("nan")
