@@ -91,6 +91,8 @@ def library_path() -> str:
 def load_library():
     """Loads the built library; raises if it is missing (no fallback)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -199,12 +201,28 @@ def _ptr(t) -> Optional[int]:
 
 
 def _stream(stream) -> Optional[int]:
-    import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+_raw_stream = None
+
+
+def _current_stream() -> int:
+    """The current device's current stream, without a Stream object where torch can give its
+    handle alone (3 us less a call)."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        dev = getattr(torch._C, "_cuda_getDevice", None)
+        torch.cuda.current_stream()  # initialises CUDA, or raises
+        _raw_stream = ((lambda: get(dev())) if get and dev else
+                       (lambda: torch.cuda.current_stream().cuda_stream))
+    return _raw_stream()
 
 
 def make_config(P: int, Tr: int, E: int, k: int, H: int, dispatch_dtype: int = MOE_BF16,
@@ -425,6 +443,10 @@ class ExpertHandle:
         self.cfg = cfg
         self.workspace = workspace
         self.fp8 = cfg.dtype == MOE_FP8_E4M3
+        E, H, F, R = cfg.num_experts, cfg.hidden, cfg.inter, cfg.rows_max
+        #: elements that each tensor must hold, and the bytes of one of them
+        self.offsets, self.rows_h, self.rows_f = E + 1, R * H, R * F
+        self.w13, self.w2, self.elt = E * 2 * F * H, E * H * F, 1 if self.fp8 else 2
         h = _c_void_p()
         _check("moe_expert_create", load_library().moe_expert_create(
             ctypes.byref(cfg), _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -467,40 +489,36 @@ def _scale(name: str, x: ExpertHandle, t, count: int) -> Optional[int]:
 def moe_expert_gated(x: ExpertHandle, expert_offset, inp, inp_scale, w13, w13_scale, hid,
                      hid_scale=None, gate_up=None, stream=None) -> None:
     """hid = silu(inp Wg^T) * (inp Wu^T) over the experts' segments (see the header)."""
-    c, elt = x.cfg, 1 if x.fp8 else 2
-    E, H, F, R = c.num_experts, c.hidden, c.inter, c.rows_max
+    elt = x.elt
     _check("moe_expert_gated", load_library().moe_expert_gated(
-        x.ptr, _buf("expert_offset", expert_offset, E + 1, 4), _buf("inp", inp, R * H, elt),
-        _scale("inp_scale", x, inp_scale, R * H), _buf("w13", w13, E * 2 * F * H, elt),
-        _scale("w13_scale", x, w13_scale, E * 2 * F * H // 128), _buf("hid", hid, R * F, elt),
-        _scale("hid_scale", x, hid_scale, R * F),
-        _buf("gate_up", gate_up, R * 2 * F, 2, optional=True), _stream(stream)))
+        x.ptr, _buf("expert_offset", expert_offset, x.offsets, 4),
+        _buf("inp", inp, x.rows_h, elt), _scale("inp_scale", x, inp_scale, x.rows_h),
+        _buf("w13", w13, x.w13, elt), _scale("w13_scale", x, w13_scale, x.w13 // 128),
+        _buf("hid", hid, x.rows_f, elt), _scale("hid_scale", x, hid_scale, x.rows_f),
+        _buf("gate_up", gate_up, 2 * x.rows_f, 2, optional=True), _stream(stream)))
 
 
 def moe_expert_down(x: ExpertHandle, expert_offset, hid, hid_scale, w2, w2_scale, y,
                     stream=None) -> None:
     """y = hid W2^T over the experts' segments (see the header)."""
-    c, elt = x.cfg, 1 if x.fp8 else 2
-    E, H, F, R = c.num_experts, c.hidden, c.inter, c.rows_max
+    elt = x.elt
     _check("moe_expert_down", load_library().moe_expert_down(
-        x.ptr, _buf("expert_offset", expert_offset, E + 1, 4), _buf("hid", hid, R * F, elt),
-        _scale("hid_scale", x, hid_scale, R * F), _buf("w2", w2, E * H * F, elt),
-        _scale("w2_scale", x, w2_scale, E * H * F // 128), _buf("y", y, R * H, 2),
-        _stream(stream)))
+        x.ptr, _buf("expert_offset", expert_offset, x.offsets, 4),
+        _buf("hid", hid, x.rows_f, elt), _scale("hid_scale", x, hid_scale, x.rows_f),
+        _buf("w2", w2, x.w2, elt), _scale("w2_scale", x, w2_scale, x.w2 // 128),
+        _buf("y", y, x.rows_h, 2), _stream(stream)))
 
 
 def moe_expert_backward(x: ExpertHandle, expert_offset, inp, gate_up, hid, dy, w13, w2, dx=None,
                         dw13=None, dw2=None, stream=None) -> None:
     """Gradients of the gated block; dx, or dw13 and dw2 together, may be left out."""
-    c = x.cfg
-    E, H, F, R = c.num_experts, c.hidden, c.inter, c.rows_max
     _check("moe_expert_backward", load_library().moe_expert_backward(
-        x.ptr, _buf("expert_offset", expert_offset, E + 1, 4), _buf("inp", inp, R * H, 2),
-        _buf("gate_up", gate_up, R * 2 * F, 2), _buf("hid", hid, R * F, 2),
-        _buf("dy", dy, R * H, 2), _buf("w13", w13, E * 2 * F * H, 2),
-        _buf("w2", w2, E * H * F, 2), _buf("dx", dx, R * H, 2, optional=True),
-        _buf("dw13", dw13, E * 2 * F * H, 2, optional=True),
-        _buf("dw2", dw2, E * H * F, 2, optional=True), _stream(stream)))
+        x.ptr, _buf("expert_offset", expert_offset, x.offsets, 4),
+        _buf("inp", inp, x.rows_h, 2), _buf("gate_up", gate_up, 2 * x.rows_f, 2),
+        _buf("hid", hid, x.rows_f, 2), _buf("dy", dy, x.rows_h, 2), _buf("w13", w13, x.w13, 2),
+        _buf("w2", w2, x.w2, 2), _buf("dx", dx, x.rows_h, 2, optional=True),
+        _buf("dw13", dw13, x.w13, 2, optional=True), _buf("dw2", dw2, x.w2, 2, optional=True),
+        _stream(stream)))
 
 
 def moe_expert_set_wait_limit(x: ExpertHandle, cycles: int) -> None:

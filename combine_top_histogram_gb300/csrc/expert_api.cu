@@ -55,6 +55,29 @@ moe::ExpertArgs expert_args(moe_expert_t x, const int32_t* offset) {
   return a;
 }
 
+// Whether the few-rows kernels run: they stream each expert's weights once for
+// every eight rows it has. By the rows a call can have and their average per
+// expert. Measured (us, tiles / few rows; top-8 of E = 256, H = 7168, F = 2048):
+// gated bf16 110 / 86 at 8 rows, 545 / 529 at 64, 1414 / 1381 at 256, 2169 /
+// 2546 at 1536; gated e4m3 307 / 289 at 64; down bf16 71 / 50 at 8, 277 / 261
+// at 64; down e4m3, with little to read per row of weights, 47 / 37 at 8,
+// 113 / 92 at 32, 154 / 166 at 64. E = 8, H = 4096, F = 1408, gated bf16:
+// 48 / 42 at 32, 49 / 61 at 128. Above 64 rows the gain is a few per cent and
+// one expert with all of them would cost many passes.
+bool use_rows(moe_expert_t x, moe::ExpertOp op) {
+  const long long E3 = 3ll * x->cfg.num_experts, rows = x->cfg.rows_max;
+  const bool fp8_down = op == moe::kDown && x->cfg.dtype == MOE_FP8_E4M3;
+  return rows <= (E3 > 8 ? E3 : 8) && rows <= (fp8_down ? 48 : 64);
+}
+
+cudaError_t forward(moe_expert_t x, moe::ExpertOp op, const moe::ExpertArgs& a, const void* in,
+                    const void* w, void* stream) {
+  const bool fp8 = x->cfg.dtype == MOE_FP8_E4M3;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return use_rows(x, op) ? moe::launch_expert_rows(op, fp8, a, in, w, x->num_sms, st)
+                     : moe::launch_expert_gemm(op, fp8, a, in, w, x->num_sms, st);
+}
+
 }  // namespace
 
 extern "C" {
@@ -113,8 +136,7 @@ int moe_expert_gated(moe_expert_t x, const int32_t* expert_offset, const void* i
   a.out = hid;
   a.out_scale = hid_scale;
   a.gu_out = static_cast<uint16_t*>(gate_up);
-  return cuda_rc(moe::launch_expert_gemm(moe::kGated, fp8, a, in, w13, x->num_sms,
-                                         static_cast<cudaStream_t>(stream)));
+  return cuda_rc(forward(x, moe::kGated, a, in, w13, stream));
 }
 
 int moe_expert_down(moe_expert_t x, const int32_t* expert_offset, const void* hid,
@@ -130,8 +152,7 @@ int moe_expert_down(moe_expert_t x, const int32_t* expert_offset, const void* hi
   a.sa = hid_scale;
   a.sb = w2_scale;
   a.out = y;
-  return cuda_rc(moe::launch_expert_gemm(moe::kDown, fp8, a, hid, w2, x->num_sms,
-                                         static_cast<cudaStream_t>(stream)));
+  return cuda_rc(forward(x, moe::kDown, a, hid, w2, stream));
 }
 
 int moe_expert_backward(moe_expert_t x, const int32_t* expert_offset, const void* in,

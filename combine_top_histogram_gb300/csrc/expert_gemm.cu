@@ -33,6 +33,7 @@
 #include <stdint.h>
 
 #include "expert_internal.cuh"
+#include "expert_math.cuh"
 #include "expert_ptx.cuh"
 #include "internal.cuh"
 
@@ -205,12 +206,6 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 }
 __device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
-
-// 1 / (1 + exp(-g)); exp(-g) = +inf gives 0.
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
-// g / (1 + exp(-g)). __fdividef returns 0 for divisors above 2^126 (there the
-// quotient is below every value that a product with it could show).
-__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
 
 // ---- row-coalesced access of a warp's 32 x 32 bf16 tile --------------------
 // Each lane holds one row; the tile goes through 2 KB of shared memory

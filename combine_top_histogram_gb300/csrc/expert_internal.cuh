@@ -43,6 +43,9 @@ struct ExpertArgs {
 // `b` weights (kDw: rows [rows_max, N]).
 cudaError_t launch_expert_gemm(ExpertOp op, bool fp8, const ExpertArgs& args, const void* a,
                                const void* b, int num_sms, cudaStream_t st);
+// kGated or kDown for a few rows (expert_rows.cu).
+cudaError_t launch_expert_rows(ExpertOp op, bool fp8, const ExpertArgs& args, const void* a,
+                               const void* b, int num_sms, cudaStream_t st);
 // Opts the kernels in to their shared memory and checks their register split.
 cudaError_t expert_gemm_prepare();
 
