@@ -3,7 +3,9 @@
 The path -- route -> count -> permute/pack -> all-to-all-v dispatch ->
 (expert) -> combine -> unpermute with the top-k weighted sum -- runs in the
 hand-written sm_103a kernels of ``libmoe_ep.so`` (sources in ``csrc/``, C ABI
-in ``include/moe_ep.h``). This package holds the ctypes binding
+in ``include/moe_ep.h``), and so do the experts between dispatch and combine (a
+gated feed-forward block in bf16 or block-scaled e4m3) and the gradients of
+the experts and the combine. This package holds the ctypes binding
 (``binding``), a buffer-owning convenience layer (``layer``), the seeded
 input generators (``workloads``) and byte accounting (``accounting``).
 Importing the package does not load the library; the first binding call does,
@@ -19,4 +21,4 @@ from .binding import (  # noqa: F401
     moe_handle_create, moe_read_status, moe_recv_rows_max, moe_route_dispatch_layout,
     moe_route_topk, moe_workspace_bytes)
 from .build import build  # noqa: F401
-from .layer import MoeLayer  # noqa: F401
+from .layer import ExpertBlock, MoeLayer  # noqa: F401

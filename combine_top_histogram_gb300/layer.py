@@ -4,11 +4,71 @@
 and output buffers sized by the library's worst-case rule, then runs the path
 through the binding: route+layout (or layout from given ids) -> dispatch ->
 expert stand-in -> combine. Convenience for tests, the benchmark and smoke
-checks; every step runs in the library's kernels.
+checks; every step runs in the library's kernels. With ``set_experts`` the
+stand-in is replaced by gated feed-forward experts (``ExpertBlock``), and a
+layer built for training has a ``backward``.
 """
 from __future__ import annotations
 
 from . import binding as B
+
+
+class ExpertBlock:
+    """The experts of one layer: their weights, the handle, and the buffers
+    between the two products (and, for training, what the backward pass needs).
+
+    w13 [E, 2F, H] (the F gate rows, then the F up rows) and w2 [E, H, F]: bf16,
+    or e4m3 codes (uint8) with fp32 scales for each 128 x 128 block.
+    """
+
+    def __init__(self, w13, w2, rows: int, w13_scale=None, w2_scale=None, train: bool = False):
+        import torch
+        self.E, F2, self.H = w13.shape
+        self.F = F2 // 2
+        if tuple(w2.shape) != (self.E, self.H, self.F) or F2 % 2:
+            raise ValueError(f"w13 {tuple(w13.shape)} and w2 {tuple(w2.shape)} do not belong "
+                             "together: expected [E, 2F, H] and [E, H, F]")
+        self.fp8 = w13.element_size() == 1
+        if self.fp8 and (w13_scale is None or w2_scale is None):
+            raise ValueError("e4m3 weights need their scales")
+        self.w13, self.w2, self.w13_scale, self.w2_scale = w13, w2, w13_scale, w2_scale
+        self.rows, self.train = rows, train
+        self.handle = B.moe_expert_create(B.make_expert_config(
+            self.E, self.H, self.F, rows, B.MOE_FP8_E4M3 if self.fp8 else B.MOE_BF16, train),
+            device=w13.device)
+        bf = dict(dtype=torch.bfloat16, device=w13.device)
+        if self.fp8:
+            self.hid = torch.empty((rows, self.F), dtype=torch.uint8, device=w13.device)
+            self.hid_scale = torch.empty((rows, self.F // 128), dtype=torch.float32,
+                                         device=w13.device)
+        else:
+            self.hid, self.hid_scale = torch.empty((rows, self.F), **bf), None
+        self.gate_up = torch.empty((rows, 2 * self.F), **bf) if train else None
+        self.dw13 = torch.empty_like(w13) if train else None
+        self.dw2 = torch.empty_like(w2) if train else None
+
+    def forward(self, expert_offset, x, x_scale, y, stream=None):
+        """y = (silu(x Wg^T) * (x Wu^T)) W2^T over the experts' segments."""
+        B.moe_expert_gated(self.handle, expert_offset, x, x_scale, self.w13, self.w13_scale,
+                           self.hid, self.hid_scale, self.gate_up, stream)
+        B.moe_expert_down(self.handle, expert_offset, self.hid, self.hid_scale, self.w2,
+                          self.w2_scale, y, stream)
+        return y
+
+    def backward(self, expert_offset, x, dy, dx, stream=None):
+        """dx from dy; the weights' gradients land in self.dw13 and self.dw2. After the
+        forward of the same rows."""
+        if not self.train:
+            raise ValueError("the experts were not built for training")
+        B.moe_expert_backward(self.handle, expert_offset, x, self.gate_up, self.hid, dy, self.w13,
+                              self.w2, dx, self.dw13, self.dw2, stream)
+        return dx
+
+    def status(self, stream=None) -> int:
+        return B.moe_expert_read_status(self.handle, stream)
+
+    def close(self):
+        self.handle.close()
 
 
 class MoeLayer:
@@ -42,6 +102,20 @@ class MoeLayer:
         self.w = torch.empty((T, k), dtype=torch.float32, device=dev)
         self.slots = None  # fixed-slot buffers, allocated on first use
         self.fixed = False  # the last dispatch wrote the fixed-slot layout
+        self.experts = None  # an ExpertBlock in the stand-in's place
+        self.grads = None    # backward's buffers, allocated on first use
+
+    def set_experts(self, w13, w2, w13_scale=None, w2_scale=None, train: bool = False):
+        """Gated feed-forward experts in the stand-in's place (None: the stand-in again).
+        Their type is the dispatch's: bf16, or e4m3 codes with 128 x 128 block scales."""
+        if w13 is None:
+            self.experts = None
+            return None
+        experts = ExpertBlock(w13, w2, self.rows, w13_scale, w2_scale, train)
+        if (experts.E, experts.H, experts.fp8) != (self.E, self.H, self.fp8):
+            raise ValueError("the experts' number, width and type are those of the layer")
+        self.experts = experts
+        return experts
 
     # -- steps ---------------------------------------------------------------
     def route_layout(self, logits, stream=None):
@@ -119,6 +193,13 @@ class MoeLayer:
         self.fixed = False
 
     def expert(self, expert_scale=None, stream=None):
+        """The experts of set_experts on the receive rows, or the stand-in."""
+        if self.experts is not None:
+            if self.fixed:
+                raise ValueError("experts run over the compact receive rows, not fixed slots")
+            self.experts.forward(self.layout_view()["expert_offset"], self.recv_x,
+                                 self.recv_scale, self.y, stream)
+            return
         if self.fixed:
             s = self.slots
             B.moe_expert_standin(self.handle, s["x"], s["scale"], expert_scale, s["y"], stream)
@@ -128,6 +209,27 @@ class MoeLayer:
 
     def combine(self, w, stream=None):
         B.moe_combine(self.handle, self.slots["y"] if self.fixed else self.y, w, self.out, stream)
+
+    def backward(self, dout, w, stream=None) -> dict:
+        """Gradients of the last forward (set_experts with train=True, bf16 dispatch) from
+        dout [T, H], with the w [T, k] it combined with: dx [T, H], dw [T, k], and the
+        experts' dw13 and dw2. Combine backward, the experts' backward, and the dispatch's:
+        the gradients of a token's k rows added up, which is a combine with unit weights."""
+        import torch
+        if self.experts is None or not self.experts.train:
+            raise ValueError("backward needs experts built for training (set_experts)")
+        if self.grads is None:
+            dev = self.out.device
+            self.grads = {"dy": torch.empty_like(self.y), "dx_rows": torch.empty_like(self.recv_x),
+                          "dw": torch.empty((self.T, self.k), dtype=torch.float32, device=dev),
+                          "dx": torch.empty_like(self.out),
+                          "ones": torch.ones((self.T, self.k), dtype=torch.float32, device=dev)}
+        g = self.grads
+        B.moe_combine_backward(self.handle, dout, self.y, w, g["dy"], g["dw"], stream)
+        self.experts.backward(self.layout_view()["expert_offset"], self.recv_x, g["dy"],
+                              g["dx_rows"], stream)
+        B.moe_combine(self.handle, g["dx_rows"], g["ones"], g["dx"], stream)
+        return {"dx": g["dx"], "dw": g["dw"], "dw13": self.experts.dw13, "dw2": self.experts.dw2}
 
     def forward(self, x, ids=None, w=None, logits=None, expert_scale=None, stream=None,
                 two_stage=False, fused=False, allgather=False, fixed_slots=False):
@@ -161,8 +263,11 @@ class MoeLayer:
                           stream=None):
         """The layer in token chunks on two streams: after the layout, chunk c+1's
         dispatch (main stream) overlaps chunk c's expert and combine (side
-        stream, ordered after chunk c's dispatch by an event)."""
+        stream, ordered after chunk c's dispatch by an event). With the stand-in only: a
+        chunk's rows are spread over every expert's segment."""
         import torch
+        if self.experts is not None:
+            raise ValueError("the chunked pipeline runs the stand-in, not experts")
         main = stream if stream is not None else torch.cuda.current_stream()
         if getattr(self, "_side", None) is None:
             self._side = torch.cuda.Stream(device=self.out.device)
