@@ -207,6 +207,24 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 __device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3) |
+         (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3) << 16;
+}
+
+// 32 bytes to memory that is 16-byte aligned at least.
+__device__ __forceinline__ void store32(void* to, const uint32_t (&v)[8]) {
+  if ((reinterpret_cast<uintptr_t>(to) & 31) == 0) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    uint4* q = static_cast<uint4*>(to);
+    q[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    q[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
 // ---- row-coalesced access of a warp's 32 x 32 bf16 tile --------------------
 // Each lane holds one row; the tile goes through 2 KB of shared memory
 // (16-byte units, swizzled by row so that neither side has bank conflicts) so
@@ -753,18 +771,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (as == 0) aph ^= 1;
         }
         if (!ok) break;
-        const int wrow = quarter * 32, rows = t.rows - wrow;
-        const long long row = (long long)t.row0 + wrow;
+        const long long row = (long long)t.row0 + quarter * 32;
         if constexpr (OP == kDown) {
+          // straight to memory, 32 bytes of a row at a time (a whole sector):
+          // these stores keep the sums' registers, and with them the products,
+          // waiting, so they are few (through shared memory as above a tile
+          // took about 6000 cycles more than its products)
+          uint16_t* out = static_cast<uint16_t*>(p.out) + (row + lane) * p.N + t.n0 * kTileN +
+                          half * 128;
+          const int cols = p.N - t.n0 * kTileN - half * 128;
+          if (mine && cols > 0) {
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const int c = t.n0 * kTileN + half * 128 + g * 32;
-            uint32_t o[16];
+            for (int g = 0; g < 8; ++g) {
+              uint32_t o[8];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              o[i] = bf16x2(acc[g * 16 + i].x, acc[g * 16 + i].y);
-            put_store(buf, lane, o, static_cast<uint16_t*>(p.out) + row * p.N + c, p.N, rows,
-                      p.N - c);
+              for (int i = 0; i < 8; ++i) o[i] = bf16x2(acc[g * 8 + i].x, acc[g * 8 + i].y);
+              store32(out + g * 16, o);
+            }
           }
         } else {
           // h = silu(g) u, then e4m3 codes with one scale for the tile's 128
@@ -785,30 +808,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = fmaxf(m, s.amax[parity][half ^ 1][r]);
           parity ^= 1;  // the other buffer next: this one is read until then
           const float scale = __fdiv_rn(m, 448.0f);
-          if (mine && half == 0) p.out_scale[((long long)t.row0 + r) * (p.F >> 7) + t.n0] = scale;
+          if (mine) {
+            if (half == 0) p.out_scale[((long long)t.row0 + r) * (p.F >> 7) + t.n0] = scale;
+            uint8_t* out =
+                static_cast<uint8_t*>(p.out) + (row + lane) * p.F + t.n0 * 128 + half * 64;
+            // h / s by the reciprocal: within 2^-23, as h itself
+            const float inv = __frcp_rn(scale);
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            uint32_t q[4];
+            for (int u = 0; u < 2; ++u) {
+              uint32_t q[8];
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const float* f = h + 16 * u + 4 * w;
-              uint32_t codes = 0;
-#pragma unroll
-              for (int b = 0; b < 2; ++b) {
-                const float x0 = scale > 0.0f ? __fdiv_rn(f[2 * b], scale) : 0.0f;
-                const float x1 = scale > 0.0f ? __fdiv_rn(f[2 * b + 1], scale) : 0.0f;
-                codes |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE,
-                                                            __NV_E4M3)
-                         << (16 * b);
+              for (int w = 0; w < 8; ++w) {
+                const float* f = h + 32 * u + 4 * w;
+                if (scale >= 1e-30f) {
+                  q[w] = e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+                } else if (scale > 0.0f) {  // the reciprocal may overflow
+                  q[w] = e4m3x4(__fdiv_rn(f[0], scale), __fdiv_rn(f[1], scale),
+                                __fdiv_rn(f[2], scale), __fdiv_rn(f[3], scale));
+                } else {
+                  q[w] = 0u;
+                }
               }
-              q[w] = codes;
+              store32(out + u * 32, q);
             }
-            buf[unit_at(lane, u)] = make_uint4(q[0], q[1], q[2], q[3]);
           }
-          __syncwarp();
-          tile_store(buf, lane,
-                     static_cast<uint8_t*>(p.out) + row * p.F + t.n0 * 128 + half * 64, p.F, rows, 4);
-          __syncwarp();
         }
       }
     }

@@ -5,11 +5,17 @@
 
 namespace moe {
 
-// 1 / (1 + exp(-g)); exp(-g) = +inf gives 0.
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+// 1 / (1 + exp(-g)) as 1 / (1 + 2^(-g log2 e)) with the hardware's approximate
+// 2^x and reciprocal, each within 2^-22 of the value; the rounded argument adds
+// up to |g| 2^-24. 2^x = +inf (g below -88) gives 0, where the true value is
+// below 2^-127.
+__device__ __forceinline__ float sigmoid(float g) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return r;
+}
 
-// g / (1 + exp(-g)). __fdividef returns 0 for divisors above 2^126 (there the
-// quotient is below every value that a product with it could show).
-__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+__device__ __forceinline__ float silu(float g) { return g * sigmoid(g); }
 
 }  // namespace moe
