@@ -45,17 +45,21 @@ constexpr int kTileN = 256;
 constexpr int kThreads = 384;          // copy, product, TMEM, spare; 8 epilogue warps
 constexpr int kEpiWarp0 = 4;
 constexpr int kABytes = kTileM * 128;  // a stage holds 128 bytes of K (or 64 k) per row
-template <int CG>
-struct Ring {
+// Shared memory of a kernel: the ring of stages, and what the epilogue warps
+// pass their results through: 32 rows x 64 bytes per warp, or (kOut) the
+// warp's whole 32 x 128 bf16 results, which the copy engine then writes beside
+// the next tile's products; those take the room of a stage or two.
+template <int OP, bool FP8, int CG>
+struct Plan {
   static constexpr int kBRows = kTileN / CG;  // rows (or columns) of B in one CTA
   static constexpr int kStageBytes = kABytes + kBRows * 128;
-  static constexpr int kStages = CG == 2 ? 6 : 4;
+  static constexpr bool kOut = OP == kDown && FP8;
+  static constexpr int kStages = (CG == 2 ? 6 : 4) - (kOut ? CG : 0);
+  static constexpr int kWarpBytes = kOut ? 2 * 4096 : 2048;
+  static constexpr int kRingBytes = kStages * kStageBytes;
+  static constexpr int kEpiBytes = 8 * kWarpBytes;
 };
-constexpr int kRingBytes = 192 * 1024;
-static_assert(Ring<1>::kStages * Ring<1>::kStageBytes == kRingBytes, "ring");
-static_assert(Ring<2>::kStages * Ring<2>::kStageBytes == kRingBytes, "ring");
 constexpr int kMaxStages = 6;
-constexpr int kEpiBytes = 8 * 2048;    // 32 rows x 64 bytes per epilogue warp
 constexpr int kGroupM = 8;             // row tiles that share weight tiles in L2
 
 struct Shared {
@@ -72,8 +76,16 @@ struct Shared {
   int pre[MOE_MAX_EXPERTS + 1];        // row tiles before expert e
 };
 
-constexpr int kSmemBytes = 1024 + kRingBytes + kEpiBytes + (int)sizeof(Shared);
-static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
+template <int OP, bool FP8, int CG>
+constexpr int smem_bytes() {
+  using P = Plan<OP, FP8, CG>;
+  constexpr int bytes = 1024 + P::kRingBytes + P::kEpiBytes + (int)sizeof(Shared);
+  static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
+  // more than half of an SM's: a second CTA, and with it a second allocation
+  // of the tensor memory, never shares it
+  static_assert(bytes > 114 * 1024, "one CTA per SM");
+  return bytes;
+}
 
 struct Tile {
   int e;
@@ -270,6 +282,17 @@ __device__ __forceinline__ void tile_load(uint4* buf, int lane, const uint8_t* i
   }
 }
 
+// The warp's 32 x 128 bf16 results on their way to the copy engine: two pieces
+// of 64 columns, 128 bytes a row, swizzled as the copies expect. out_begin
+// waits until the last copies have read them.
+__device__ __forceinline__ int out_unit(int row, int u) {
+  return (u >> 3) * 256 + row * 8 + ((u & 7) ^ (row & 7));
+}
+__device__ __forceinline__ void out_begin(int lane) {
+  if (lane == 0) bulk_wait_read();
+  __syncwarp();
+}
+
 // bf16 columns [0, cols) of the lanes' rows to `out` (row pitch in elements);
 // cols is a multiple of 8.
 __device__ __forceinline__ void put_store(uint4* buf, int lane, const uint32_t (&v)[16],
@@ -415,9 +438,9 @@ __device__ __forceinline__ void take_registers() {
 
 // The warp that issues the products: its place in the ring of stages and in
 // the two accumulators.
-template <int CG, bool FP8, bool AMN, bool BMN>
+template <class PLAN, int CG, bool FP8, bool AMN, bool BMN>
 struct Issuer {
-  static constexpr int kStages = Ring<CG>::kStages, kStageBytes = Ring<CG>::kStageBytes;
+  static constexpr int kStages = PLAN::kStages, kStageBytes = PLAN::kStageBytes;
   static constexpr uint32_t kIdesc = mma_desc(FP8, AMN, BMN, kTileM * CG, kTileN);
   // 16 k of bf16 (32 of e4m3): 32 bytes along K, or 16 lines of 128 bytes
   static constexpr uint64_t kA = (AMN ? 2048 : 32) >> 4, kB = (BMN ? 2048 : 32) >> 4;
@@ -532,17 +555,19 @@ __device__ __forceinline__ void fma2(float2& acc, uint32_t lo, uint32_t hi, floa
 template <int OP, bool FP8, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
     k_expert_gemm(const __grid_constant__ CUtensorMap map_a,
-                  const __grid_constant__ CUtensorMap map_b, const ExpertArgs p) {
+                  const __grid_constant__ CUtensorMap map_b,
+                  const __grid_constant__ CUtensorMap map_c, const ExpertArgs p) {
   constexpr bool kAmn = OP == kDw;
   constexpr bool kBmn = OP == kDw || OP == kDgate || OP == kDx;
   constexpr int kElems = FP8 ? 128 : 64;  // reduction elements of one stage
-  constexpr int kStages = Ring<CG>::kStages, kStageBytes = Ring<CG>::kStageBytes;
+  using P = Plan<OP, FP8, CG>;
+  constexpr int kStages = P::kStages, kStageBytes = P::kStageBytes;
   constexpr bool kPair = CG == 2;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint4* epi = reinterpret_cast<uint4*>(smem + kRingBytes);
-  Shared& s = *reinterpret_cast<Shared*>(smem + kRingBytes + kEpiBytes);
+  uint4* epi = reinterpret_cast<uint4*>(smem + P::kRingBytes);
+  Shared& s = *reinterpret_cast<Shared*>(smem + P::kRingBytes + P::kEpiBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = kPair ? (int)(blockIdx.x & 1) : 0;  // clusters are pairs of neighbours
 
@@ -564,6 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     tma_prefetch_map(&map_a);
     tma_prefetch_map(&map_b);
+    if constexpr (P::kOut) tma_prefetch_map(&map_c);
   }
   pdl_wait();  // the segments and the operands come from earlier kernels
   load_segments<CG>(p, s);
@@ -679,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     } else if (warp == 1) {
-      Issuer<CG, FP8, kAmn, kBmn> io(s, smem, tmem, ctl);
+      Issuer<P, CG, FP8, kAmn, kBmn> io(s, smem, tmem, ctl);
       bool ok = true;
       Tile t;
       while (ok && walk.next(t)) {
@@ -708,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     take_registers<FP8>();
     const int ew = warp - kEpiWarp0, quarter = warp & 3, half = ew >> 2;
-    uint4* buf = epi + ew * 128;
+    uint4* buf = epi + ew * (P::kWarpBytes / 16);
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     int as = 0;
     uint32_t aph = 0, parity = 0;
@@ -773,14 +799,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         const long long row = (long long)t.row0 + quarter * 32;
         if constexpr (OP == kDown) {
-          // straight to memory, 32 bytes of a row at a time (a whole sector):
-          // these stores keep the sums' registers, and with them the products,
-          // waiting, so they are few (through shared memory as above a tile
-          // took about 6000 cycles more than its products)
-          uint16_t* out = static_cast<uint16_t*>(p.out) + (row + lane) * p.N + t.n0 * kTileN +
-                          half * 128;
-          const int cols = p.N - t.n0 * kTileN - half * 128;
-          if (mine && cols > 0) {
+          // (Stored by the lanes themselves, 32 rows at a time, a tile's 64 KB
+          // take about 5500 cycles in which the products wait for the
+          // registers; the few warps with a segment's end still do so.)
+          const int col = t.n0 * kTileN + half * 128;
+          const int left = t.rows - quarter * 32;
+          if (col < p.N && left >= 32) {
+            out_begin(lane);
+#pragma unroll
+            for (int g = 0; g < 16; ++g)
+              buf[out_unit(lane, g)] = make_uint4(bf16x2(acc[g * 4].x, acc[g * 4].y),
+                                                  bf16x2(acc[g * 4 + 1].x, acc[g * 4 + 1].y),
+                                                  bf16x2(acc[g * 4 + 2].x, acc[g * 4 + 2].y),
+                                                  bf16x2(acc[g * 4 + 3].x, acc[g * 4 + 3].y));
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&map_c, smem_u32(buf), col, (int)row);
+              tma_store_2d(&map_c, smem_u32(buf) + 4096, col + 64, (int)row);
+              bulk_commit();
+            }
+          } else if (col < p.N && mine) {
+            uint16_t* out = static_cast<uint16_t*>(p.out) + (row + lane) * p.N + col;
 #pragma unroll
             for (int g = 0; g < 8; ++g) {
               uint32_t o[8];
@@ -808,33 +848,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = fmaxf(m, s.amax[parity][half ^ 1][r]);
           parity ^= 1;  // the other buffer next: this one is read until then
           const float scale = __fdiv_rn(m, 448.0f);
-          if (mine) {
-            if (half == 0) p.out_scale[((long long)t.row0 + r) * (p.F >> 7) + t.n0] = scale;
-            uint8_t* out =
-                static_cast<uint8_t*>(p.out) + (row + lane) * p.F + t.n0 * 128 + half * 64;
-            // h / s by the reciprocal: within 2^-23, as h itself
-            const float inv = __frcp_rn(scale);
+          if (mine && half == 0) p.out_scale[((long long)t.row0 + r) * (p.F >> 7) + t.n0] = scale;
+          // h / s by the reciprocal: within 2^-23, as h itself
+          const float inv = __frcp_rn(scale);
+          uint8_t* out =
+              static_cast<uint8_t*>(p.out) + (row + lane) * p.F + t.n0 * 128 + half * 64;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              uint32_t q[8];
+          for (int u = 0; u < 2; ++u) {
+            uint32_t q[8];
 #pragma unroll
-              for (int w = 0; w < 8; ++w) {
-                const float* f = h + 32 * u + 4 * w;
-                if (scale >= 1e-30f) {
-                  q[w] = e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
-                } else if (scale > 0.0f) {  // the reciprocal may overflow
-                  q[w] = e4m3x4(__fdiv_rn(f[0], scale), __fdiv_rn(f[1], scale),
-                                __fdiv_rn(f[2], scale), __fdiv_rn(f[3], scale));
-                } else {
-                  q[w] = 0u;
-                }
+            for (int w = 0; w < 8; ++w) {
+              const float* f = h + 32 * u + 4 * w;
+              if (scale >= 1e-30f) {
+                q[w] = e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+              } else if (scale > 0.0f) {  // the reciprocal may overflow
+                q[w] = e4m3x4(__fdiv_rn(f[0], scale), __fdiv_rn(f[1], scale),
+                              __fdiv_rn(f[2], scale), __fdiv_rn(f[3], scale));
+              } else {
+                q[w] = 0u;
               }
-              store32(out + u * 32, q);
             }
+            if (mine) store32(out + u * 32, q);
           }
         }
       }
     }
+    if constexpr (P::kOut) bulk_wait();  // the copies out of this CTA's memory are done
   }
   __syncwarp();
   tc_fence_before();
@@ -886,7 +925,7 @@ template <int OP, bool FP8, int CG>
 cudaError_t launch(const ExpertArgs& p, const void* a, const void* b, int num_sms,
                    cudaStream_t st) {
   constexpr int kRows = kTileM * CG;
-  CUtensorMap ma, mb;
+  CUtensorMap ma, mb, mc = {};
   cudaError_t e;
   if (OP == kDw) {
     e = make_map(&ma, a, false, p.M, p.rows_max, 0, 64);
@@ -899,6 +938,8 @@ cudaError_t launch(const ExpertArgs& p, const void* a, const void* b, int num_sm
       else e = make_map(&mb, b, false, p.N, p.K, p.E, 64);
     }
   }
+  if (e == cudaSuccess && OP == kDown && FP8)
+    e = make_map(&mc, p.out, false, p.N, p.rows_max, 0, 32);
   if (e != cudaSuccess) return e;
   // Row tiles are at most one per kRows rows plus one per segment.
   const long long segments = p.E < p.rows_max ? p.E : p.rows_max;
@@ -908,7 +949,7 @@ cudaError_t launch(const ExpertArgs& p, const void* a, const void* b, int num_sm
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((tiles < most ? tiles : most) * CG));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.dynamicSmemBytes = smem_bytes<OP, FP8, CG>();
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -919,7 +960,7 @@ cudaError_t launch(const ExpertArgs& p, const void* a, const void* b, int num_sm
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CG == 2 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k_expert_gemm<OP, FP8, CG>, ma, mb, p);
+  return cudaLaunchKernelEx(&cfg, k_expert_gemm<OP, FP8, CG>, ma, mb, mc, p);
 }
 
 // Whether pairs of CTAs share 256-row tiles: each then writes and reads a
@@ -940,14 +981,18 @@ bool use_pair(ExpertOp op, bool fp8, const ExpertArgs& p) {
 template <int OP, bool FP8>
 cudaError_t launch(bool pair, const ExpertArgs& p, const void* a, const void* b, int num_sms,
                    cudaStream_t st) {
-  return pair ? launch<OP, FP8, 2>(p, a, b, num_sms, st) : launch<OP, FP8, 1>(p, a, b, num_sms, st);
+  if constexpr (!FP8) {
+    if (pair) return launch<OP, FP8, 2>(p, a, b, num_sms, st);
+  }
+  return launch<OP, FP8, 1>(p, a, b, num_sms, st);
 }
 
 template <int OP, bool FP8, int CG>
 cudaError_t prepare() {
   const auto kernel = k_expert_gemm<OP, FP8, CG>;
   cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           smem_bytes<OP, FP8, CG>());
   if (e != cudaSuccess || !FP8) return e;
   // The register split (4 warps x 56, 8 warps x 224) spends exactly 12 x 168.
   cudaFuncAttributes attr;
@@ -959,7 +1004,10 @@ cudaError_t prepare() {
 template <int OP, bool FP8>
 cudaError_t prepare() {
   const cudaError_t e = prepare<OP, FP8, 1>();
-  return e == cudaSuccess ? prepare<OP, FP8, 2>() : e;
+  if constexpr (!FP8) {
+    if (e == cudaSuccess) return prepare<OP, FP8, 2>();
+  }
+  return e;
 }
 
 }  // namespace
