@@ -271,25 +271,25 @@ __device__ __forceinline__ void tile_store(const uint4* buf, int lane, uint8_t* 
   }
 }
 
-__device__ __forceinline__ void tile_load(uint4* buf, int lane, const uint8_t* in, long long pitch,
-                                          int rows, int units) {
+// The 32 x 32 bf16 tile at `in` (row pitch in elements), as tile_store's lanes
+// hold it; zeros outside its rows and columns.
+__device__ __forceinline__ void tile_fetch(uint4 (&v)[4], int lane, const uint16_t* in,
+                                           long long pitch, int rows, int cols) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = i * 8 + (lane >> 2), u = lane & 3;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (r < rows && u < units) v = *reinterpret_cast<const uint4*>(in + r * pitch + u * 16);
-    buf[unit_at(r, u)] = v;
+    v[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (r < rows && u * 8 < cols) v[i] = *reinterpret_cast<const uint4*>(in + r * pitch + u * 8);
   }
 }
 
-// The warp's 32 x 128 bf16 results on their way to the copy engine: two pieces
-// of 64 columns, 128 bytes a row, swizzled as the copies expect. out_begin
-// waits until the last copies have read them.
-__device__ __forceinline__ int out_unit(int row, int u) {
-  return (u >> 3) * 256 + row * 8 + ((u & 7) ^ (row & 7));
-}
-__device__ __forceinline__ void out_begin(int lane) {
-  if (lane == 0) bulk_wait_read();
+// A fetched tile, handed to the lanes by row.
+__device__ __forceinline__ void tile_turn(uint4* buf, int lane, const uint4 (&in)[4],
+                                          uint32_t (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) buf[unit_at(i * 8 + (lane >> 2), lane & 3)] = in[i];
+  __syncwarp();
+  tile_get(buf, lane, v);
   __syncwarp();
 }
 
@@ -303,12 +303,28 @@ __device__ __forceinline__ void put_store(uint4* buf, int lane, const uint32_t (
   __syncwarp();
 }
 
-__device__ __forceinline__ void load_get(uint4* buf, int lane, uint32_t (&v)[16],
-                                         const uint16_t* in, long long pitch, int rows, int cols) {
-  tile_load(buf, lane, reinterpret_cast<const uint8_t*>(in), 2 * pitch, rows, cols >> 3);
+// The warp's 32 x 128 bf16 results on their way to the copy engine: two pieces
+// of 64 columns, 128 bytes a row, swizzled as the copies expect. out_begin
+// waits until the last copies have read them.
+__device__ __forceinline__ int out_unit(int row, int u) {
+  return (u >> 3) * 256 + row * 8 + ((u & 7) ^ (row & 7));
+}
+__device__ __forceinline__ void out_begin(int lane) {
+  if (lane == 0) bulk_wait_read();
   __syncwarp();
-  tile_get(buf, lane, v);
-  __syncwarp();
+}
+
+// kDgate: the pre-activations that belong to the 32 columns j of a warp's part
+// of the tile, gate and up.
+struct GateUp {
+  uint4 g[4], u[4];
+};
+__device__ __forceinline__ void gate_fetch(GateUp& v, const ExpertArgs& p, const Tile& t, int half,
+                                           int quarter, int lane, int j) {
+  const int c = t.n0 * kTileN + half * 128 + j * 32, rows = t.rows - quarter * 32;
+  const uint16_t* gu = p.gu + ((long long)t.row0 + quarter * 32) * 2 * p.F + c;
+  tile_fetch(v.g, lane, gu, 2ll * p.F, rows, p.F - c);
+  tile_fetch(v.u, lane, gu + p.F, 2ll * p.F, rows, p.F - c);
 }
 
 // ---- epilogues of a finished bf16 accumulator ------------------------------
@@ -317,7 +333,7 @@ __device__ __forceinline__ void load_get(uint4* buf, int lane, uint32_t (&v)[16]
 template <int OP>
 __device__ __forceinline__ void epilogue_bf16(const ExpertArgs& p, const Tile& t, uint32_t taddr,
                                               int half, int quarter, int lane, uint4* buf,
-                                              bool zero) {
+                                              bool zero, GateUp& pre) {
   const int wrow = quarter * 32;
   if constexpr (OP == kGated) {
     const int rows = t.rows - wrow;
@@ -357,9 +373,9 @@ __device__ __forceinline__ void epilogue_bf16(const ExpertArgs& p, const Tile& t
     for (int j = 0; j < 4; ++j) {
       const int c = t.n0 * kTileN + half * 128 + j * 32;
       uint32_t g[16], u[16], d[32];
-      const uint16_t* gu = p.gu + row * 2 * p.F + c;
-      load_get(buf, lane, g, gu, 2ll * p.F, rows, p.F - c);
-      load_get(buf, lane, u, gu + p.F, 2ll * p.F, rows, p.F - c);
+      tile_turn(buf, lane, pre.g, g);
+      tile_turn(buf, lane, pre.u, u);
+      if (j < 3) gate_fetch(pre, p, t, half, quarter, lane, j + 1);  // beside this part's work
       tc_ld32(d, taddr + half * 128 + j * 32);
       tc_wait_ld();
       tc_loaded(d);
@@ -742,12 +758,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     Tile t;
     while (ok && walk.next(t)) {
       if constexpr (!FP8) {
+        GateUp pre;
+        if constexpr (OP == kDgate) gate_fetch(pre, p, t, half, quarter, lane, 0);
         if (t.kb > 0) {
           ok = __all_sync(~0u, mbar_wait<kPair>(smem_u32(&s.tfull[as]), aph, ctl));
           if (!ok) break;
           tc_fence_after();
         }
-        epilogue_bf16<OP>(p, t, tmem + lanes + as * kTileN, half, quarter, lane, buf, t.kb == 0);
+        epilogue_bf16<OP>(p, t, tmem + lanes + as * kTileN, half, quarter, lane, buf, t.kb == 0,
+                          pre);
         if (t.kb > 0) {
           tc_fence_before();
           __syncwarp();
