@@ -4,12 +4,13 @@
 //   dy[inv[g,j]] = w[g,j] dout[g]            (each receive row has one slot)
 //   dw[g,j]      = <dout[g], y[inv[g,j]]>    (0 for masked and dropped slots)
 //
-// One pass: a CTA takes a token, each thread holds its 16-byte pieces of
-// dout[g] and, for every slot, reads the same pieces of the slot's y row
-// (all slots' loads before the first product), adds their products in fp32
-// and writes the scaled pieces to the slot's dy row. The k sums are then
-// reduced over the CTA in a fixed order (no atomics: the same inputs give the
-// same bits). Bound by HBM: y in, dy out, dout once.
+// One pass: a CTA takes a token at a time; each thread loads its 16-byte pieces
+// of dout[g] and, for every slot, the same pieces of the slot's y row (a few
+// pieces of all slots before the first product), adds their products in fp32
+// and writes the scaled pieces to the slot's dy row. The slots of the CTA's
+// next token are loaded beside this one's rows. The k sums are then reduced
+// over the CTA in a fixed order (no atomics: the same inputs give the same
+// bits). Bound by HBM: y in, dy out, dout once.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -39,46 +40,66 @@ __device__ __forceinline__ float dot8(const uint4 a, const uint4 b, float acc) {
   return acc;
 }
 
-// K slots at a time: K == k for the common k, 8 otherwise (any k).
-template <int K>
+// K slots at a time: K == k for the common k, 8 otherwise (any k). V pieces of
+// a row at a time.
+template <int K, int V>
 __global__ void __launch_bounds__(kThreads) k_combine_backward(const CombineBackwardArgs p) {
   __shared__ int rows_buf[2][MOE_MAX_TOPK];
   __shared__ float w_buf[2][MOE_MAX_TOPK];
   __shared__ float part[2][kThreads / 32][MOE_MAX_TOPK];
   const int nvec = p.H >> 3, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  int par = 0;
+  int par = 0, row_next = -1;
+  float w_next = 0.0f;
+  const auto fetch = [&](long long g) {
+    if (tid < p.k && g < p.T) {
+      row_next = __ldg(p.inv + g * p.k + tid);
+      w_next = __ldg(p.w + g * p.k + tid);
+    }
+  };
   pdl_wait();
+  fetch(blockIdx.x);
   for (long long g = blockIdx.x; g < p.T; g += gridDim.x) {
     int* rows_s = rows_buf[par];
     float* w_s = w_buf[par];
     if (tid < p.k) {
-      const int r = __ldg(p.inv + g * p.k + tid);
-      rows_s[tid] = (r >= 0 && row_ok(r, p.rows, p.status)) ? r : -1;
-      w_s[tid] = __ldg(p.w + g * p.k + tid);
+      rows_s[tid] = (row_next >= 0 && row_ok(row_next, p.rows, p.status)) ? row_next : -1;
+      w_s[tid] = w_next;
     }
     __syncthreads();
+    fetch(g + gridDim.x);
     const uint4* d = reinterpret_cast<const uint4*>(p.dout + g * p.H);
     for (int j0 = 0; j0 < p.k; j0 += K) {
       float acc[K];
 #pragma unroll
       for (int j = 0; j < K; ++j) acc[j] = 0.0f;
-      for (int v = tid; v < nvec; v += kThreads) {
-        const uint4 dv = __ldg(d + v);
-        uint4 yv[K];
+      for (int v0 = tid; v0 < nvec; v0 += V * kThreads) {
+        uint4 dv[V], yv[V][K];
 #pragma unroll
-        for (int j = 0; j < K; ++j) {
-          const int r = j0 + j < p.k ? rows_s[j0 + j] : -1;
-          yv[j] = r >= 0 ? __ldcs(reinterpret_cast<const uint4*>(p.y + (long long)r * p.H) + v)
-                         : make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < V; ++i) {
+          const int v = v0 + i * kThreads;
+          if (v >= nvec) break;
+          dv[i] = __ldg(d + v);
+#pragma unroll
+          for (int j = 0; j < K; ++j) {
+            const int r = j0 + j < p.k ? rows_s[j0 + j] : -1;
+            yv[i][j] = r >= 0 ? __ldcs(reinterpret_cast<const uint4*>(p.y + (long long)r * p.H) + v)
+                              : make_uint4(0u, 0u, 0u, 0u);
+          }
         }
 #pragma unroll
-        for (int j = 0; j < K; ++j) {
-          const int r = j0 + j < p.k ? rows_s[j0 + j] : -1;
-          if (r < 0) continue;
-          acc[j] = dot8(dv, yv[j], acc[j]);
-          const float w = w_s[j0 + j];
-          __stcs(reinterpret_cast<uint4*>(p.dy + (long long)r * p.H) + v,
-                 make_uint4(scale2(dv.x, w), scale2(dv.y, w), scale2(dv.z, w), scale2(dv.w, w)));
+        for (int i = 0; i < V; ++i) {
+          const int v = v0 + i * kThreads;
+          if (v >= nvec) break;
+#pragma unroll
+          for (int j = 0; j < K; ++j) {
+            const int r = j0 + j < p.k ? rows_s[j0 + j] : -1;
+            if (r < 0) continue;
+            acc[j] = dot8(dv[i], yv[i][j], acc[j]);
+            const float w = w_s[j0 + j];
+            __stcs(reinterpret_cast<uint4*>(p.dy + (long long)r * p.H) + v,
+                   make_uint4(scale2(dv[i].x, w), scale2(dv[i].y, w), scale2(dv[i].z, w),
+                              scale2(dv[i].w, w)));
+          }
         }
       }
 #pragma unroll
@@ -104,10 +125,10 @@ cudaError_t launch_combine_backward(const CombineBackwardArgs& a, int num_sms, c
   if (blocks > cap) blocks = cap;
   const dim3 grid((unsigned)blocks), block(kThreads);
   switch (a.k) {
-    case 1: return launch_pdl(k_combine_backward<1>, grid, block, 0, st, a);
-    case 2: return launch_pdl(k_combine_backward<2>, grid, block, 0, st, a);
-    case 4: return launch_pdl(k_combine_backward<4>, grid, block, 0, st, a);
-    default: return launch_pdl(k_combine_backward<8>, grid, block, 0, st, a);
+    case 1: return launch_pdl(k_combine_backward<1, 4>, grid, block, 0, st, a);
+    case 2: return launch_pdl(k_combine_backward<2, 4>, grid, block, 0, st, a);
+    case 4: return launch_pdl(k_combine_backward<4, 2>, grid, block, 0, st, a);
+    default: return launch_pdl(k_combine_backward<8, 1>, grid, block, 0, st, a);
   }
 }
 
