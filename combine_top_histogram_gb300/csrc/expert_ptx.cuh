@@ -134,6 +134,7 @@ __device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, co
 template <bool PAIR>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const WaitCtl& c) {
   if (mbar_test(bar, parity)) return true;
+  if (c.limit > 0 && mbar_try(bar, parity)) return true;  // suspended for a while
   return mbar_wait_slow<PAIR>(bar, parity, c);
 }
 
