@@ -41,21 +41,21 @@ namespace moe {
 namespace {
 
 constexpr int kTileM = 128;            // rows of one CTA's accumulator
-constexpr int kTileN = 256;
+constexpr int kAccColumns = 256;       // tensor-memory columns of one accumulator
 constexpr int kThreads = 384;          // copy, product, TMEM, spare; 8 epilogue warps
 constexpr int kEpiWarp0 = 4;
 constexpr int kABytes = kTileM * 128;  // a stage holds 128 bytes of K (or 64 k) per row
 // Shared memory of a kernel: the ring of stages, and what the epilogue warps
 // pass their results through: 32 rows x 64 bytes per warp, or (kOut) the
-// warp's whole 32 x 128 bf16 results, which the copy engine then writes beside
-// the next tile's products; those take the room of a stage or two.
-template <int OP, bool FP8, int CG>
+// warp's whole 32 x TN / 2 bf16 results, which the copy engine then writes
+// beside the next tile's products; those take the room of one stage.
+template <int OP, bool FP8, int CG, int TN>
 struct Plan {
-  static constexpr int kBRows = kTileN / CG;  // rows (or columns) of B in one CTA
+  static constexpr int kBRows = TN / CG;  // rows (or columns) of B in one CTA
   static constexpr int kStageBytes = kABytes + kBRows * 128;
-  static constexpr bool kOut = OP == kDown && FP8;
-  static constexpr int kStages = (CG == 2 ? 6 : 4) - (kOut ? CG : 0);
-  static constexpr int kWarpBytes = kOut ? 2 * 4096 : 2048;
+  static constexpr bool kOut = (OP == kDown && FP8) || (OP == kDw && TN == 128);
+  static constexpr int kStages = (kStageBytes > 32768 ? 4 : 6) - (kOut ? CG : 0);
+  static constexpr int kWarpBytes = kOut ? TN / 128 * 4096 : 2048;
   static constexpr int kRingBytes = kStages * kStageBytes;
   static constexpr int kEpiBytes = 8 * kWarpBytes;
 };
@@ -76,9 +76,9 @@ struct Shared {
   int pre[MOE_MAX_EXPERTS + 1];        // row tiles before expert e
 };
 
-template <int OP, bool FP8, int CG>
+template <int OP, bool FP8, int CG, int TN>
 constexpr int smem_bytes() {
-  using P = Plan<OP, FP8, CG>;
+  using P = Plan<OP, FP8, CG, TN>;
   constexpr int bytes = 1024 + P::kRingBytes + P::kEpiBytes + (int)sizeof(Shared);
   static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
   // more than half of an SM's: a second CTA, and with it a second allocation
@@ -303,9 +303,9 @@ __device__ __forceinline__ void put_store(uint4* buf, int lane, const uint32_t (
   __syncwarp();
 }
 
-// The warp's 32 x 128 bf16 results on their way to the copy engine: two pieces
-// of 64 columns, 128 bytes a row, swizzled as the copies expect. out_begin
-// waits until the last copies have read them.
+// The warp's bf16 results on their way to the copy engine: pieces of 32 rows x
+// 64 columns, 128 bytes a row, swizzled as the copies expect. out_begin waits
+// until the last copies have read them.
 __device__ __forceinline__ int out_unit(int row, int u) {
   return (u >> 3) * 256 + row * 8 + ((u & 7) ^ (row & 7));
 }
@@ -319,9 +319,10 @@ __device__ __forceinline__ void out_begin(int lane) {
 struct GateUp {
   uint4 g[4], u[4];
 };
+template <int TN>
 __device__ __forceinline__ void gate_fetch(GateUp& v, const ExpertArgs& p, const Tile& t, int half,
                                            int quarter, int lane, int j) {
-  const int c = t.n0 * kTileN + half * 128 + j * 32, rows = t.rows - quarter * 32;
+  const int c = t.n0 * TN + half * (TN / 2) + j * 32, rows = t.rows - quarter * 32;
   const uint16_t* gu = p.gu + ((long long)t.row0 + quarter * 32) * 2 * p.F + c;
   tile_fetch(v.g, lane, gu, 2ll * p.F, rows, p.F - c);
   tile_fetch(v.u, lane, gu + p.F, 2ll * p.F, rows, p.F - c);
@@ -330,20 +331,20 @@ __device__ __forceinline__ void gate_fetch(GateUp& v, const ExpertArgs& p, const
 // ---- epilogues of a finished bf16 accumulator ------------------------------
 // taddr: the warp's lanes and the accumulator's first column. half: which of
 // the two warps that share the lanes (each takes half of the columns).
-template <int OP>
+template <int OP, int TN>
 __device__ __forceinline__ void epilogue_bf16(const ExpertArgs& p, const Tile& t, uint32_t taddr,
                                               int half, int quarter, int lane, uint4* buf,
-                                              bool zero, GateUp& pre) {
+                                              bool zero, GateUp& pre, const CUtensorMap& map_c) {
   const int wrow = quarter * 32;
   if constexpr (OP == kGated) {
     const int rows = t.rows - wrow;
     const long long row = (long long)t.row0 + wrow;
 #pragma unroll 1
-    for (int j = 0; j < 2; ++j) {
-      const int c = t.n0 * 128 + half * 64 + j * 32;
+    for (int j = 0; j < TN / 128; ++j) {
+      const int at = half * (TN / 4) + j * 32, c = t.n0 * (TN / 2) + at;
       uint32_t g[32], u[32], h[16];
-      tc_ld32(g, taddr + half * 64 + j * 32);
-      tc_ld32(u, taddr + 128 + half * 64 + j * 32);
+      tc_ld32(g, taddr + at);
+      tc_ld32(u, taddr + TN / 2 + at);
       tc_wait_ld();
       tc_loaded(g);
       tc_loaded(u);
@@ -370,13 +371,13 @@ __device__ __forceinline__ void epilogue_bf16(const ExpertArgs& p, const Tile& t
     const int rows = t.rows - wrow;
     const long long row = (long long)t.row0 + wrow;
 #pragma unroll 1
-    for (int j = 0; j < 4; ++j) {
-      const int c = t.n0 * kTileN + half * 128 + j * 32;
+    for (int j = 0; j < TN / 64; ++j) {
+      const int at = half * (TN / 2) + j * 32, c = t.n0 * TN + at;
       uint32_t g[16], u[16], d[32];
       tile_turn(buf, lane, pre.g, g);
       tile_turn(buf, lane, pre.u, u);
-      if (j < 3) gate_fetch(pre, p, t, half, quarter, lane, j + 1);  // beside this part's work
-      tc_ld32(d, taddr + half * 128 + j * 32);
+      if (j < TN / 64 - 1) gate_fetch<TN>(pre, p, t, half, quarter, lane, j + 1);  // beside this part's work
+      tc_ld32(d, taddr + at);
       tc_wait_ld();
       tc_loaded(d);
 #pragma unroll
@@ -393,25 +394,59 @@ __device__ __forceinline__ void epilogue_bf16(const ExpertArgs& p, const Tile& t
       put_store(buf, lane, g, out, 2ll * p.F, rows, p.F - c);
       put_store(buf, lane, u, out + p.F, 2ll * p.F, rows, p.F - c);
     }
+  } else if constexpr (OP == kDw && TN == 128) {
+    // to the copy engine, which leaves out what lies past the gradient's rows
+    // or columns
+    const int col = t.n0 * TN + half * 64, row = t.m0 + wrow;
+    if (row >= p.M || col >= p.N) return;
+    out_begin(lane);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      uint32_t d[32];
+      if (zero) {  // a segment without rows
+#pragma unroll
+        for (int i = 0; i < 32; ++i) d[i] = 0u;
+      } else {
+        tc_ld32(d, taddr + half * 64 + j * 32);
+        tc_wait_ld();
+        tc_loaded(d);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          o[i] = bf16x2(__uint_as_float(d[8 * u + 2 * i]), __uint_as_float(d[8 * u + 2 * i + 1]));
+        buf[out_unit(lane, j * 4 + u)] = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_3d(&map_c, smem_u32(buf), col, row, t.e);
+      bulk_commit();
+    }
   } else {
     const int rows = OP == kDw ? p.M - t.m0 - wrow : t.rows - wrow;
     const long long row = OP == kDw ? (long long)t.e * p.M + t.m0 + wrow : (long long)t.row0 + wrow;
+    if (zero) {  // kDw: a segment without rows; half a row of the tile per 16 lanes
+      const int c = t.n0 * TN + half * (TN / 2) + (lane & 15) * 8;
+      uint16_t* out = static_cast<uint16_t*>(p.out) + (row + (lane >> 4)) * p.N + c;
+      if (c < p.N)
+        for (int r = lane >> 4; r < min(rows, 32); r += 2, out += 2ll * p.N)
+          *reinterpret_cast<uint4*>(out) = make_uint4(0u, 0u, 0u, 0u);
+      return;
+    }
 #pragma unroll 1
-    for (int j = 0; j < 4; ++j) {
-      const int c = t.n0 * kTileN + half * 128 + j * 32;
-      uint32_t o[16];
-      if (zero) {  // a segment without rows
+    for (int j = 0; j < TN / 64; ++j) {
+      const int at = half * (TN / 2) + j * 32, c = t.n0 * TN + at;
+      uint32_t d[32], o[16];
+      tc_ld32(d, taddr + at);
+      tc_wait_ld();
+      tc_loaded(d);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = 0u;
-      } else {
-        uint32_t d[32];
-        tc_ld32(d, taddr + half * 128 + j * 32);
-        tc_wait_ld();
-        tc_loaded(d);
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          o[i] = bf16x2(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1]));
-      }
+      for (int i = 0; i < 16; ++i)
+        o[i] = bf16x2(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1]));
       put_store(buf, lane, o, static_cast<uint16_t*>(p.out) + row * p.N + c, p.N, rows, p.N - c);
     }
   }
@@ -454,10 +489,10 @@ __device__ __forceinline__ void take_registers() {
 
 // The warp that issues the products: its place in the ring of stages and in
 // the two accumulators.
-template <class PLAN, int CG, bool FP8, bool AMN, bool BMN>
+template <class PLAN, int CG, int TN, bool FP8, bool AMN, bool BMN>
 struct Issuer {
   static constexpr int kStages = PLAN::kStages, kStageBytes = PLAN::kStageBytes;
-  static constexpr uint32_t kIdesc = mma_desc(FP8, AMN, BMN, kTileM * CG, kTileN);
+  static constexpr uint32_t kIdesc = mma_desc(FP8, AMN, BMN, kTileM * CG, TN);
   // 16 k of bf16 (32 of e4m3): 32 bytes along K, or 16 lines of 128 bytes
   static constexpr uint64_t kA = (AMN ? 2048 : 32) >> 4, kB = (BMN ? 2048 : 32) >> 4;
   const uint32_t full0, empty0, tfull0, tempty0, tmem;
@@ -484,7 +519,7 @@ struct Issuer {
   // The products of the stage, `steps` of 16 k (e4m3: 32); begins, ends: of
   // the sum in the accumulator.
   __device__ __forceinline__ void block(bool begins, bool ends, int steps) {
-    const uint32_t d = tmem + as * kTileN;
+    const uint32_t d = tmem + as * kAccColumns;
     const uint64_t da = da0 + (uint64_t)(st * (kStageBytes >> 4));
     const uint64_t db = db0 + (uint64_t)(st * (kStageBytes >> 4));
     if (steps == 4) {
@@ -568,7 +603,7 @@ __device__ __forceinline__ void fma2(float2& acc, uint32_t lo, uint32_t hi, floa
   acc = __ffma2_rn(make_float2(__uint_as_float(lo), __uint_as_float(hi)), make_float2(s, s), acc);
 }
 
-template <int OP, bool FP8, int CG>
+template <int OP, bool FP8, int CG, int TN>
 __global__ void __launch_bounds__(kThreads, 1)
     k_expert_gemm(const __grid_constant__ CUtensorMap map_a,
                   const __grid_constant__ CUtensorMap map_b,
@@ -576,7 +611,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool kAmn = OP == kDw;
   constexpr bool kBmn = OP == kDw || OP == kDgate || OP == kDx;
   constexpr int kElems = FP8 ? 128 : 64;  // reduction elements of one stage
-  using P = Plan<OP, FP8, CG>;
+  using P = Plan<OP, FP8, CG, TN>;
+  static_assert(TN == 256 || (TN == 128 && !FP8 && CG == 1), "tile");
   constexpr int kStages = P::kStages, kStageBytes = P::kStageBytes;
   constexpr bool kPair = CG == 2;
 
@@ -636,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // copies cover at least the tile's rows (a pair's always 128)
         const int a_copies = kAmn ? 0 : kPair ? 1 : (min(rows, kTileM) + p.a_box - 1) / p.a_box;
         const uint32_t bytes =
-            kAmn || kPair ? kStageBytes : a_copies * p.a_box * 128 + kTileN * 128;
+            kAmn || kPair ? kStageBytes : a_copies * p.a_box * 128 + TN * 128;
         for (int kb = 0; kb < blocks; ++kb) {
           ok = __all_sync(~0u, mbar_wait<kPair>(empty0 + st * 8, ph ^ 1, ctl));
           if (!ok) break;
@@ -663,11 +699,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < a_copies; ++i)
               tma_load_2d<CG>(a + i * p.a_box * 128, &map_a, bar, kb * kElems, row0 + i * p.a_box);
           }
-          // B: 256 columns, or this CTA's 128 of them
+          // B: the tile's columns, or this CTA's half of them
           if constexpr (kBmn) {
 #pragma unroll
-            for (int i = 0; i < 4 / CG; ++i) {
-              const int n = n0 * kTileN + rank * 128 + i * 64;
+            for (int i = 0; i < TN / 64 / CG; ++i) {
+              const int n = n0 * TN + rank * 128 + i * 64;
               if constexpr (OP == kDw)
                 tma_load_2d<CG>(b + i * 8192, &map_b, bar, n, row0 + kb * 64);
               else
@@ -677,8 +713,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 2 / CG; ++i) {
               const int half = i + rank;  // kGated: gate columns, then up columns
-              const int n = OP == kGated ? half * p.F + n0 * 128 : n0 * kTileN + half * 128;
-              tma_load_3d<CG>(b + i * 16384, &map_b, bar, kb * kElems, n, e);
+              const int n = OP == kGated ? half * p.F + n0 * (TN / 2) : n0 * TN + half * (TN / 2);
+              tma_load_3d<CG>(b + i * (TN / 2 * 128), &map_b, bar, kb * kElems, n, e);
             }
           }
           if (issued < kStages) ++issued;
@@ -714,14 +750,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = __all_sync(~0u,
                           mbar_wait<kPair>(smem_u32(&s.tail[last]), (phases >> last) & 1, ctl));
           if (!ok) break;
-          clear_rows<2 + 4 / CG>(smem + last * kStageBytes, valid, lane);
+          clear_rows<2 + TN / 64 / CG>(smem + last * kStageBytes, valid, lane);
           if (lane == 0) mbar_arrive_release(cluster_addr(smem_u32(&s.full[last]), 0));
           phases ^= 1u << last;
         }
       }
       __syncwarp();
     } else if (warp == 1) {
-      Issuer<P, CG, FP8, kAmn, kBmn> io(s, smem, tmem, ctl);
+      Issuer<P, CG, TN, FP8, kAmn, kBmn> io(s, smem, tmem, ctl);
       bool ok = true;
       Tile t;
       while (ok && walk.next(t)) {
@@ -734,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (OP == kDw && tail != 0 && kb == blocks - 1) {
             // rows of the next segment follow: zero them in both operands
             steps = (tail + 15) >> 4;
-            clear_rows<2 + 4 / CG>(smem + io.st * kStageBytes, tail, lane);
+            clear_rows<2 + TN / 64 / CG>(smem + io.st * kStageBytes, tail, lane);
           }
           io.block(FP8 || kb == 0, FP8 || kb == blocks - 1, steps);
         }
@@ -759,14 +795,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && walk.next(t)) {
       if constexpr (!FP8) {
         GateUp pre;
-        if constexpr (OP == kDgate) gate_fetch(pre, p, t, half, quarter, lane, 0);
+        if constexpr (OP == kDgate) gate_fetch<TN>(pre, p, t, half, quarter, lane, 0);
         if (t.kb > 0) {
           ok = __all_sync(~0u, mbar_wait<kPair>(smem_u32(&s.tfull[as]), aph, ctl));
           if (!ok) break;
           tc_fence_after();
         }
-        epilogue_bf16<OP>(p, t, tmem + lanes + as * kTileN, half, quarter, lane, buf, t.kb == 0,
-                          pre);
+        epilogue_bf16<OP, TN>(p, t, tmem + lanes + as * kAccColumns, half, quarter, lane, buf, t.kb == 0,
+                          pre, map_c);
         if (t.kb > 0) {
           tc_fence_before();
           __syncwarp();
@@ -788,7 +824,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = __all_sync(~0u, mbar_wait<kPair>(smem_u32(&s.tfull[as]), aph, ctl));
           if (!ok) break;
           tc_fence_after();
-          const uint32_t ta = tmem + lanes + as * kTileN;
+          const uint32_t ta = tmem + lanes + as * kAccColumns;
           uint32_t v[2][32];
           tc_ld32(v[0], ta + c0);
           const float2 sc = s.scale[as][r];
@@ -821,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // (Stored by the lanes themselves, 32 rows at a time, a tile's 64 KB
           // take about 5500 cycles in which the products wait for the
           // registers; the few warps with a segment's end still do so.)
-          const int col = t.n0 * kTileN + half * 128;
+          const int col = t.n0 * TN + half * 128;
           const int left = t.rows - quarter * 32;
           if (col < p.N && left >= 32) {
             out_begin(lane);
@@ -940,10 +976,28 @@ cudaError_t make_map(CUtensorMap* m, const void* base, bool fp8, long long cols,
   return rc == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int OP, bool FP8, int CG>
-cudaError_t launch(const ExpertArgs& p, const void* a, const void* b, int num_sms,
+// Row tiles are at most one per `rows` rows plus one per segment; the host
+// knows no more.
+template <int OP>
+long long most_tiles(const ExpertArgs& p, int rows, int nt) {
+  if (OP == kDw) return (long long)((p.M + rows - 1) / rows) * nt * p.E;
+  return (p.rows_max / rows + (p.E < p.rows_max ? p.E : p.rows_max)) * nt;
+}
+
+template <int OP>
+int column_tiles(const ExpertArgs& p, int tn) {
+  const int n = OP == kGated ? p.F : p.N, w = OP == kGated ? tn / 2 : tn;
+  return (n + w - 1) / w;
+}
+
+template <int OP, bool FP8, int CG, int TN>
+cudaError_t launch(const ExpertArgs& args, const void* a, const void* b, int num_sms,
                    cudaStream_t st) {
   constexpr int kRows = kTileM * CG;
+  ExpertArgs p = args;
+  p.nt = column_tiles<OP>(p, TN);
+  // Segments of a few rows copy no more than those, 32 at a time.
+  p.a_box = CG == 1 && p.rows_max <= 64ll * p.E ? 32 : 128;
   CUtensorMap ma, mb, mc = {};
   cudaError_t e;
   if (OP == kDw) {
@@ -952,23 +1006,22 @@ cudaError_t launch(const ExpertArgs& p, const void* a, const void* b, int num_sm
   } else {
     e = make_map(&ma, a, FP8, p.K, p.rows_max, 0, p.a_box);
     if (e == cudaSuccess) {
-      if (OP == kGated) e = make_map(&mb, b, FP8, p.K, 2ll * p.F, p.E, 128);
-      else if (OP == kDown) e = make_map(&mb, b, FP8, p.K, p.N, p.E, 128);
+      if (OP == kGated) e = make_map(&mb, b, FP8, p.K, 2ll * p.F, p.E, TN / 2);
+      else if (OP == kDown) e = make_map(&mb, b, FP8, p.K, p.N, p.E, TN / 2);
       else e = make_map(&mb, b, false, p.N, p.K, p.E, 64);
     }
   }
+  if (e == cudaSuccess && OP == kDw && TN == 128)
+    e = make_map(&mc, p.out, false, p.N, p.M, p.E, 32);
   if (e == cudaSuccess && OP == kDown && FP8)
     e = make_map(&mc, p.out, false, p.N, p.rows_max, 0, 32);
   if (e != cudaSuccess) return e;
-  // Row tiles are at most one per kRows rows plus one per segment.
-  const long long segments = p.E < p.rows_max ? p.E : p.rows_max;
-  const long long tiles = OP == kDw ? (long long)((p.M + kRows - 1) / kRows) * p.nt * p.E
-                                    : (p.rows_max / kRows + segments) * p.nt;
+  const long long tiles = most_tiles<OP>(p, kRows, p.nt);
   const long long most = num_sms / CG;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((tiles < most ? tiles : most) * CG));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem_bytes<OP, FP8, CG>();
+  cfg.dynamicSmemBytes = smem_bytes<OP, FP8, CG, TN>();
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -979,7 +1032,7 @@ cudaError_t launch(const ExpertArgs& p, const void* a, const void* b, int num_sm
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CG == 2 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k_expert_gemm<OP, FP8, CG>, ma, mb, mc, p);
+  return cudaLaunchKernelEx(&cfg, k_expert_gemm<OP, FP8, CG, TN>, ma, mb, mc, p);
 }
 
 // Whether pairs of CTAs share 256-row tiles: each then writes and reads a
@@ -997,21 +1050,36 @@ bool use_pair(ExpertOp op, bool fp8, const ExpertArgs& p) {
   return p.rows_max >= (op == kDw ? 768ll : 192ll) * p.E;
 }
 
+// Whether tiles are 128 columns wide: where 256 would give at most two tiles
+// per SM, more and smaller ones spread a product's copies, which bound it then,
+// over more SMs (64 bytes a cycle go into each). Drawn bf16 cases of all
+// products, tiles of 256 / 128 columns, us: backward of 77 tokens, top-3,
+// E = 16, H = 520, F = 264 40.5 / 30.8, down of 10740 tokens, top-5, E = 17,
+// H = 1824, F = 1432 277 / 238; 0.94 of the time in the mean over 31 cases with
+// this rule, 0.96 with half of its threshold, 0.945 with twice. Where tiles are
+// many, narrow ones cost: kDw of E = 32, H = 4096, F = 2048 at 512 rows an
+// expert makes its backward pass 1316 / 1618.
+template <int OP>
+bool use_narrow(const ExpertArgs& p, int num_sms) {
+  return most_tiles<OP>(p, kTileM, column_tiles<OP>(p, 256)) <= 2ll * num_sms;
+}
+
 template <int OP, bool FP8>
 cudaError_t launch(bool pair, const ExpertArgs& p, const void* a, const void* b, int num_sms,
                    cudaStream_t st) {
   if constexpr (!FP8) {
-    if (pair) return launch<OP, FP8, 2>(p, a, b, num_sms, st);
+    if (pair) return launch<OP, FP8, 2, 256>(p, a, b, num_sms, st);
+    if (use_narrow<OP>(p, num_sms)) return launch<OP, FP8, 1, 128>(p, a, b, num_sms, st);
   }
-  return launch<OP, FP8, 1>(p, a, b, num_sms, st);
+  return launch<OP, FP8, 1, 256>(p, a, b, num_sms, st);
 }
 
-template <int OP, bool FP8, int CG>
+template <int OP, bool FP8, int CG, int TN>
 cudaError_t prepare() {
-  const auto kernel = k_expert_gemm<OP, FP8, CG>;
+  const auto kernel = k_expert_gemm<OP, FP8, CG, TN>;
   cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           smem_bytes<OP, FP8, CG>());
+                           smem_bytes<OP, FP8, CG, TN>());
   if (e != cudaSuccess || !FP8) return e;
   // The register split (4 warps x 56, 8 warps x 224) spends exactly 12 x 168.
   cudaFuncAttributes attr;
@@ -1022,9 +1090,10 @@ cudaError_t prepare() {
 
 template <int OP, bool FP8>
 cudaError_t prepare() {
-  const cudaError_t e = prepare<OP, FP8, 1>();
+  cudaError_t e = prepare<OP, FP8, 1, 256>();
   if constexpr (!FP8) {
-    if (e == cudaSuccess) return prepare<OP, FP8, 2>();
+    if (e == cudaSuccess) e = prepare<OP, FP8, 2, 256>();
+    if (e == cudaSuccess) e = prepare<OP, FP8, 1, 128>();
   }
   return e;
 }
@@ -1045,8 +1114,6 @@ cudaError_t expert_gemm_prepare() {
 cudaError_t launch_expert_gemm(ExpertOp op, bool fp8, const ExpertArgs& args, const void* a,
                                const void* b, int num_sms, cudaStream_t st) {
   ExpertArgs p = args;
-  p.a_box = 128;
-  p.nt = op == kGated ? (p.F + 127) / 128 : (p.N + kTileN - 1) / kTileN;
   const bool pair = use_pair(op, fp8, p);
   switch (op) {
     case kGated:
