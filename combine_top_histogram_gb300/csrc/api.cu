@@ -799,7 +799,8 @@ int moe_combine_tokens(moe_handle_t h, int64_t token_begin, int64_t token_end, c
 int moe_combine_backward(moe_handle_t h, const void* dout, const void* y, const float* w, void* dy,
                          float* dw, void* stream) {
   if (!h || !dout || !y || !w || !dy || !dw) return MOE_ERR_INVALID_ARG;
-  if (!aligned(dout, 16) || !aligned(y, 16) || !aligned(dy, 16)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(dout, 16) || !aligned(y, 16) || !aligned(dy, 16) || !aligned(w, 4) || !aligned(dw, 4))
+    return MOE_ERR_INVALID_ARG;
   if (h->dispatch_gen == 0 || h->dispatch_gen != h->layout_gen) return MOE_ERR_STATE;
   moe::CombineBackwardArgs a{};
   a.dout = static_cast<const uint16_t*>(dout);

@@ -34,8 +34,9 @@ int validate(const moe_expert_config_t* c) {
   // int32 tile numbers: 128 rows x 128 columns at least, per expert and widest
   // side of a product
   const long long wide = (c->hidden > 2ll * c->inter ? c->hidden : 2ll * c->inter) / 128 + 1;
-  if ((c->rows_max / 128 + c->num_experts) * wide >= (1ll << 31) ||
-      wide * wide * c->num_experts >= (1ll << 31))
+  constexpr long long kMost = (1ll << 31) - 4096;  // a step past the last tile fits too
+  if ((c->rows_max / 128 + c->num_experts) * wide >= kMost ||
+      wide * wide * c->num_experts >= kMost)
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
@@ -126,7 +127,9 @@ int moe_expert_gated(moe_expert_t x, const int32_t* expert_offset, const void* i
   if (fp8 ? (!in_scale || !w13_scale || !hid_scale || gate_up)
           : (in_scale || w13_scale || hid_scale))
     return MOE_ERR_INVALID_ARG;
-  if (!aligned(in, 16) || !aligned(w13, 16) || !aligned(hid, 16) || !aligned(gate_up, 16))
+  if (!aligned(in, 16) || !aligned(w13, 16) || !aligned(hid, 16) || !aligned(gate_up, 16) ||
+      !aligned(expert_offset, 4) || !aligned(in_scale, 4) || !aligned(w13_scale, 4) ||
+      !aligned(hid_scale, 4))
     return MOE_ERR_INVALID_ARG;
   moe::ExpertArgs a = expert_args(x, expert_offset);
   a.N = x->cfg.inter;
@@ -145,7 +148,9 @@ int moe_expert_down(moe_expert_t x, const int32_t* expert_offset, const void* hi
   if (!x || !expert_offset || !hid || !w2 || !y) return MOE_ERR_INVALID_ARG;
   const bool fp8 = x->cfg.dtype == MOE_FP8_E4M3;
   if (fp8 ? (!hid_scale || !w2_scale) : (hid_scale || w2_scale)) return MOE_ERR_INVALID_ARG;
-  if (!aligned(hid, 16) || !aligned(w2, 16) || !aligned(y, 16)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(hid, 16) || !aligned(w2, 16) || !aligned(y, 16) || !aligned(expert_offset, 4) ||
+      !aligned(hid_scale, 4) || !aligned(w2_scale, 4))
+    return MOE_ERR_INVALID_ARG;
   moe::ExpertArgs a = expert_args(x, expert_offset);
   a.N = x->cfg.hidden;
   a.K = x->cfg.inter;
@@ -163,7 +168,7 @@ int moe_expert_backward(moe_expert_t x, const int32_t* expert_offset, const void
   if ((!dw13) != (!dw2) || (!dx && !dw13)) return MOE_ERR_INVALID_ARG;
   if (!aligned(in, 16) || !aligned(gate_up, 16) || !aligned(hid, 16) || !aligned(dy, 16) ||
       !aligned(w13, 16) || !aligned(w2, 16) || !aligned(dx, 16) || !aligned(dw13, 16) ||
-      !aligned(dw2, 16))
+      !aligned(dw2, 16) || !aligned(expert_offset, 4))
     return MOE_ERR_INVALID_ARG;
   if (!x->cfg.train) return MOE_ERR_STATE;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -545,11 +545,12 @@ struct Issuer {
 // FP8: two warps keep the scales of the next accumulators ready, so that the
 // epilogue warps never wait for memory: for each reduction block the 128 rows'
 // scale times those of the tile's two weight blocks. Thread j of 64 serves
-// rows j and j + 64 and loads four blocks ahead.
+// rows j and j + 64 and loads two blocks ahead (four spilled registers that
+// the issuing warp of the same register share then missed: 2 % slower).
 template <int OP, int CG>
 __device__ __forceinline__ void scale_warp(const ExpertArgs& p, Shared& s, const WaitCtl& ctl,
                                            Walk<OP, CG>& walk, int j) {
-  constexpr int kAhead = 4;
+  constexpr int kAhead = 2;
   int as = 0;
   uint32_t ph = 1;
   Tile t;

@@ -365,6 +365,68 @@ def test_offsets_are_held_to_the_buffers(gpu):
         assert untouched(hid[rows:]) and untouched(y[rows:])
 
 
+@pytest.mark.parametrize("spare", ["exact", "roomy"])
+def test_rows_past_32_bit_offsets(gpu, spare):
+    """Segments whose rows start more than 2^32 bytes (and 2^31 elements) into their buffers."""
+    counts, H, F = [1, 130, 3], 4104, 16
+    E, n = len(counts), sum(counts)
+    first = (1 << 31) // H + 1
+    rows = first + n + SPARE[spare][0]
+    assert first * H * 2 > 1 << 32
+    off = offsets(counts) + first
+    big = lambda w: torch.zeros(rows, w, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    x, dy, dx = big(H), big(H), big(H)
+    gu, hid = big(2 * F), big(F)
+    tail = slice(first, first + n)
+    x[tail], dy[tail] = normal(n, H), normal(n, H, std=0.1, seed=3)
+    w13, w2 = normal(E, 2 * F, H, std=H ** -0.5, seed=1), normal(E, H, F, std=F ** -0.5, seed=2)
+    h = B.moe_expert_create(B.make_expert_config(E, H, F, rows, train=True))
+    B.moe_expert_gated(h, off, x, None, w13, None, hid, None, gu)
+    both, err = R.rows_times(x[tail].double(), w13.double(), counts)
+    v, e = R.silu_product(both[:, :F], both[:, F:], err[:, :F], err[:, F:])
+    R.check("hid", hid[tail], *R.bf16_out(v, e))
+    R.check("gate_up", gu[tail], *R.bf16_out(both, err))
+    B.moe_expert_down(h, off, hid, None, w2, None, dx)  # dx as y, for room
+    R.check("y", dx[tail], *R.bf16_out(*R.rows_times(hid[tail].double(), w2.double(), counts)))
+    dw13, dw2 = poisoned(E, 2 * F, H), poisoned(E, H, F)
+    B.moe_expert_backward(h, off, x, gu, hid, dy, w13, w2, dx, dw13, dw2)
+    want = R.backward(*(t[tail].double() for t in (x, gu, hid, dy)), w13.double(), w2.double(),
+                      counts)
+    for name, got, ref in (("dx", dx[tail], want[0]), ("dw13", dw13, want[1]),
+                           ("dw2", dw2, want[2])):
+        R.check(name, got, *ref)
+    assert B.moe_expert_read_status(h) == 0 and not dx[:first].any() and not hid[:first].any()
+
+
+@pytest.mark.parametrize("rows", [3, 140])
+def test_weights_past_32_bit_offsets(gpu, rows):
+    """The last expert's weights and gradients lie more than 2^32 bytes into theirs."""
+    H, F = 4104, 1032
+    E = (1 << 31) // (2 * F * H) + 2
+    counts = [0] * (E - 1) + [rows]
+    w13 = torch.zeros(E, 2 * F, H, dtype=torch.bfloat16, device="cuda")
+    w2 = torch.zeros(E, H, F, dtype=torch.bfloat16, device="cuda")
+    w13[-1], w2[-1] = normal(2 * F, H, std=H ** -0.5, seed=1), normal(H, F, std=F ** -0.5, seed=2)
+    x, dy = normal(rows, H), normal(rows, H, std=0.1, seed=3)
+    hid, gu, y, dx = poisoned(rows, F), poisoned(rows, 2 * F), poisoned(rows, H), poisoned(rows, H)
+    h = B.moe_expert_create(B.make_expert_config(E, H, F, rows, train=True))
+    off = offsets(counts)
+    B.moe_expert_gated(h, off, x, None, w13, None, hid, None, gu)
+    one = [rows]
+    both, err = R.rows_times(x.double(), w13[-1:].double(), one)
+    v, e = R.silu_product(both[:, :F], both[:, F:], err[:, :F], err[:, F:])
+    R.check("hid", hid, *R.bf16_out(v, e))
+    B.moe_expert_down(h, off, hid, None, w2, None, y)
+    R.check("y", y, *R.bf16_out(*R.rows_times(hid.double(), w2[-1:].double(), one)))
+    dw13, dw2 = poisoned(E, 2 * F, H), poisoned(E, H, F)
+    B.moe_expert_backward(h, off, x, gu, hid, dy, w13, w2, dx, dw13, dw2)
+    want = R.backward(*(t.double() for t in (x, gu, hid, dy, w13[-1:], w2[-1:])), one)
+    R.check("dx", dx, *want[0])
+    R.check("dw13", dw13[-1:], *want[1])
+    R.check("dw2", dw2[-1:], *want[2])
+    assert not dw13[:-1].any() and not dw2[:-1].any() and B.moe_expert_read_status(h) == 0
+
+
 def test_waits_that_run_out_set_the_status(gpu):
     """With a wait limit of zero the kernel gives up, reports it and leaves; the next call
     with the usual limit is right."""
@@ -465,6 +527,9 @@ def test_refusals(gpu):
     odd = torch.empty(n * H + 1, dtype=torch.bfloat16, device="cuda")[1:].view(n, H)
     assert code(B.moe_expert_gated, h, off, odd, None, w13, None, hid) == -1
     assert lib.moe_expert_down(None, *[None] * 7) == -1
+    shifted = torch.empty(1024, dtype=torch.uint8, device="cuda")[2:]  # 2 bytes past 4
+    assert lib.moe_expert_gated(h.ptr, shifted.data_ptr(), x.data_ptr(), None, w13.data_ptr(),
+                                None, hid.data_ptr(), None, None, None) == -1
     assert code(B.moe_combine_backward, B.moe_handle_create(B.make_config(1, n, E, 1, H)), y, y,
                 torch.empty(n, device="cuda"), y, torch.empty(n, device="cuda")) == -5
     out = ctypes.c_void_p()
