@@ -9,7 +9,7 @@
 // are neighbours. S is 8 where there are few groups, so that even one token of
 // a small layer spreads over many SMs, and less where there are many, so that
 // the start and the end of a CTA are paid for by more bytes (down, e4m3, one
-// token of E = 256, top-8, H = 7168, F = 2048: 28.5 us at S = 8).
+// token of E = 256, top-8, H = 7168, F = 2048: 24.3 us at S = 4, 28.5 at 8).
 // A warp's products are mma.sync m16n8 with the weight rows as the 16 and up
 // to eight rows of the segment as the 8: the tensor cores take the bytes as
 // they are loaded (16 per lane, along K; both operands permute k in the same
@@ -296,9 +296,15 @@ cudaError_t launch(const ExpertArgs& p, const void* a, const void* b, int num_sm
     const int c = channels * (kWarps / s);
     return segments * ((p.N + c - 1) / c);
   };
-  // the smallest split that still gives four CTAs per SM
+  // The smallest split that still gives three CTAs per SM (measured against two
+  // and four: 0.985 and 0.981 of the time of four in the mean over 38 calls of
+  // one to four tokens; down e4m3, one token of E = 256, top-8, H = 7168,
+  // F = 2048 24.2 / 24.3 / 26.0 us at four / three / two, gated 55.8 / 44.4 /
+  // 44.2); two where the split's CTAs form clusters, which cost more (E = 64,
+  // H = 2048, F = 1024, top-2: 11.7 / 11.2 / 9.6).
+  const long long enough = (OP == kGated && FP8 ? 2ll : 3ll) * num_sms;
   int s = 1;
-  while (s < 8 && ctas(s) < 4ll * num_sms) s *= 2;
+  while (s < 8 && ctas(s) < enough) s *= 2;
   switch (s) {
     case 1: return launch<OP, FP8, 1>(ctas(1), p, a, b, st);
     case 2: return launch<OP, FP8, 2>(ctas(2), p, a, b, st);
