@@ -10,7 +10,10 @@
 // and writes the scaled pieces to the slot's dy row. The slots of the CTA's
 // next token are loaded beside this one's rows. The k sums are then reduced
 // over the CTA in a fixed order (no atomics: the same inputs give the same
-// bits). Bound by HBM: y in, dy out, dout once.
+// bits). Bound by HBM: y in, dy out, dout once (32768 tokens, top-2, H = 4096:
+// 191 us, 6.75 TB/s, the rate of a copy; with one piece of a row at a time and
+// the slots loaded in the token's turn 227; 1024 tokens, top-8, H = 7168: 42 us,
+// 5.9 TB/s, one wave of CTAs and the launch).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

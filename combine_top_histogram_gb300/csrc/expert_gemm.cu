@@ -17,10 +17,25 @@
 // along the contiguous axis, 128-byte swizzle) with TMA into a ring of stages,
 // one thread issues the tcgen05 products into one of two 256-column TMEM
 // accumulators, and eight warps read the other one back, so a tile's epilogue
-// runs beside the next tile's products.
+// runs beside the next tile's products. Where tiles are few they are 128
+// columns wide. The copy and issue warps run converged, one elected lane
+// executing: as a branch of one lane they kept addresses and descriptors in
+// vector registers and bound the products (gated bf16, E = 8, 65536 rows by
+// Zipf(1.2), H = 4096, F = 1408: 903 us, against 791).
 // With e4m3 operands the products of one 128-channel block are a partial sum
 // that the eight warps multiply by the row's and the block's fp32 scales and
 // add up in registers: the accumulators then alternate per block.
+//
+// What bounds it: of bf16 with many rows the tensor pipe (pairs: 94 % of the
+// SMs' active cycles in kGated and kDx, 82 % in kDw; 1.91 PFLOP/s in that case,
+// 1.66 where passes follow each other for long and the card is at its power
+// cap), without pairs shared memory, whose 128 bytes a cycle serve the copies
+// and the products (96 KB for a block's 512 cycles). Of e4m3 with many rows
+// the way of the accumulators, two of which fill the tensor memory, between
+// the products and the warps that scale them (820 cycles a block, 512 of
+// products; E = 64, 32768 rows, H = 7168, F = 2048: 2.15 PFLOP/s, 1.96 for
+// long). With few rows per expert HBM (E = 256, 8192 rows: 0.99 of the copy
+// rate).
 //
 // Segments end anywhere: rows past a segment's end are computed (they belong
 // to the next expert) and not stored; in kDw, where rows are the reduction
