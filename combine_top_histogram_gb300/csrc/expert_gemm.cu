@@ -13,9 +13,9 @@
 // One persistent CTA per SM. A CTA computes 128 x 256 tiles, or the two CTAs
 // of a cluster compute 256 x 256 tiles together (CG = 2): each holds its 128
 // rows of A and accumulator and half of B's columns, and the first CTA issues
-// the products of both. One thread per CTA copies operand tiles (128 bytes
+// the products of both. One warp per CTA copies operand tiles (128 bytes
 // along the contiguous axis, 128-byte swizzle) with TMA into a ring of stages,
-// one thread issues the tcgen05 products into one of two 256-column TMEM
+// one warp issues the tcgen05 products into one of two 256-column TMEM
 // accumulators, and eight warps read the other one back, so a tile's epilogue
 // runs beside the next tile's products. Where tiles are few they are 128
 // columns wide. The copy and issue warps run converged, one elected lane
@@ -107,7 +107,7 @@ struct Tile {
   int row0;     // this CTA's first row (kDw: first row of the segment)
   int rows;     // rows of the segment from row0 on (kDw: the reduction length)
   int m0;       // kDw: this CTA's first gradient row
-  int n0;       // first output column
+  int n0;       // column tile
   int kb;       // reduction blocks
 };
 
@@ -237,6 +237,13 @@ __device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3) |
          (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3) << 16;
+}
+
+// The larger one; NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 
 // 32 bytes to memory that is 16-byte aligned at least.
@@ -909,14 +916,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 32; ++i) {
             h[2 * i] = silu(acc[i].x) * acc[32 + i].x;
             h[2 * i + 1] = silu(acc[i].y) * acc[32 + i].y;
-            m = fmaxf(m, fmaxf(fabsf(h[2 * i]), fabsf(h[2 * i + 1])));
+            m = max_nan(m, max_nan(fabsf(h[2 * i]), fabsf(h[2 * i + 1])));
           }
           s.amax[parity][half][r] = m;
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&s.pair[quarter]));
           ok = __all_sync(~0u, mbar_wait<kPair>(smem_u32(&s.pair[quarter]), parity, ctl));
           if (!ok) break;
-          m = fmaxf(m, s.amax[parity][half ^ 1][r]);
+          m = max_nan(m, s.amax[parity][half ^ 1][r]);
           parity ^= 1;  // the other buffer next: this one is read until then
           const float scale = __fdiv_rn(m, 448.0f);
           if (mine && half == 0) p.out_scale[((long long)t.row0 + r) * (p.F >> 7) + t.n0] = scale;

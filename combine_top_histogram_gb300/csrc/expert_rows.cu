@@ -219,8 +219,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (mine) static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(v);
       } else {
         out[i] = silu(v) * v1;
-        if constexpr (kQuant) {  // the largest magnitude, NaN left out
-          if (mine) atomicMax(&amax[r], __float_as_int(fmaxf(0.0f, fabsf(out[i]))));
+        if constexpr (kQuant) {  // the largest magnitude, by its bits: NaN is above all
+          if (mine) atomicMax(&amax[r], __float_as_int(fabsf(out[i])));
         } else if (mine) {
           static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(out[i]);
           if (p.gu_out) {

@@ -409,8 +409,8 @@ int moe_combine_tokens(moe_handle_t h, int64_t token_begin, int64_t token_end, c
  * [rows_max, F/128]), the weights one for each 128 x 128 block (w13_scale
  * [E, 2F/128, H/128], w2_scale [E, H/128, F/128]); a value is code * scale.
  * moe_expert_gated then quantises h with the dispatch's rule (s = amax/448,
- * codes e4m3 RNE satfinite of h/s, an all-zero block has s = 0 and zero codes);
- * y is bf16. Sums are fp32; FP8 sums are exact products of codes added up
+ * codes e4m3 RNE satfinite of h/s, an all-zero block has s = 0 and zero codes;
+ * a NaN makes its block's s NaN); y is bf16. Sums are fp32; FP8 sums are exact products of codes added up
  * within each 128-channel block, then scaled and added in fp32.
  * expert_offset is int32 [E+1] on the device: the layout's expert_offset of a
  * compact dispatch (moe_dispatch and its comparators; not the fixed-slot

@@ -320,6 +320,43 @@ def test_special_values_stay_in_their_rows(gpu):
     assert not torch.isfinite(dw2[1]).all()
 
 
+@pytest.mark.parametrize("counts", [[1, 0, 3, 2], [70, 0, 3, 200]])
+def test_special_values_of_e4m3_rows(gpu, counts):
+    """A NaN or an infinite scale of one row shows in that row's scales and results, and
+    in no other's; few rows and many."""
+    H, F, E, n = 256, 384, len(counts), sum(counts)
+    x, xs = quant_rows(normal(n, H))
+    xs[0, 1] = float("nan")  # the whole row's sums
+    x[2, 3] = 0x7F           # one NaN code
+    xs[n - 1, 0] = float("inf")
+    w13, ws = quant_weights(normal(E, 2 * F, H, std=H ** -0.5, seed=1))
+    w2, ws2 = quant_weights(normal(E, H, F, std=F ** -0.5, seed=2))
+    hid, hs = poisoned(n, F, dtype=torch.uint8), poisoned(n, F // 128, dtype=torch.float32)
+    y = poisoned(n, H)
+    h = B.moe_expert_create(B.make_expert_config(E, H, F, n, B.MOE_FP8_E4M3))
+    B.moe_expert_gated(h, offsets(counts), x, xs, w13, ws, hid, hs)
+    B.moe_expert_down(h, offsets(counts), hid, hs, w2, ws2, y)
+    bad = torch.zeros(n, dtype=torch.bool, device="cuda")
+    bad[[0, 2, n - 1]] = True
+    assert torch.isfinite(hs[~bad]).all() and torch.isfinite(y[~bad]).all()
+    assert not torch.isfinite(hs[bad]).any() and not torch.isfinite(y[bad]).any()
+
+
+@pytest.mark.parametrize("counts", [[1, 0, 3, 2], [70, 0, 3, 200]])
+def test_special_values_of_few_and_many_rows(gpu, counts):
+    H, F, E, n = 264, 136, len(counts), sum(counts)
+    x, w13 = normal(n, H), normal(E, 2 * F, H, std=H ** -0.5, seed=1)
+    w2 = normal(E, H, F, std=F ** -0.5, seed=2)
+    x[1, 5], x[n - 1, 0] = float("nan"), float("-inf")
+    hid, y = poisoned(n, F), poisoned(n, H)
+    h = B.moe_expert_create(B.make_expert_config(E, H, F, n))
+    B.moe_expert_gated(h, offsets(counts), x, None, w13, None, hid)
+    B.moe_expert_down(h, offsets(counts), hid, None, w2, None, y)
+    bad = torch.zeros(n, dtype=torch.bool, device="cuda")
+    bad[[1, n - 1]] = True
+    assert torch.isfinite(y[~bad]).all() and not torch.isfinite(y[bad]).any()
+
+
 def test_large_gates_saturate(gpu):
     """Gates of +-200 and +-3e38: the sigmoid is 0 or 1, never NaN for finite products."""
     H, F = 8, 8
@@ -446,6 +483,37 @@ def test_waits_that_run_out_set_the_status(gpu):
     both, err = R.rows_times(x.double(), w13.double(), counts)
     v, e = R.silu_product(both[:, :F], both[:, F:], err[:, :F], err[:, F:])
     R.check("hid", hid, *R.bf16_out(v, e))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+def test_few_rows_in_a_graph(gpu, dtype):
+    """The single-token kernels (of e4m3 a cluster launch) in a captured graph."""
+    counts, H, F = FP8_CASES["token_top8"]
+    E, n = len(counts), sum(counts)
+    off, x, fp8 = offsets(counts), normal(n, H), dtype == "fp8"
+    w13, w2 = normal(E, 2 * F, H, std=H ** -0.5, seed=1), normal(E, H, F, std=F ** -0.5, seed=2)
+    xs = s13 = s2 = hs = None
+    hid = poisoned(n, F)
+    if fp8:
+        (x, xs), (w13, s13), (w2, s2) = quant_rows(x), quant_weights(w13), quant_weights(w2)
+        hid, hs = poisoned(n, F, dtype=torch.uint8), poisoned(n, F // 128, dtype=torch.float32)
+    y = poisoned(n, H)
+    h = B.moe_expert_create(B.make_expert_config(E, H, F, n, int(fp8)))
+
+    def run():
+        B.moe_expert_gated(h, off, x, xs, w13, s13, hid, hs)
+        B.moe_expert_down(h, off, hid, hs, w2, s2, y)
+
+    run()
+    torch.cuda.synchronize()
+    first = hid.clone(), y.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    hid.zero_(), y.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(hid, first[0]) and torch.equal(y, first[1])
 
 
 def test_same_inputs_same_bits_on_another_stream_and_in_a_graph(gpu):
