@@ -82,13 +82,13 @@ struct Shared {
   uint64_t tfull[2], tempty[2], drain;
   uint64_t tail[kMaxStages];           // kDw, second CTA: its copies of a segment's last block
   uint32_t tmem;
-  int abort;
+  int abort, uneven;
   uint64_t pair[4];                    // the two warps of a lane quarter exchange amax
   float amax[2][2][kTileM];            // [tile parity][half][row]
   uint64_t sempty[2];                  // the epilogue has read scale[i]
   float2 scale[2][kTileM];             // FP8: row scale x scales of the tile's two weight blocks
   int off[MOE_MAX_EXPERTS + 1];
-  int pre[MOE_MAX_EXPERTS + 1];        // row tiles before expert e
+  int pre[MOE_MAX_EXPERTS + 1];        // row tiles before expert e (kDw: see sort_segments)
 };
 
 template <int OP, bool FP8, int CG, int TN>
@@ -116,19 +116,31 @@ struct Tile {
 // columns together, so that concurrent CTAs share both operands in L2. Each
 // role walks for itself; a step costs two divisions and, within an expert or
 // to one of the next few, no search.
+// kDw's tiles take as long as their expert has rows. Where some have many more
+// than others, the experts come by falling rows (sort_segments) and every
+// second step goes backwards over the CTAs, so that those with the long tiles
+// of one step get the short ones of the next (Zipf(1.2) over 8 experts, 76
+// pairs: the last pair ends 7 and 6 % after the mean for dW2 and dW13 of the
+// skewed training layer, without 17 and 8 %; its backward pass 2640 / 2570 us).
+// Even ones keep the plain order, which costs less to walk (E = 64 of 256 rows
+// each: 464 / 480 us).
 template <int OP, int CG>
 struct Walk {
   static constexpr int kRows = kTileM * CG;
   const ExpertArgs& p;
   const Shared& s;
-  const int k_elems, rank, step, mt_w;
+  const int k_elems, rank, first, step, mt_w;
   int t, e, base, per;  // tile, its expert, the expert's first tile and tiles
+  int place = 0;        // kDw: the expert's place by falling rows
+  bool uneven, back = true;  // kDw: some experts' rows are many more; this step goes backwards
 
   __device__ __forceinline__ Walk(const ExpertArgs& pa, const Shared& sh, int ke, int rk, int tile0,
                                   int st)
-      : p(pa), s(sh), k_elems(ke), rank(rk), step(st),
+      : p(pa), s(sh), k_elems(ke), rank(rk), first(tile0), step(st),
         mt_w(OP == kDw ? (pa.M + kRows - 1) / kRows : 0), t(tile0 - st), e(0), base(0) {
     per = tiles(0);
+    uneven = OP == kDw && sh.uneven;
+    if (uneven) e = sh.pre[0];
   }
 
   __device__ __forceinline__ int tiles(int x) const {
@@ -137,13 +149,22 @@ struct Walk {
 
   __device__ __forceinline__ bool next(Tile& o) {
     t += step;
-    if (t >= (OP == kDw ? mt_w * p.E : s.pre[p.E]) * p.nt) return false;
+    uint32_t local;  // tile of the expert
     if (OP == kDw) {
-      if (t - base >= per) {
-        e = t / per;
-        base = e * per;
+      int at = t;
+      if (uneven) {
+        back = !back;
+        if (back) at += step - 1 - 2 * first;
       }
+      if (at >= mt_w * p.E * p.nt) return false;
+      if (at < base || at - base >= per) {
+        place = at / per;
+        base = place * per;
+        e = uneven ? s.pre[place] : place;
+      }
+      local = at - base;
     } else {
+      if (t >= s.pre[p.E] * p.nt) return false;
       for (int i = 0; i < 4 && t - base >= per; ++i) {
         base += per;
         per = tiles(++e);
@@ -159,9 +180,10 @@ struct Walk {
         base = s.pre[e] * p.nt;
         per = tiles(e);
       }
+      local = t - base;
     }
     const int mt = OP == kDw ? mt_w : s.pre[e + 1] - s.pre[e];
-    const uint32_t local = t - base, group = kGroupM * p.nt;
+    const uint32_t group = kGroupM * p.nt;
     const uint32_t g = local / group, idx = local - g * group;
     const uint32_t gs = min(kGroupM, mt - (int)g * kGroupM);
     const uint32_t n = gs == kGroupM ? idx / kGroupM : idx / gs;
@@ -225,6 +247,29 @@ __device__ __forceinline__ void load_segments(const ExpertArgs& p, Shared& s) {
     if (lane == 0) s.pre[p.E] = carry;
   }
   __syncthreads();
+}
+
+// kDw: whether some expert has more than 1.5 times the mean of the rows, among
+// up to 256 experts (of more, one expert's tiles weigh little) of more than two
+// blocks each on average; then the experts by falling rows, equal ones by their
+// number, in pre.
+__device__ __forceinline__ void sort_segments(const ExpertArgs& p, Shared& s) {
+  const long long total = s.off[p.E] - s.off[0];
+  int most = 0;
+  for (int e = threadIdx.x; e < p.E; e += kThreads) most = max(most, s.off[e + 1] - s.off[e]);
+  const bool uneven = __syncthreads_or(p.E <= 256 && total > 128ll * p.E &&
+                                       2ll * most * p.E > 3 * total);
+  if (threadIdx.x == 0) s.uneven = uneven;
+  if (!uneven) return;
+  for (int e = threadIdx.x; e < p.E; e += kThreads) {
+    const int n = s.off[e + 1] - s.off[e];
+    int place = 0;
+    for (int i = 0; i < p.E; ++i) {
+      const int m = s.off[i + 1] - s.off[i];
+      place += m > n || (m == n && i < e);
+    }
+    s.pre[place] = e;
+  }
 }
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
@@ -668,6 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_wait();  // the segments and the operands come from earlier kernels
   load_segments<CG>(p, s);
+  if constexpr (OP == kDw) sort_segments(p, s);
   tc_fence_before();
   if constexpr (kPair) cluster_sync();  // both CTAs' barriers exist
   else __syncthreads();

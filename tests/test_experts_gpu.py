@@ -602,3 +602,20 @@ def test_refusals(gpu):
                 torch.empty(n, device="cuda"), y, torch.empty(n, device="cuda")) == -5
     out = ctypes.c_void_p()
     assert lib.moe_expert_create(None, None, 0, ctypes.byref(out)) == -1
+
+
+@pytest.mark.parametrize("counts", [[3, 900, 0, 40, 130, 5], [700, 0, 0, 0, 3, 900, 64, 1]])
+def test_backward_of_uneven_experts(gpu, counts):
+    """Weight gradients where few experts have most rows: their tiles are walked in another
+    order."""
+    H, F = 1032, 776
+    E, n = len(counts), sum(counts)
+    t = backward_inputs(counts, H, F, n)
+    dx, dw13, dw2 = poisoned(n, H), poisoned(E, 2 * F, H), poisoned(E, H, F)
+    h = B.moe_expert_create(B.make_expert_config(E, H, F, n, train=True))
+    B.moe_expert_backward(h, offsets(counts), t["x"], t["gu"], t["hid"], t["dy"], t["w13"],
+                          t["w2"], dx, dw13, dw2)
+    assert B.moe_expert_read_status(h) == 0
+    want = R.backward(*(t[k].double() for k in ("x", "gu", "hid", "dy", "w13", "w2")), counts)
+    for name, got, ref in (("dx", dx, want[0]), ("dw13", dw13, want[1]), ("dw2", dw2, want[2])):
+        R.check(name, got, *ref)
