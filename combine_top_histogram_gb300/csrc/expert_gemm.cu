@@ -334,7 +334,8 @@ __device__ __forceinline__ void tile_store(const uint4* buf, int lane, uint8_t* 
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = i * 8 + (lane >> 2), u = lane & 3;
-    if (r < rows && u < units) *reinterpret_cast<uint4*>(out + r * pitch + u * 16) = buf[unit_at(r, u)];
+    if (r < rows && u < units)
+      *reinterpret_cast<uint4*>(out + r * pitch + u * 16) = buf[unit_at(r, u)];
   }
 }
 
@@ -443,7 +444,8 @@ __device__ __forceinline__ void epilogue_bf16(const ExpertArgs& p, const Tile& t
       uint32_t g[16], u[16], d[32];
       tile_turn(buf, lane, pre.g, g);
       tile_turn(buf, lane, pre.u, u);
-      if (j < TN / 64 - 1) gate_fetch<TN>(pre, p, t, half, quarter, lane, j + 1);  // beside this part's work
+      if (j < TN / 64 - 1)  // beside this part's work
+        gate_fetch<TN>(pre, p, t, half, quarter, lane, j + 1);
       tc_ld32(d, taddr + at);
       tc_wait_ld();
       tc_loaded(d);
@@ -870,8 +872,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after();
         }
-        epilogue_bf16<OP, TN>(p, t, tmem + lanes + as * kAccColumns, half, quarter, lane, buf, t.kb == 0,
-                          pre, map_c);
+        epilogue_bf16<OP, TN>(p, t, tmem + lanes + as * kAccColumns, half, quarter, lane, buf,
+                              t.kb == 0, pre, map_c);
         if (t.kb > 0) {
           tc_fence_before();
           __syncwarp();
@@ -923,9 +925,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         const long long row = (long long)t.row0 + quarter * 32;
         if constexpr (OP == kDown) {
-          // (Stored by the lanes themselves, 32 rows at a time, a tile's 64 KB
-          // take about 5500 cycles in which the products wait for the
-          // registers; the few warps with a segment's end still do so.)
+          // To the copy engine: stored by the lanes themselves, 32 rows at a time, a
+          // tile's 64 KB take about 5500 cycles in which the products wait for the
+          // registers. The few warps with a segment's end still store so.
           const int col = t.n0 * TN + half * 128;
           const int left = t.rows - quarter * 32;
           if (col < p.N && left >= 32) {
@@ -1017,8 +1019,8 @@ EncodeTiled encode_tiled() {
   static const EncodeTiled fn = [] {
     void* f = nullptr;
     cudaDriverEntryPointQueryResult r;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) !=
-            cudaSuccess ||
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &r) != cudaSuccess ||
         r != cudaDriverEntryPointSuccess)
       f = nullptr;
     return reinterpret_cast<EncodeTiled>(f);

@@ -197,6 +197,8 @@ class MoeLayer:
         if self.experts is not None:
             if self.fixed:
                 raise ValueError("experts run over the compact receive rows, not fixed slots")
+            if expert_scale is not None:
+                raise ValueError("expert_scale belongs to the stand-in")
             self.experts.forward(self.layout_view()["expert_offset"], self.recv_x,
                                  self.recv_scale, self.y, stream)
             return
@@ -330,4 +332,6 @@ class MoeLayer:
         return B.moe_read_status(self.handle, stream)
 
     def close(self):
+        if self.experts is not None:
+            self.experts.close()
         self.handle.close()

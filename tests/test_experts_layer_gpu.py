@@ -123,6 +123,8 @@ def test_layer_refusals(gpu):
         layer.forward_pipelined(x, ids=ids, w=w)
     with pytest.raises(ValueError):
         layer.backward(x, w)
+    with pytest.raises(ValueError):
+        layer.forward(x, ids=ids, w=w, expert_scale=torch.ones(4, device="cuda"))
     layer.set_experts(None, None)  # the stand-in again
     layer.forward(x, ids=ids, w=w, fixed_slots=True)
 
