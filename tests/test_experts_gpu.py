@@ -289,6 +289,12 @@ def test_combine_backward(gpu, shape, fixed):
     assert untouched(dy[~used])
 
 
+@pytest.mark.parametrize("k", [1, 2, 4, 8])
+@pytest.mark.parametrize("tokens,H", [(304, 1032), (305, 1032), (7, 4104), (304, 1024)])
+def test_combine_backward_of_few_and_wide_tokens(gpu, k, tokens, H):
+    test_combine_backward(gpu, (1, tokens, 16, k, H, 0), False)
+
+
 def test_special_values_stay_in_their_rows(gpu):
     """An infinity or NaN of one row or one weight reaches only the results it enters."""
     counts, H, F = [3, 140, 2], 192, 136
