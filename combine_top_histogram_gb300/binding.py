@@ -244,6 +244,8 @@ class Handle:
     def __init__(self, cfg: moe_config_t, workspace):
         self.cfg = cfg
         self.workspace = workspace
+        #: rows that the last dispatch's inv can name (the receive rows, or the fixed slots)
+        self.recv_rows = self.rows = moe_recv_rows_max(cfg)
         h = _c_void_p()
         _check("moe_handle_create", load_library().moe_handle_create(
             ctypes.byref(cfg), _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -303,6 +305,7 @@ def moe_dispatch_fixed_slots(h: Handle, x, w, slot_x, slot_scale, meta: dict, st
     _check("moe_dispatch_fixed_slots", load_library().moe_dispatch_fixed_slots(
         h.ptr, _ptr(x), _ptr(w), _ptr(slot_x), _ptr(slot_scale), ctypes.byref(m),
         _stream(stream)))
+    h.rows = moe_fixed_slot_rows(h.cfg)
 
 
 def moe_layout_tables(h: Handle, stream=None) -> None:
@@ -340,6 +343,7 @@ def moe_dispatch(h: Handle, x, w, recv_x, recv_scale, meta: dict, stream=None) -
     _check("moe_dispatch", load_library().moe_dispatch(
         h.ptr, _ptr(x), _ptr(w), _ptr(recv_x), _ptr(recv_scale), ctypes.byref(m),
         _stream(stream)))
+    h.rows = h.recv_rows
 
 
 def moe_dispatch_two_stage(h: Handle, x, w, send_x, send_scale, recv_x, recv_scale, meta: dict,
@@ -349,6 +353,7 @@ def moe_dispatch_two_stage(h: Handle, x, w, send_x, send_scale, recv_x, recv_sca
     _check("moe_dispatch_two_stage", load_library().moe_dispatch_two_stage(
         h.ptr, _ptr(x), _ptr(w), _ptr(send_x), _ptr(send_scale), _ptr(recv_x), _ptr(recv_scale),
         ctypes.byref(m), _stream(stream)))
+    h.rows = h.recv_rows
 
 
 def moe_layout_dispatch_fused(h: Handle, logits, ids, w, x, recv_x, recv_scale, meta: dict,
@@ -359,6 +364,7 @@ def moe_layout_dispatch_fused(h: Handle, logits, ids, w, x, recv_x, recv_scale, 
     _check("moe_layout_dispatch_fused", load_library().moe_layout_dispatch_fused(
         h.ptr, _ptr(logits), _ptr(ids), _ptr(w), _ptr(x), _ptr(recv_x), _ptr(recv_scale),
         ctypes.byref(m), _stream(stream)))
+    h.rows = h.recv_rows
 
 
 def moe_set_wait_limit(h: Handle, polls: int) -> None:
@@ -372,6 +378,7 @@ def moe_dispatch_tokens(h: Handle, begin: int, end: int, x, w, recv_x, recv_scal
     _check("moe_dispatch_tokens", load_library().moe_dispatch_tokens(
         h.ptr, int(begin), int(end), _ptr(x), _ptr(w), _ptr(recv_x), _ptr(recv_scale),
         ctypes.byref(m), _stream(stream)))
+    h.rows = h.recv_rows
 
 
 def moe_expert_standin_tokens(h: Handle, begin: int, end: int, recv_x, recv_scale, expert_scale,
@@ -393,6 +400,7 @@ def moe_dispatch_allgather(h: Handle, x, w, gathered_x, gathered_scale, recv_x, 
     _check("moe_dispatch_allgather", load_library().moe_dispatch_allgather(
         h.ptr, _ptr(x), _ptr(w), _ptr(gathered_x), _ptr(gathered_scale), _ptr(recv_x),
         _ptr(recv_scale), ctypes.byref(m), _stream(stream)))
+    h.rows = h.recv_rows
 
 
 def moe_expert_standin(h: Handle, recv_x, recv_scale, expert_scale, y, stream=None) -> None:
@@ -418,12 +426,14 @@ def _buf(name: str, t, count: int, size: int, optional: bool = False) -> Optiona
 
 
 def moe_combine_backward(h: Handle, dout, y, w, dy, dw, stream=None) -> None:
-    """Gradients of moe_combine on the last dispatch's layout (see the header)."""
+    """Gradients of moe_combine on the last dispatch's layout (see the header); y and dy hold
+    every row that it can name."""
     c = h.cfg
-    T = c.num_ranks * c.tokens_per_rank
+    T, rows_h = c.num_ranks * c.tokens_per_rank, h.rows * c.hidden
     _check("moe_combine_backward", load_library().moe_combine_backward(
-        h.ptr, _buf("dout", dout, T * c.hidden, 2), _ptr(y), _buf("w", w, T * c.top_k, 4),
-        _buf("dy", dy, y.numel(), 2), _buf("dw", dw, T * c.top_k, 4), _stream(stream)))
+        h.ptr, _buf("dout", dout, T * c.hidden, 2), _buf("y", y, rows_h, 2),
+        _buf("w", w, T * c.top_k, 4), _buf("dy", dy, rows_h, 2),
+        _buf("dw", dw, T * c.top_k, 4), _stream(stream)))
 
 
 def make_expert_config(E: int, H: int, F: int, rows_max: int, dtype: int = MOE_BF16,

@@ -220,6 +220,8 @@ class MoeLayer:
         import torch
         if self.experts is None or not self.experts.train:
             raise ValueError("backward needs experts built for training (set_experts)")
+        if self.fixed:  # inv names fixed slots, which y and recv_x do not hold
+            raise ValueError("backward follows a compact dispatch, not fixed slots")
         if self.grads is None:
             dev = self.out.device
             self.grads = {"dy": torch.empty_like(self.y), "dx_rows": torch.empty_like(self.recv_x),
@@ -237,6 +239,8 @@ class MoeLayer:
                 two_stage=False, fused=False, allgather=False, fixed_slots=False):
         """Whole layer; with logits the routed ids/weights land in self.ids / self.w.
         two_stage=True dispatches through the two-stage comparator."""
+        if fixed_slots and not fused and self.experts is not None:
+            raise ValueError("experts run over the compact receive rows, not fixed slots")
         if fused:
             self.layout_dispatch_fused(x, ids, w, logits, stream)
             if logits is not None:
