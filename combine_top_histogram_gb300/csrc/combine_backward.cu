@@ -63,7 +63,13 @@ __global__ void __launch_bounds__(kThreads) k_combine_backward(const CombineBack
     int* rows_s = rows_buf[par];
     float* w_s = w_buf[par];
     if (tid < p.k) {
-      rows_s[tid] = (row_next >= 0 && row_ok(row_next, p.rows, p.status)) ? row_next : -1;
+      // A row past the buffers (tokens that a chunked dispatch has left out keep the
+      // rows of an earlier layout) is reported and taken as no slot, in every build.
+      if (row_next >= p.rows) {
+        atomicOr(p.status, MOE_STATUS_BOUNDS);
+        row_next = -1;
+      }
+      rows_s[tid] = row_next >= 0 ? row_next : -1;
       w_s[tid] = w_next;
     }
     __syncthreads();

@@ -194,7 +194,7 @@ struct CombineBackwardArgs {
   long long T;
   long long rows;         // rows of y and dy
   int k, H;
-  uint32_t* status;       // MOE_STATUS_BOUNDS (debug bounds checks)
+  uint32_t* status;       // MOE_STATUS_BOUNDS
 };
 
 struct StandinArgs {

@@ -92,9 +92,10 @@ extern "C" {
 #define MOE_STATUS_SLOT_OVERFLOW 0x4u  /* fixed slots: more than T_r assignments of one
                                           source to one expert (an id repeated within a
                                           token); the excess is not written, inv = -1 */
-#define MOE_STATUS_BOUNDS 0x8u         /* debug bounds build only (moe_debug_bounds()):
-                                          a computed row index fell outside its buffer;
-                                          that access was skipped (and inv = -1) */
+#define MOE_STATUS_BOUNDS 0x8u         /* debug bounds build (moe_debug_bounds()), and
+                                          moe_combine_backward in every build: a row
+                                          index fell outside its buffer; that access was
+                                          skipped (and, where computed, inv = -1) */
 
 /* Problem description. Passed by pointer; copied into the handle. */
 typedef struct {
@@ -485,7 +486,10 @@ int moe_expert_read_status(moe_expert_t x, uint32_t *flags, void *stream);
  * with inv[g*k+j] >= 0, dy[inv[g*k+j]] = bf16(w[g,j] * dout[g]) and
  * dw[g,j] = sum_c dout[g,c] * y[inv[g*k+j],c] (fp32); masked and dropped slots
  * get dw = 0. dout: bf16 [T, H]; y, dy: bf16 rows as moe_combine's y (both
- * layouts); w, dw: fp32 [T, k]. Rows that no slot names are not written. (The
+ * layouts); w, dw: fp32 [T, k]. Rows that no slot names are not written. A slot
+ * whose inv lies past these rows (a token that moe_dispatch_tokens has not
+ * covered since a fixed-slot dispatch) is taken as masked and sets
+ * MOE_STATUS_BOUNDS. (The
  * gradient of a bf16 dispatch is moe_combine with unit weights.)
  * Errors: INVALID_ARG, STATE, CUDA. */
 int moe_combine_backward(moe_handle_t h, const void *dout, const void *y, const float *w, void *dy,

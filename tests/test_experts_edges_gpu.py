@@ -1,0 +1,37 @@
+"""The expert operators at the edges of their contracts: states of a layer that a call
+order leaves behind, descending offsets, other streams, ties of e4m3 codes, waits that run
+out in pairs of CTAs; and the kernel forms that only larger or uneven calls reach."""
+import pytest
+import torch
+
+import expert_reference as R
+from combine_top_histogram_gb300 import binding as B
+from test_experts_gpu import normal, poisoned, untouched
+
+pytestmark = pytest.mark.gpu
+
+
+def test_combine_backward_after_a_partial_dispatch(gpu):
+    """Tokens that a chunked dispatch has not covered since a fixed-slot one still name slot
+    rows: those past the receive rows are reported and touch nothing."""
+    from combine_top_histogram_gb300 import MoeLayer
+    P, Tr, E, k, H = 1, 64, 16, 2, 136
+    g = torch.Generator(device="cuda").manual_seed(3)
+    ids = torch.rand(Tr, E, device="cuda", generator=g).topk(k, 1).indices.to(torch.int32)
+    w = torch.softmax(torch.randn(Tr, k, device="cuda", generator=g), 1)
+    layer, x = MoeLayer(P, Tr, E, k, H), normal(Tr, H)
+    layer.layout(ids)
+    layer.dispatch_fixed_slots(x, w)
+    B.moe_dispatch_tokens(layer.handle, 0, Tr // 2, x, w, layer.recv_x, None, layer.meta)
+    inv = layer.layout_view()["inv"].view(Tr, k).long().clone()
+    past = inv >= layer.rows
+    assert past[Tr // 2:].any() and not past[:Tr // 2].any()
+    y, dout = normal(layer.rows, H, seed=1), normal(Tr, H, seed=2)
+    whole = poisoned(B.moe_fixed_slot_rows(layer.cfg), H)  # room for every row inv names
+    dy, dw = whole[:layer.rows], poisoned(Tr, k, dtype=torch.float32)
+    B.moe_combine_backward(layer.handle, dout, y, w, dy, dw)
+    assert layer.status() == B.MOE_STATUS_BOUNDS and layer.status() == 0
+    assert untouched(whole[layer.rows:]) and not dw[past].any()
+    first = inv[:Tr // 2]
+    prod = y[first].double() * dout[:Tr // 2].double()[:, None, :]
+    R.check("dw", dw[:Tr // 2], prod.sum(2), prod.abs().sum(2) * (H + 8) * 2.0 ** -23)
