@@ -103,18 +103,32 @@ class MoeLayer:
         self.slots = None  # fixed-slot buffers, allocated on first use
         self.fixed = False  # the last dispatch wrote the fixed-slot layout
         self.experts = None  # an ExpertBlock in the stand-in's place
-        self.grads = None    # backward's buffers, allocated on first use
+        self.grads = None    # backward's buffers, of experts built for training
 
     def set_experts(self, w13, w2, w13_scale=None, w2_scale=None, train: bool = False):
         """Gated feed-forward experts in the stand-in's place (None: the stand-in again).
-        Their type is the dispatch's: bf16, or e4m3 codes with 128 x 128 block scales."""
+        Their type is the dispatch's: bf16, or e4m3 codes with 128 x 128 block scales.
+        Allocates what forward and backward need and waits for the device, so that both can
+        follow on any stream and the former experts' buffers are free. Outside stream capture."""
+        import torch
         if w13 is None:
-            self.experts = None
+            if self.experts is not None:
+                torch.cuda.synchronize(self.out.device)
+            self.experts = self.grads = None
             return None
         experts = ExpertBlock(w13, w2, self.rows, w13_scale, w2_scale, train)
         if (experts.E, experts.H, experts.fp8) != (self.E, self.H, self.fp8):
             raise ValueError("the experts' number, width and type are those of the layer")
-        self.experts = experts
+        grads = None
+        if train:
+            dev = self.out.device
+            grads = {"dy": torch.empty_like(self.y), "dx_rows": torch.empty_like(self.recv_x),
+                     "dw": torch.empty((self.T, self.k), dtype=torch.float32, device=dev),
+                     "dx": torch.empty_like(self.out),
+                     "ones": torch.ones((self.T, self.k), dtype=torch.float32, device=dev)}
+        # the ones are filled, and whatever used the new buffers' memory is done with it
+        torch.cuda.synchronize(self.out.device)
+        self.experts, self.grads = experts, grads
         return experts
 
     # -- steps ---------------------------------------------------------------
@@ -217,17 +231,10 @@ class MoeLayer:
         dout [T, H], with the w [T, k] it combined with: dx [T, H], dw [T, k], and the
         experts' dw13 and dw2. Combine backward, the experts' backward, and the dispatch's:
         the gradients of a token's k rows added up, which is a combine with unit weights."""
-        import torch
         if self.experts is None or not self.experts.train:
             raise ValueError("backward needs experts built for training (set_experts)")
         if self.fixed:  # inv names fixed slots, which y and recv_x do not hold
             raise ValueError("backward follows a compact dispatch, not fixed slots")
-        if self.grads is None:
-            dev = self.out.device
-            self.grads = {"dy": torch.empty_like(self.y), "dx_rows": torch.empty_like(self.recv_x),
-                          "dw": torch.empty((self.T, self.k), dtype=torch.float32, device=dev),
-                          "dx": torch.empty_like(self.out),
-                          "ones": torch.ones((self.T, self.k), dtype=torch.float32, device=dev)}
         g = self.grads
         B.moe_combine_backward(self.handle, dout, self.y, w, g["dy"], g["dw"], stream)
         self.experts.backward(self.layout_view()["expert_offset"], self.recv_x, g["dy"],

@@ -35,3 +35,47 @@ def test_combine_backward_after_a_partial_dispatch(gpu):
     first = inv[:Tr // 2]
     prod = y[first].double() * dout[:Tr // 2].double()[:, None, :]
     R.check("dw", dw[:Tr // 2], prod.sum(2), prod.abs().sum(2) * (H + 8) * 2.0 ** -23)
+
+
+def busy(ms=100):
+    """Work on the current stream that takes about so long."""
+    a = torch.zeros(8192, 8192, dtype=torch.bfloat16, device="cuda")
+    out = torch.empty_like(a)
+    for _ in range(ms):  # 0.6 to 0.8 ms each
+        torch.matmul(a, a, out=out)
+        torch.matmul(a, a, out=out)
+
+
+def test_layer_on_a_side_stream_beside_a_busy_one(gpu):
+    """The first forward and backward of a training layer on a stream of its own, while the
+    current stream has work queued, give what they give on the current stream."""
+    from combine_top_histogram_gb300 import MoeLayer
+    P, Tr, E, k, H, F = 2, 37, 8, 2, 264, 72
+    w13, w2 = normal(E, 2 * F, H, std=H ** -0.5, seed=1), normal(E, H, F, std=F ** -0.5, seed=2)
+    x, dout = normal(P * Tr, H), normal(P * Tr, H, std=0.1, seed=4)
+    g = torch.Generator(device="cuda").manual_seed(0)
+    ids = torch.rand(P * Tr, E, device="cuda", generator=g).topk(k, 1).indices.to(torch.int32)
+    w = torch.softmax(torch.randn(P * Tr, k, device="cuda", generator=g), 1)
+
+    def step(stream=None):
+        layer = MoeLayer(P, Tr, E, k, H)
+        busy(1)
+        layer.set_experts(w13, w2, train=True)
+        side = stream is not None
+        if side:
+            busy()
+        out = layer.forward(x, ids=ids, w=w, stream=stream)
+        grad = layer.backward(dout, w, stream=stream)
+        if side:
+            stream.synchronize()
+            assert not torch.cuda.current_stream().query()  # it was busy all the while
+        return layer, [out, *(grad[n] for n in ("dx", "dw", "dw13", "dw2"))]
+
+    keep, want = step()
+    torch.cuda.synchronize()
+    other, got = step(torch.cuda.Stream())
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert keep.status() == other.status() == 0
+    assert keep.experts.status() == other.experts.status() == 0

@@ -48,8 +48,7 @@ def recorder(cuda_lib, monkeypatch):
     monkeypatch.setattr(B, "load_library", lambda: rec)
     monkeypatch.setattr(B, "_ptr", lambda t: None if t is None else t.data_ptr())
     monkeypatch.setattr(B, "_stream", lambda stream: 0)
-    monkeypatch.setattr(torch.cuda, "current_stream",
-                        lambda *a: type("Stream", (), {"synchronize": lambda self: None})())
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda device=None: None)
     return rec
 
 
@@ -102,3 +101,12 @@ def test_combine_backward_wants_every_row_of_the_last_dispatch(recorder, fixed, 
     t[short] = bf16(layer.rows, layer.H)
     B.moe_combine_backward(*args())
     assert recorder.calls[-1] == "moe_combine_backward"
+
+
+def test_backward_allocates_nothing(recorder, monkeypatch):
+    """Buffers made in a backward on another stream would be filled on the current one."""
+    layer, x, ids, w = layer_for_training()
+    layer.forward(x, ids=ids, w=w)
+    for name in ("ones", "empty", "empty_like", "zeros"):
+        monkeypatch.setattr(torch, name, lambda *a, **k: pytest.fail("allocated"))
+    layer.backward(x, w, stream=1)
