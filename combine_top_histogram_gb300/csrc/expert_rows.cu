@@ -61,7 +61,9 @@ __device__ __forceinline__ uint4 stream_if(const uint8_t* p, bool ok) {
 }
 
 // The a-th expert that has rows, its first row and its rows; n = 0 if there
-// are not so many. Whole CTA.
+// are not so many. Whole CTA. Segments are those of the tile kernels: offsets
+// held to [0, rows_max], ends to ascending order. Where some end descends (the
+// caller's own offsets; a layout's never do) one thread walks them again.
 struct Segment {
   int e, row0, n;
 };
@@ -71,16 +73,18 @@ __device__ __forceinline__ Segment find_segment(const ExpertArgs& p, int a) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int kPer = MOE_MAX_EXPERTS / kThreads;
   const int per = (p.E + kThreads - 1) / kThreads;  // <= kPer
+  const auto offset = [&](int e) { return min(max(__ldg(p.offset + e), 0), (int)p.rows_max); };
   int lo[kPer], n[kPer], count = 0;
+  bool descends = false;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int e = tid * per + i;
     lo[i] = n[i] = 0;
     if (i < per && e < p.E) {
-      const int most = (int)p.rows_max;
-      lo[i] = min(max(__ldg(p.offset + e), 0), most);
-      n[i] = max(min(max(__ldg(p.offset + e + 1), 0), most) - lo[i], 0);
+      lo[i] = offset(e);
+      n[i] = offset(e + 1) - lo[i];
     }
+    descends |= n[i] < 0;
     count += n[i] > 0;
   }
   int sum = count;
@@ -90,14 +94,24 @@ __device__ __forceinline__ Segment find_segment(const ExpertArgs& p, int a) {
   }
   if (lane == 31) warp_count[warp] = sum;
   if (tid == 0) found = Segment{0, 0, 0};
-  __syncthreads();
-  int before = sum - count;
-  for (int w = 0; w < warp; ++w) before += warp_count[w];
+  if (__syncthreads_or(descends)) {
+    if (tid == 0) {
+      int top = offset(0), before = 0;
+      for (int e = 0; e < p.E; ++e) {
+        const int end = max(offset(e + 1), top);
+        if (end > top && before++ == a) found = Segment{e, top, end - top};
+        top = end;
+      }
+    }
+  } else {
+    int before = sum - count;
+    for (int w = 0; w < warp; ++w) before += warp_count[w];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    if (n[i] > 0) {
-      if (before == a) found = Segment{tid * per + i, lo[i], n[i]};
-      ++before;
+    for (int i = 0; i < kPer; ++i) {
+      if (n[i] > 0) {
+        if (before == a) found = Segment{tid * per + i, lo[i], n[i]};
+        ++before;
+      }
     }
   }
   __syncthreads();

@@ -6,7 +6,7 @@ import torch
 
 import expert_reference as R
 from combine_top_histogram_gb300 import binding as B
-from test_experts_gpu import normal, poisoned, untouched
+from test_experts_gpu import normal, poisoned, quant_rows, quant_weights, untouched
 
 pytestmark = pytest.mark.gpu
 
@@ -79,3 +79,46 @@ def test_layer_on_a_side_stream_beside_a_busy_one(gpu):
         assert torch.equal(a, b)
     assert keep.status() == other.status() == 0
     assert keep.experts.status() == other.experts.status() == 0
+
+
+DESCENDING = [[0, 6, 2, 8], [0, 1 << 30, 3, 7], [-5, 4, -1, 8], [0, 8, 0, 8], [8, 0, 5, 8],
+              [2, 9, 2147483647, -2147483648], [0, 0, 0, 0], [5, 3, 2, 1]]
+
+
+@pytest.mark.parametrize("off", DESCENDING)
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("roomy", [False, True])
+def test_descending_offsets_are_clamped_alike(gpu, off, dtype, roomy):
+    """Few rows and many (the buffers' room decides): the segments of the running maximum of the
+    offsets, each held to the buffers."""
+    E, H, F, rows, fp8 = 3, 256, 128, 8, dtype == "fp8"
+    room = 4096 if roomy else rows
+    top, clamped = 0, []
+    for i, o in enumerate(off):
+        top = max(top if i else 0, min(max(o, 0), room))
+        clamped.append(top)
+    x, w13 = normal(room, H), normal(E, 2 * F, H, std=H ** -0.5, seed=1)
+    w2 = normal(E, H, F, std=F ** -0.5, seed=2)
+    xs = s13 = s2 = None
+    if fp8:
+        (x, xs), (w13, s13), (w2, s2) = quant_rows(x), quant_weights(w13), quant_weights(w2)
+    h = B.moe_expert_create(B.make_expert_config(E, H, F, room, int(fp8)))
+
+    def run(offsets):
+        o = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+        hid = poisoned(room, F, dtype=torch.uint8 if fp8 else torch.bfloat16)
+        hs = poisoned(room, F // 128, dtype=torch.float32) if fp8 else None
+        y = poisoned(room, H)
+        B.moe_expert_gated(h, o, x, xs, w13, s13, hid, hs)
+        given = hid.clone()
+        if fp8:  # every row finite, for the rows that only `down` is given
+            given, scale = quant_rows(normal(room, F, seed=3))
+        B.moe_expert_down(h, o, given, scale if fp8 else None, w2, s2, y)
+        return [t for t in (hid, hs, y) if t is not None]
+
+    got, want = run(off), run(clamped)
+    assert B.moe_expert_read_status(h) == 0
+    for a, b in zip(got, want):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+        assert untouched(a[:clamped[0]]) and untouched(a[clamped[-1]:])
+        assert all(not untouched(r) for r in a[clamped[0]:clamped[-1]])
