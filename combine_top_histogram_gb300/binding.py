@@ -413,14 +413,28 @@ def moe_combine(h: Handle, y, w, out, stream=None) -> None:
         h.ptr, _ptr(y), _ptr(w), _ptr(out), _stream(stream)))
 
 
-def _buf(name: str, t, count: int, size: int, optional: bool = False) -> Optional[int]:
-    """Device pointer of a tensor that must hold `count` elements of `size` bytes."""
+_types = None
+
+
+def _element_types():
+    """The tensor types of bf16 values, e4m3 codes (as bytes, or as torch's own type), fp32
+    values and int32 offsets."""
+    global _types
+    if _types is None:
+        import torch
+        _types = ((torch.bfloat16,), (torch.uint8, torch.float8_e4m3fn), (torch.float32,),
+                  (torch.int32,))
+    return _types
+
+
+def _buf(name: str, t, count: int, types: tuple, optional: bool = False) -> Optional[int]:
+    """Device pointer of a tensor that must hold `count` elements of one of the types."""
     if t is None:
         if optional:
             return None
         raise ValueError(f"{name}: a tensor is needed")
-    if t.element_size() != size or t.numel() < count:
-        raise ValueError(f"{name}: expected at least {count} elements of {size} bytes, "
+    if t.dtype not in types or t.numel() < count:
+        raise ValueError(f"{name}: expected at least {count} elements of {types[0]}, "
                          f"got {t.numel()} of {t.dtype}")
     return _ptr(t)
 
@@ -430,10 +444,11 @@ def moe_combine_backward(h: Handle, dout, y, w, dy, dw, stream=None) -> None:
     every row that it can name."""
     c = h.cfg
     T, rows_h = c.num_ranks * c.tokens_per_rank, h.rows * c.hidden
+    bf16, _, fp32, _ = _element_types()
     _check("moe_combine_backward", load_library().moe_combine_backward(
-        h.ptr, _buf("dout", dout, T * c.hidden, 2), _buf("y", y, rows_h, 2),
-        _buf("w", w, T * c.top_k, 4), _buf("dy", dy, rows_h, 2),
-        _buf("dw", dw, T * c.top_k, 4), _stream(stream)))
+        h.ptr, _buf("dout", dout, T * c.hidden, bf16), _buf("y", y, rows_h, bf16),
+        _buf("w", w, T * c.top_k, fp32), _buf("dy", dy, rows_h, bf16),
+        _buf("dw", dw, T * c.top_k, fp32), _stream(stream)))
 
 
 def make_expert_config(E: int, H: int, F: int, rows_max: int, dtype: int = MOE_BF16,
@@ -454,9 +469,11 @@ class ExpertHandle:
         self.workspace = workspace
         self.fp8 = cfg.dtype == MOE_FP8_E4M3
         E, H, F, R = cfg.num_experts, cfg.hidden, cfg.inter, cfg.rows_max
-        #: elements that each tensor must hold, and the bytes of one of them
+        #: elements that each tensor must hold, and their types
         self.offsets, self.rows_h, self.rows_f = E + 1, R * H, R * F
-        self.w13, self.w2, self.elt = E * 2 * F * H, E * H * F, 1 if self.fp8 else 2
+        self.w13, self.w2 = E * 2 * F * H, E * H * F
+        self.bf16, codes, self.fp32, self.int32 = _element_types()
+        self.elt = codes if self.fp8 else self.bf16
         h = _c_void_p()
         _check("moe_expert_create", load_library().moe_expert_create(
             ctypes.byref(cfg), _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -493,7 +510,7 @@ def moe_expert_create(cfg: moe_expert_config_t, workspace=None, device=None) -> 
 def _scale(name: str, x: ExpertHandle, t, count: int) -> Optional[int]:
     if t is None and not x.fp8:
         return None
-    return _buf(name, t, count // 128, 4)
+    return _buf(name, t, count // 128, x.fp32)
 
 
 def moe_expert_gated(x: ExpertHandle, expert_offset, inp, inp_scale, w13, w13_scale, hid,
@@ -501,11 +518,11 @@ def moe_expert_gated(x: ExpertHandle, expert_offset, inp, inp_scale, w13, w13_sc
     """hid = silu(inp Wg^T) * (inp Wu^T) over the experts' segments (see the header)."""
     elt = x.elt
     _check("moe_expert_gated", load_library().moe_expert_gated(
-        x.ptr, _buf("expert_offset", expert_offset, x.offsets, 4),
+        x.ptr, _buf("expert_offset", expert_offset, x.offsets, x.int32),
         _buf("inp", inp, x.rows_h, elt), _scale("inp_scale", x, inp_scale, x.rows_h),
         _buf("w13", w13, x.w13, elt), _scale("w13_scale", x, w13_scale, x.w13 // 128),
         _buf("hid", hid, x.rows_f, elt), _scale("hid_scale", x, hid_scale, x.rows_f),
-        _buf("gate_up", gate_up, 2 * x.rows_f, 2, optional=True), _stream(stream)))
+        _buf("gate_up", gate_up, 2 * x.rows_f, x.bf16, optional=True), _stream(stream)))
 
 
 def moe_expert_down(x: ExpertHandle, expert_offset, hid, hid_scale, w2, w2_scale, y,
@@ -513,22 +530,24 @@ def moe_expert_down(x: ExpertHandle, expert_offset, hid, hid_scale, w2, w2_scale
     """y = hid W2^T over the experts' segments (see the header)."""
     elt = x.elt
     _check("moe_expert_down", load_library().moe_expert_down(
-        x.ptr, _buf("expert_offset", expert_offset, x.offsets, 4),
+        x.ptr, _buf("expert_offset", expert_offset, x.offsets, x.int32),
         _buf("hid", hid, x.rows_f, elt), _scale("hid_scale", x, hid_scale, x.rows_f),
         _buf("w2", w2, x.w2, elt), _scale("w2_scale", x, w2_scale, x.w2 // 128),
-        _buf("y", y, x.rows_h, 2), _stream(stream)))
+        _buf("y", y, x.rows_h, x.bf16), _stream(stream)))
 
 
 def moe_expert_backward(x: ExpertHandle, expert_offset, inp, gate_up, hid, dy, w13, w2, dx=None,
                         dw13=None, dw2=None, stream=None) -> None:
     """Gradients of the gated block; dx, or dw13 and dw2 together, may be left out."""
+    bf16 = x.bf16
     _check("moe_expert_backward", load_library().moe_expert_backward(
-        x.ptr, _buf("expert_offset", expert_offset, x.offsets, 4),
-        _buf("inp", inp, x.rows_h, 2), _buf("gate_up", gate_up, 2 * x.rows_f, 2),
-        _buf("hid", hid, x.rows_f, 2), _buf("dy", dy, x.rows_h, 2), _buf("w13", w13, x.w13, 2),
-        _buf("w2", w2, x.w2, 2), _buf("dx", dx, x.rows_h, 2, optional=True),
-        _buf("dw13", dw13, x.w13, 2, optional=True), _buf("dw2", dw2, x.w2, 2, optional=True),
-        _stream(stream)))
+        x.ptr, _buf("expert_offset", expert_offset, x.offsets, x.int32),
+        _buf("inp", inp, x.rows_h, bf16), _buf("gate_up", gate_up, 2 * x.rows_f, bf16),
+        _buf("hid", hid, x.rows_f, bf16), _buf("dy", dy, x.rows_h, bf16),
+        _buf("w13", w13, x.w13, bf16), _buf("w2", w2, x.w2, bf16),
+        _buf("dx", dx, x.rows_h, bf16, optional=True),
+        _buf("dw13", dw13, x.w13, bf16, optional=True),
+        _buf("dw2", dw2, x.w2, bf16, optional=True), _stream(stream)))
 
 
 def moe_expert_set_wait_limit(x: ExpertHandle, cycles: int) -> None:

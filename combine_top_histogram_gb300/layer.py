@@ -28,7 +28,12 @@ class ExpertBlock:
         if tuple(w2.shape) != (self.E, self.H, self.F) or F2 % 2:
             raise ValueError(f"w13 {tuple(w13.shape)} and w2 {tuple(w2.shape)} do not belong "
                              "together: expected [E, 2F, H] and [E, H, F]")
-        self.fp8 = w13.element_size() == 1
+        codes = (torch.uint8, torch.float8_e4m3fn)
+        self.fp8 = w13.dtype in codes
+        if w13.dtype not in (*codes, torch.bfloat16) or w2.dtype not in (
+                codes if self.fp8 else (torch.bfloat16,)):
+            raise ValueError(f"weights of {w13.dtype} and {w2.dtype}: both are bfloat16, or both "
+                             "e4m3 codes (uint8 or float8_e4m3fn)")
         if self.fp8 and (w13_scale is None or w2_scale is None):
             raise ValueError("e4m3 weights need their scales")
         self.w13, self.w2, self.w13_scale, self.w2_scale = w13, w2, w13_scale, w2_scale

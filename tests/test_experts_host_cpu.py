@@ -110,3 +110,67 @@ def test_backward_allocates_nothing(recorder, monkeypatch):
     for name in ("ones", "empty", "empty_like", "zeros"):
         monkeypatch.setattr(torch, name, lambda *a, **k: pytest.fail("allocated"))
     layer.backward(x, w, stream=1)
+
+
+E, H, F, ROWS = 2, 128, 128, 8
+f32 = torch.zeros
+SAME_SIZE = {torch.bfloat16: (torch.float16, torch.int16), torch.uint8: (torch.int8,
+             torch.float8_e5m2, torch.bool), torch.float32: (torch.int32,),
+             torch.int32: (torch.float32,)}
+
+
+def call(op, fp8=False):
+    """An operator's binding and its arguments by name, every one of the right type."""
+    dt = torch.uint8 if fp8 else torch.bfloat16
+    z = lambda *s, dtype=dt: torch.zeros(*s, dtype=dtype)  # noqa: E731
+    if op == "combine_backward":
+        layer, x, ids, w = layer_for_training()
+        layer.forward(x, ids=ids, w=w)
+        return B.moe_combine_backward, layer.handle, dict(
+            dout=x, y=layer.y, w=w, dy=torch.zeros_like(layer.y), dw=torch.zeros_like(w))
+    h = B.moe_expert_create(B.make_expert_config(E, H, F, ROWS, int(fp8), op == "backward"),
+                            device="cpu")
+    a = dict(expert_offset=z(E + 1, dtype=torch.int32))
+    if op == "gated":
+        a.update(inp=z(ROWS, H), inp_scale=f32(ROWS, 1) if fp8 else None, w13=z(E, 2 * F, H),
+                 w13_scale=f32(E, 2, 1) if fp8 else None, hid=z(ROWS, F),
+                 hid_scale=f32(ROWS, 1) if fp8 else None,
+                 gate_up=None if fp8 else z(ROWS, 2 * F))
+        return B.moe_expert_gated, h, a
+    if op == "down":
+        a.update(hid=z(ROWS, F), hid_scale=f32(ROWS, 1) if fp8 else None, w2=z(E, H, F),
+                 w2_scale=f32(E, 1, 1) if fp8 else None, y=bf16(ROWS, H))
+        return B.moe_expert_down, h, a
+    a.update(inp=z(ROWS, H), gate_up=z(ROWS, 2 * F), hid=z(ROWS, F), dy=z(ROWS, H),
+             w13=z(E, 2 * F, H), w2=z(E, H, F), dx=z(ROWS, H), dw13=z(E, 2 * F, H),
+             dw2=z(E, H, F))
+    return B.moe_expert_backward, h, a
+
+
+@pytest.mark.parametrize("op, fp8", [("gated", False), ("gated", True), ("down", False),
+                                     ("down", True), ("backward", False),
+                                     ("combine_backward", False)])
+def test_other_types_of_the_same_size_are_refused(recorder, op, fp8):
+    fn, handle, args = call(op, fp8)
+    fn(handle, **args)
+    assert recorder.calls[-1] == fn.__name__
+    for name, t in args.items():
+        for other in SAME_SIZE[t.dtype] if t is not None else ():
+            with recorder.nothing_called(), pytest.raises(ValueError, match=name):
+                fn(handle, **{**args, name: t.view(other)})
+        if t is not None and t.dtype == torch.uint8:  # codes by their own name
+            fn(handle, **{**args, name: t.view(torch.float8_e4m3fn)})
+
+
+@pytest.mark.parametrize("types", [(torch.float16, torch.float16), (torch.int8, torch.int8),
+                                   (torch.float8_e5m2, torch.float8_e5m2),
+                                   (torch.bfloat16, torch.float16), (torch.uint8, torch.int8),
+                                   (torch.bfloat16, torch.uint8), (torch.float32, torch.float32)])
+def test_experts_of_other_types_are_refused(recorder, types):
+    one = torch.ones(2, 2, 1)
+    for layer in (MoeLayer(1, 4, 2, 1, 128, device="cpu"),
+                  MoeLayer(1, 4, 2, 1, 128, B.MOE_FP8_E4M3, device="cpu")):
+        with recorder.nothing_called(), pytest.raises(ValueError):
+            layer.set_experts(torch.zeros(2, 256, 128, dtype=types[0]),
+                              torch.zeros(2, 128, 128, dtype=types[1]), one, one)
+    assert layer.experts is None
