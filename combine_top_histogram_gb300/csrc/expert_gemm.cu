@@ -673,6 +673,22 @@ __device__ __forceinline__ void fma2(float2& acc, uint32_t lo, uint32_t hi, floa
   acc = __ffma2_rn(make_float2(__uint_as_float(lo), __uint_as_float(hi)), make_float2(s, s), acc);
 }
 
+// -a / s rounded to nearest for two values, y = RN(1 / s): the product by the
+// reciprocal is within 1.5 units in its last place, and each of two steps adds
+// the residual times y (P. Markstein, "Computation of elementary functions on
+// the IBM RISC System/6000 processor", IBM J. Res. Dev. 34(1), 1990: the first
+// makes the quotient faithful, the second rounds it correctly). For s between
+// 2^-64 and 2^64 only quotients below 2^-40 can differ, whose e4m3 code is a
+// signed zero. Of the negative, because a zero then keeps its sign: a = -0
+// gives +0, and a = +0 gives -0.
+__device__ __forceinline__ float2 minus_quotient(float2 a, float s, float y) {
+  const float2 ss = make_float2(s, s), ny = make_float2(-y, -y);
+  float2 q = __fmul2_rn(a, ny);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) q = __ffma2_rn(__ffma2_rn(ss, q, a), ny, q);
+  return q;
+}
+
 template <int OP, bool FP8, int CG, int TN>
 __global__ void __launch_bounds__(kThreads, 1)
     k_expert_gemm(const __grid_constant__ CUtensorMap map_a,
@@ -975,19 +991,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           parity ^= 1;  // the other buffer next: this one is read until then
           const float scale = __fdiv_rn(m, 448.0f);
           if (mine && half == 0) p.out_scale[((long long)t.row0 + r) * (p.F >> 7) + t.n0] = scale;
-          // h / s by the reciprocal: within 2^-23, as h itself
-          const float inv = __frcp_rn(scale);
           uint8_t* out =
               static_cast<uint8_t*>(p.out) + (row + lane) * p.F + t.n0 * 128 + half * 64;
+          // the reciprocal and its products far from underflow and overflow
+          const bool quick = scale >= 0x1p-64f && scale <= 0x1p64f;
+          const float y = quick ? __frcp_rn(scale) : 0.0f;
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             uint32_t q[8];
 #pragma unroll
             for (int w = 0; w < 8; ++w) {
               const float* f = h + 32 * u + 4 * w;
-              if (scale >= 1e-30f) {
-                q[w] = e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
-              } else if (scale > 0.0f) {  // the reciprocal may overflow
+              if (quick) {
+                const float2 a = minus_quotient(make_float2(f[0], f[1]), scale, y);
+                const float2 b = minus_quotient(make_float2(f[2], f[3]), scale, y);
+                q[w] = e4m3x4(a.x, a.y, b.x, b.y) ^ 0x80808080u;
+              } else if (scale > 0.0f) {
                 q[w] = e4m3x4(__fdiv_rn(f[0], scale), __fdiv_rn(f[1], scale),
                               __fdiv_rn(f[2], scale), __fdiv_rn(f[3], scale));
               } else {

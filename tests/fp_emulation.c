@@ -1,5 +1,5 @@
 /*
- * fp_emulation.c -- CPU emulation, operation for operation, of two
+ * fp_emulation.c -- CPU emulation, operation for operation, of three
  * floating-point procedures the CUDA kernels use, so that the claims made
  * about them can be checked on the host:
  *
@@ -8,7 +8,9 @@
  *      quotient RN(x / s);
  *   2. the router's softmax weights in float-float arithmetic (ffmath.cuh and
  *      route_group_warp in layout_device.cuh), against the same softmax
- *      evaluated in double and rounded once to fp32.
+ *      evaluated in double and rounded once to fp32;
+ *   3. the experts' quotient h / s by two such corrections (expert_gemm.cu,
+ *      minus_quotient), against RN(h / s) for fp32 h.
  *
  * TEST CODE. It is neither the oracle nor the CUDA path: it restates the
  * kernels' float steps in C so that they can be run exhaustively or on
@@ -107,6 +109,18 @@ void markstein_sweep(uint32_t amax_lo, uint32_t amax_hi, int64_t* pairs, int64_t
 /* The kernel's quotient for given (x, s) pairs (for sampled checks). */
 void markstein_many(int64_t n, const float* x, const float* s, float* q) {
     for (int64_t i = 0; i < n; ++i) q[i] = emu_div_by_scale(x[i], s[i]);
+}
+
+/* The experts' quotient (expert_gemm.cu, minus_quotient): the negative of
+ * x / s by two steps from x * RN(1/s), returned with its sign turned. */
+void two_step_quotient_many(int64_t n, const float* x, const float* s, float* out) {
+    for (int64_t i = 0; i < n; ++i) {
+        const float y = 1.0f / s[i];
+        float q = x[i] * -y;
+        q = emu_fmaf(emu_fmaf(s[i], q, x[i]), -y, q);
+        q = emu_fmaf(emu_fmaf(s[i], q, x[i]), -y, q);
+        out[i] = -q;
+    }
 }
 
 /* ---------------------------------------------------------------------- */

@@ -122,3 +122,44 @@ def test_descending_offsets_are_clamped_alike(gpu, off, dtype, roomy):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
         assert untouched(a[:clamped[0]]) and untouched(a[clamped[-1]:])
         assert all(not untouched(r) for r in a[clamped[0]:clamped[-1]])
+
+
+def test_codes_beside_ties_are_those_of_the_quotient(gpu):
+    """h within a few units of s times a midpoint of two e4m3 values: few rows and many give the
+    same scales and the codes of the quotient h / s, rounded once before the code is."""
+    E, per, H, F = 16, 3, 128, 256
+    n = E * per
+    g = torch.Generator(device="cuda").manual_seed(5)
+    e = torch.randint(4, 8, (E, F), device="cuda", generator=g)
+    c = (8 + torch.randint(0, 8, (E, F), device="cuda", generator=g)) * 2.0 ** (e - 3)
+    w = torch.zeros(E, 2 * F, H, device="cuda")
+    w[:, :F, 0] = 64.0         # the sigmoid of 32 or more is 1
+    w[:, F:, 0] = c            # 16 to 240, and half a step above
+    w[:, F:, 1] = 2.0 ** (e - 4)
+    w[:, F::128, 0], w[:, F::128, 1] = 448.0, 0.0  # the largest of each 128 channels
+    codes = lambda v: v.to(torch.float8_e4m3fn).view(torch.uint8)  # noqa: E731
+    ws = torch.ones(E, 2 * F // 128, 1, device="cuda")
+    ws[:, F // 128:] = 0.5 + torch.rand(E, F // 128, 1, device="cuda", generator=g)
+    x = torch.zeros(n, H, device="cuda")
+    x[:, :2] = 1.0
+    xs = 0.5 + 0.5 * torch.rand(n, 1, device="cuda", generator=g)
+    off = torch.arange(0, n + 1, per, dtype=torch.int32, device="cuda")
+
+    def run(rows):
+        big = lambda t: torch.cat([t, t.new_zeros(rows - n, *t.shape[1:])])  # noqa: E731
+        hid = poisoned(rows, F, dtype=torch.uint8)
+        hs = poisoned(rows, F // 128, dtype=torch.float32)
+        h = B.moe_expert_create(B.make_expert_config(E, H, F, rows, B.MOE_FP8_E4M3))
+        B.moe_expert_gated(h, off, big(codes(x)), big(xs), codes(w), ws, hid, hs)
+        return hid[:n], hs[:n]
+
+    (few, few_s), (many, many_s) = run(n), run(4096)
+    gate = 64 * xs                                               # exact
+    of_row = torch.arange(E, device="cuda").repeat_interleave(per)
+    scale = (xs * ws[of_row, F // 128:, 0]).repeat_interleave(128, 1)  # one rounding
+    h = gate * ((w[of_row, F:, 0] + w[of_row, F:, 1]) * scale)   # one rounding each
+    amax = h.view(n, -1, 128).amax(2)
+    s = amax / torch.full_like(amax, 448.0)  # torch multiplies by a scalar's reciprocal
+    want = codes(h / s.repeat_interleave(128, 1))
+    for got, got_s in ((few, few_s), (many, many_s)):
+        assert torch.equal(got_s, s) and torch.equal(got, want)
