@@ -83,6 +83,10 @@ struct Shared {
   uint64_t tail[kMaxStages];           // kDw, second CTA: its copies of a segment's last block
   uint32_t tmem;
   int abort, uneven;
+  uint32_t announced;                  // pairs: stages whose copies this CTA has announced,
+  uint32_t tails, tail_phase;          // in kDw's second CTA: the stages whose last ones were
+  uint32_t tails_sent, tails_done;     // for `tail`, these barriers' parities, how many there
+                                       // were and how many its other warp has handed on
   uint64_t pair[4];                    // the two warps of a lane quarter exchange amax
   float amax[2][2][kTileM];            // [tile parity][half][row]
   uint64_t sempty[2];                  // the epilogue has read scale[i]
@@ -611,6 +615,51 @@ struct Issuer {
   }
 };
 
+// Waits until the last stages that were announced, of `announced` in all, have
+// their copies.
+template <int STAGES>
+__device__ __forceinline__ void drain_stages(Shared& s, uint32_t announced) {
+  const uint32_t n = announced < STAGES ? announced : STAGES;
+  for (uint32_t i = announced - n; i != announced; ++i)
+    mbar_drain(smem_u32(&s.full[i % STAGES]), (i / STAGES) & 1);
+}
+
+// After a wait gave up in a pair and both CTAs' warps have left their loops: a
+// stage that only one CTA has announced, or whose last block the second CTA
+// has not handed on, never completes by itself. The first warps make the
+// missing arrivals and wait for what is in flight into either CTA. (No CTA is
+// more than the ring's stages ahead: a stage is announced again only after its
+// products, and those wait for both.)
+template <int OP, int STAGES>
+__device__ __forceinline__ void settle_pair(Shared& s, int rank) {
+  if (rank == 1) {
+    if (OP == kDw) {
+      uint32_t left = s.tails_sent - s.tails_done;
+      for (uint32_t i = s.announced; left != 0 && i != 0; --i) {
+        const uint32_t st = (i - 1) % STAGES;
+        if (!((s.tails >> st) & 1)) continue;
+        mbar_drain(smem_u32(&s.tail[st]), ((s.tail_phase >> st) & 1) ^ 1);
+        if ((threadIdx.x & 31) == 0)
+          mbar_arrive_release(cluster_addr(smem_u32(&s.full[st]), 0));
+        --left;
+      }
+    }
+  } else {
+    uint32_t other;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];"
+                 : "=r"(other)
+                 : "r"(cluster_addr(smem_u32(&s.announced), 1))
+                 : "memory");
+    const uint32_t most = max(s.announced, other);
+    if ((threadIdx.x & 31) == 0)
+      for (uint32_t i = min(s.announced, other); i != most; ++i)
+        mbar_arrive(smem_u32(&s.full[i % STAGES]));
+    __syncwarp();
+    drain_stages<STAGES>(s, most);
+  }
+  __syncwarp();
+}
+
 // FP8: two warps keep the scales of the next accumulators ready, so that the
 // epilogue warps never wait for memory: for each reduction block the 128 rows'
 // scale times those of the tile's two weight blocks. Thread j of 64 serves
@@ -744,8 +793,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < kEpiWarp0) {
     give_registers<FP8>();
     if (warp == 0) {
-      int st = 0, issued = 0;
-      uint32_t ph = 0;
+      int st = 0;
+      uint32_t ph = 0, announced = 0, tails = 0, tail_phase = 0, tails_sent = 0;
       bool ok = true;
       Tile t;
       const uint32_t ring = smem_u32(smem);
@@ -771,8 +820,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar = smem_u32(&s.tail[st]);
             mbar_expect_elected(bar, bytes);
             bar = cluster_addr(bar, 1);
+            tails |= 1u << st;
+            tail_phase ^= 1u << st;
+            ++tails_sent;
           } else if constexpr (kPair) {
             mbar_expect_relaxed_elected(bar, bytes);
+            if (OP == kDw) tails &= ~(1u << st);
           } else {
             mbar_expect_elected(bar, bytes);
           }
@@ -804,22 +857,23 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_3d<CG>(b + i * (TN / 2 * 128), &map_b, bar, kb * kElems, n, e);
             }
           }
-          if (issued < kStages) ++issued;
+          ++announced;
           if (++st == kStages) {
             st = 0;
             ph ^= 1;
           }
         }
       }
-      // copies in flight land before the CTA (the pair) ends, also when a wait
-      // gave up
-      for (int i = 0; i < (rank == 0 ? issued : 0); ++i) {
-        if (--st < 0) {
-          st = kStages - 1;
-          ph ^= 1;
-        }
-        mbar_drain(smem_u32(&s.full[st]), ph);
+      // Copies in flight land before the CTA (the pair) ends, also when a wait
+      // gave up: then a pair may have announced unlike numbers of stages, and
+      // settles that below.
+      if (kPair && lane == 0) {
+        s.announced = announced;
+        s.tails = tails;
+        s.tail_phase = tail_phase;
+        s.tails_sent = tails_sent;
       }
+      if (rank == 0 && !(kPair && *ctl.abort)) drain_stages<kStages>(s, announced);
       __syncwarp();
     } else if (kPair && warp == 1 && rank == 1) {
       // The second CTA issues no products. In kDw it clears its rows past a
@@ -827,6 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (OP == kDw) {
         int st = 0;
         uint32_t phases = 0;  // bit i: parity of tail[i]'s next phase
+        uint32_t handed_on = 0;
         bool ok = true;
         Tile t;
         while (ok && walk.next(t)) {
@@ -840,7 +895,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           clear_rows<2 + TN / 64 / CG>(smem + last * kStageBytes, valid, lane);
           if (lane == 0) mbar_arrive_release(cluster_addr(smem_u32(&s.full[last]), 0));
           phases ^= 1u << last;
+          ++handed_on;
         }
+        if (lane == 0) s.tails_done = handed_on;
       }
       __syncwarp();
     } else if (warp == 1) {
@@ -1022,8 +1079,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncwarp();
   tc_fence_before();
-  if constexpr (kPair) cluster_sync();  // neither CTA's memory is used any more
-  else __syncthreads();
+  if constexpr (kPair) {
+    cluster_sync();  // neither CTA's memory is used any more, unless a wait gave up
+    if (*ctl.abort) {  // set in both CTAs before that
+      if (warp == 0) settle_pair<OP, kStages>(s, rank);
+      cluster_sync();
+    }
+  } else {
+    __syncthreads();
+  }
   tc_fence_after();
   if (warp == 2) tc_dealloc<CG>(tmem, 512);
 }

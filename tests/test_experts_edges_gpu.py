@@ -163,3 +163,39 @@ def test_codes_beside_ties_are_those_of_the_quotient(gpu):
     want = codes(h / s.repeat_interleave(128, 1))
     for got, got_s in ((few, few_s), (many, many_s)):
         assert torch.equal(got_s, s) and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("cycles", [0, 300, 2000, 8000, 30000])
+def test_waits_that_run_out_in_pairs(gpu, cycles):
+    """Two CTAs on one tile (enough rows an expert, ragged segments): whatever wait runs out
+    first, every kernel leaves and says so, and the next call with the usual limit is right."""
+    counts, H, F = [1300, 0, 215, 1029], 1032, 520
+    E, n = len(counts), sum(counts)
+    rows = 768 * E + 5
+    x, gu, hid = normal(rows, H), poisoned(rows, 2 * F), poisoned(rows, F)
+    w13, w2 = normal(E, 2 * F, H, std=H ** -0.5, seed=1), normal(E, H, F, std=F ** -0.5, seed=2)
+    dy, y, dx = normal(rows, H, std=0.1, seed=3), poisoned(rows, H), poisoned(rows, H)
+    dw13, dw2 = poisoned(E, 2 * F, H), poisoned(E, H, F)
+    off = torch.tensor([0] + counts, device="cuda").cumsum(0).to(torch.int32)
+    h = B.moe_expert_create(B.make_expert_config(E, H, F, rows, train=True))
+    calls = (lambda: B.moe_expert_gated(h, off, x, None, w13, None, hid, None, gu),
+             lambda: B.moe_expert_down(h, off, hid, None, w2, None, y),
+             lambda: B.moe_expert_backward(h, off, x, gu, hid, dy, w13, w2, dx, dw13, dw2))
+    B.moe_expert_set_wait_limit(h, cycles)
+    for _ in range(5):
+        for call in calls:
+            call()
+            status = B.moe_expert_read_status(h)
+            assert status == B.MOE_STATUS_TIMEOUT or (cycles > 0 and status == 0)
+    B.moe_expert_set_wait_limit(h, 1 << 32)
+    for call in calls:
+        call()
+    assert B.moe_expert_read_status(h) == 0
+    both, err = R.rows_times(x[:n].double(), w13.double(), counts)
+    v, e = R.silu_product(both[:, :F], both[:, F:], err[:, :F], err[:, F:])
+    R.check("hid", hid[:n], *R.bf16_out(v, e))
+    R.check("y", y[:n], *R.bf16_out(*R.rows_times(hid[:n].double(), w2.double(), counts)))
+    want = R.backward(*(t[:n].double() for t in (x, gu, hid, dy)), w13.double(), w2.double(),
+                      counts)
+    for name, got, ref in (("dx", dx[:n], want[0]), ("dw13", dw13, want[1]), ("dw2", dw2, want[2])):
+        R.check(name, got, *ref)
