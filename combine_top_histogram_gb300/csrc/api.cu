@@ -332,7 +332,8 @@ int moe_handle_create(const moe_config_t* cfg, void* d_workspace, size_t bytes,
   if (cudaMemset(ws + p.off_ctrl, 0, 64) != cudaSuccess ||
       cudaMemset(ws + p.off_acc, 0, (size_t)cfg->num_experts * 4) != cudaSuccess ||
       cudaMemset(ws + p.off_acc_se, 0, (size_t)cfg->num_ranks * cfg->num_experts * 4) !=
-          cudaSuccess) {
+          cudaSuccess ||
+      cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess) {  // before work on any stream
     free(h);
     return MOE_ERR_CUDA;
   }
@@ -847,11 +848,13 @@ int moe_expert_standin_tokens(moe_handle_t h, int64_t token_begin, int64_t token
 
 int moe_read_status(moe_handle_t h, uint32_t* flags, void* stream) {
   if (!h || !flags) return MOE_ERR_INVALID_ARG;
+  // all on the caller's stream: a later call on it finds the word cleared
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaStreamSynchronize(st) != cudaSuccess) return MOE_ERR_CUDA;
-  if (cudaMemcpy(flags, h->status, sizeof(uint32_t), cudaMemcpyDeviceToHost) != cudaSuccess)
+  if (cudaMemcpyAsync(flags, h->status, sizeof(uint32_t), cudaMemcpyDeviceToHost, st) !=
+          cudaSuccess ||
+      cudaMemsetAsync(h->status, 0, sizeof(uint32_t), st) != cudaSuccess ||
+      cudaStreamSynchronize(st) != cudaSuccess)
     return MOE_ERR_CUDA;
-  if (cudaMemset(h->status, 0, sizeof(uint32_t)) != cudaSuccess) return MOE_ERR_CUDA;
   return MOE_OK;
 }
 

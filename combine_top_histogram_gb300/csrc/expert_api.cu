@@ -99,7 +99,8 @@ int moe_expert_create(const moe_expert_config_t* cfg, void* d_workspace, size_t 
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
       moe::expert_gemm_prepare() != cudaSuccess ||
-      cudaMemset(d_workspace, 0, kAlign) != cudaSuccess)
+      cudaMemset(d_workspace, 0, kAlign) != cudaSuccess ||
+      cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess)  // before work on any stream
     return MOE_ERR_CUDA;
   moe_expert* x = static_cast<moe_expert*>(calloc(1, sizeof(moe_expert)));
   if (!x) return MOE_ERR_INVALID_ARG;
@@ -209,11 +210,13 @@ int moe_expert_set_wait_limit(moe_expert_t x, int64_t cycles) {
 
 int moe_expert_read_status(moe_expert_t x, uint32_t* flags, void* stream) {
   if (!x || !flags) return MOE_ERR_INVALID_ARG;
+  // all on the caller's stream: a later call on it finds the word cleared
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaStreamSynchronize(st) != cudaSuccess) return MOE_ERR_CUDA;
-  if (cudaMemcpy(flags, x->status, sizeof(uint32_t), cudaMemcpyDeviceToHost) != cudaSuccess)
+  if (cudaMemcpyAsync(flags, x->status, sizeof(uint32_t), cudaMemcpyDeviceToHost, st) !=
+          cudaSuccess ||
+      cudaMemsetAsync(x->status, 0, sizeof(uint32_t), st) != cudaSuccess ||
+      cudaStreamSynchronize(st) != cudaSuccess)
     return MOE_ERR_CUDA;
-  if (cudaMemset(x->status, 0, sizeof(uint32_t)) != cudaSuccess) return MOE_ERR_CUDA;
   return MOE_OK;
 }
 

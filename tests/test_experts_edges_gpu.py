@@ -199,3 +199,38 @@ def test_waits_that_run_out_in_pairs(gpu, cycles):
                       counts)
     for name, got, ref in (("dx", dx[:n], want[0]), ("dw13", dw13, want[1]), ("dw2", dw2, want[2])):
         R.check(name, got, *ref)
+
+
+def test_handles_made_beside_a_busy_stream(gpu):
+    """A handle's control words are cleared when its creation returns, and a status that was read
+    is cleared on its stream, whatever the default stream has queued."""
+    from combine_top_histogram_gb300 import MoeLayer
+    H, F, rows = 512, 256, 320
+    x, w13 = normal(rows, H), normal(2, 2 * F, H, std=H ** -0.5, seed=1)
+    hid = poisoned(rows, F)
+    off = torch.tensor([0, 300, 320], dtype=torch.int32, device="cuda")
+    P, Tr, E, k = 2, 37, 8, 2
+    g = torch.Generator(device="cuda").manual_seed(0)
+    ids = torch.rand(P * Tr, E, device="cuda", generator=g).topk(k, 1).indices.to(torch.int32)
+    w = torch.softmax(torch.randn(P * Tr, k, device="cuda", generator=g), 1)
+    t = normal(P * Tr, 64)
+    want = MoeLayer(P, Tr, E, k, 64).forward(t, ids=ids, w=w).clone()
+    dirty = torch.full((1 << 26,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    del dirty  # the next workspaces' memory
+    side = torch.cuda.Stream()
+    busy()
+    h = B.moe_expert_create(B.make_expert_config(2, H, F, rows))
+    busy()
+    B.moe_expert_set_wait_limit(h, 0)
+    for _ in range(3):
+        B.moe_expert_gated(h, off, x, None, w13, None, hid, stream=side)
+        assert B.moe_expert_read_status(h, side) == B.MOE_STATUS_TIMEOUT
+        assert B.moe_expert_read_status(h, side) == 0
+    assert not torch.cuda.current_stream().query()
+    layer = MoeLayer(P, Tr, E, k, 64)
+    busy()
+    layer.forward(t, ids=ids, w=w, stream=side)
+    assert layer.status(side) == 0
+    assert not torch.cuda.current_stream().query()
+    assert torch.equal(layer.out, want)
