@@ -51,6 +51,7 @@ class ExpertBlock:
         self.gate_up = torch.empty((rows, 2 * self.F), **bf) if train else None
         self.dw13 = torch.empty_like(w13) if train else None
         self.dw2 = torch.empty_like(w2) if train else None
+        self.ran = False  # hid and gate_up hold a forward's results
 
     def forward(self, expert_offset, x, x_scale, y, stream=None):
         """y = (silu(x Wg^T) * (x Wu^T)) W2^T over the experts' segments."""
@@ -58,6 +59,7 @@ class ExpertBlock:
                            self.hid, self.hid_scale, self.gate_up, stream)
         B.moe_expert_down(self.handle, expert_offset, self.hid, self.hid_scale, self.w2,
                           self.w2_scale, y, stream)
+        self.ran = True
         return y
 
     def backward(self, expert_offset, x, dy, dx, stream=None):
@@ -65,6 +67,8 @@ class ExpertBlock:
         forward of the same rows."""
         if not self.train:
             raise ValueError("the experts were not built for training")
+        if not self.ran:
+            raise ValueError("backward follows a forward of these experts")
         B.moe_expert_backward(self.handle, expert_offset, x, self.gate_up, self.hid, dy, self.w13,
                               self.w2, dx, self.dw13, self.dw2, stream)
         return dx
@@ -240,6 +244,8 @@ class MoeLayer:
             raise ValueError("backward needs experts built for training (set_experts)")
         if self.fixed:  # inv names fixed slots, which y and recv_x do not hold
             raise ValueError("backward follows a compact dispatch, not fixed slots")
+        if not self.experts.ran:  # nothing yet in gate_up and hid
+            raise ValueError("backward follows a forward of these experts")
         g = self.grads
         B.moe_combine_backward(self.handle, dout, self.y, w, g["dy"], g["dw"], stream)
         self.experts.backward(self.layout_view()["expert_offset"], self.recv_x, g["dy"],

@@ -112,6 +112,21 @@ def test_backward_allocates_nothing(recorder, monkeypatch):
     layer.backward(x, w, stream=1)
 
 
+def test_backward_needs_a_forward_of_these_experts(recorder):
+    """New experts have no hidden rows yet, whatever ran before them."""
+    layer, x, ids, w = layer_for_training()
+    for _ in range(2):
+        layer.layout(ids)
+        layer.dispatch(x, w)
+        with recorder.nothing_called(), pytest.raises(ValueError, match="forward"):
+            layer.backward(x, w)
+        with recorder.nothing_called(), pytest.raises(ValueError, match="forward"):
+            layer.experts.backward(ids, layer.recv_x, layer.y, layer.y)
+        layer.forward(x, ids=ids, w=w)
+        layer.backward(x, w)
+        layer.set_experts(layer.experts.w13, layer.experts.w2, train=True)
+
+
 E, H, F, ROWS = 2, 128, 128, 8
 f32 = torch.zeros
 SAME_SIZE = {torch.bfloat16: (torch.float16, torch.int16), torch.uint8: (torch.int8,
