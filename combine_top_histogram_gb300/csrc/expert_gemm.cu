@@ -7,6 +7,10 @@
 //   kDown   y  = h W2^T                             A = h,   B = w2  (K-major)
 //   kDgate  dh = dy W2, then dg = dh u s (1 + g (1 - s)), du = dh g s with
 //           s = 1 / (1 + exp(-g))                   A = dy,  B = w2  (N-major)
+//           (dg and du rounded to bf16, which kDx and kDw feed to the tensor
+//           cores: their results are within 0.0024 of 64-bit ones, 0.0017 if
+//           only the results were rounded; in 32 bits their products would be
+//           two or three of bf16 each)
 //   kDx     dx = [dg du] W13                        A = dgu, B = w13 (N-major)
 //   kDw     dW = a^T b over the segment's rows      A = a (M-major), B = b (N-major)
 //
@@ -1198,7 +1202,10 @@ cudaError_t launch(const ExpertArgs& args, const void* a, const void* b, int num
 // at 128, 251 / 230 at 256; kDw, where the rows are the reduction axis and the
 // epilogue of a short sum weighs more, 480 / 498 at 512, 757 / 737 at 1024.
 // e4m3 (H = 7168) does not gain: 961 / 1158 at 512 rows, where an accumulator
-// is handed back and forth between the two CTAs for each 128 channels.
+// is handed back and forth between the two CTAs for each 128 channels. The rule
+// does not look at how many tiles there are: alone / paired at 32768 rows of
+// one expert, backward of H = 256, F = 128 327 / 341 (two weight tiles, each
+// 512 blocks long), of H = 4096, F = 1408 1774 / 1515.
 bool use_pair(ExpertOp op, bool fp8, const ExpertArgs& p) {
   if (fp8) return false;
   return p.rows_max >= (op == kDw ? 768ll : 192ll) * p.E;
@@ -1206,13 +1213,15 @@ bool use_pair(ExpertOp op, bool fp8, const ExpertArgs& p) {
 
 // Whether tiles are 128 columns wide: where 256 would give at most two tiles
 // per SM, more and smaller ones spread a product's copies, which bound it then,
-// over more SMs (64 bytes a cycle go into each). Drawn bf16 cases of all
-// products, tiles of 256 / 128 columns, us: backward of 77 tokens, top-3,
-// E = 16, H = 520, F = 264 40.5 / 30.8, down of 10740 tokens, top-5, E = 17,
-// H = 1824, F = 1432 277 / 238; 0.94 of the time in the mean over 31 cases with
-// this rule, 0.96 with half of its threshold, 0.945 with twice. Where tiles are
-// many, narrow ones cost: kDw of E = 32, H = 4096, F = 2048 at 512 rows an
-// expert makes its backward pass 1316 / 1618.
+// over more SMs (64 bytes a cycle go into each). bf16, uniform routing, passes
+// one after another, tiles of 256 / 128 columns, us: backward of 231 rows,
+// E = 16, H = 520, F = 264 39.8 / 30.4; H = 4096, F = 1408, E = 8: down at 1024
+// rows 24.1 / 23.2, gated at 1400 58.9 / 55.1. What the rule gives away: where
+// the wide tiles come to about whole turns of the SMs, narrow ones only add to
+// the copies (there, gated at 512 rows 38.5 / 49.4, down 13.9 / 18.4, and at
+// 1400 rows 25.5 / 29.3). Where tiles are many they cost: E = 16 at 2048 rows
+// gated 70.4 / 77.1, down 41.1 / 45.1, backward 265 / 318; kDw of E = 32,
+// H = 4096, F = 2048 at 512 rows an expert makes its backward pass 1316 / 1618.
 template <int OP>
 bool use_narrow(const ExpertArgs& p, int num_sms) {
   return most_tiles<OP>(p, kTileM, column_tiles<OP>(p, 256)) <= 2ll * num_sms;

@@ -7,8 +7,8 @@ namespace moe {
 
 // 1 / (1 + exp(-g)) as 1 / (1 + 2^(-g log2 e)) with the hardware's approximate
 // 2^x and reciprocal, each within 2^-22 of the value; the rounded argument adds
-// up to |g| 2^-24. 2^x = +inf (g below -88) gives 0, where the true value is
-// below 2^-127.
+// up to |g| 2^-24. A result below 2^-126 (g below -87.3) is flushed to 0, and
+// silu(g), there below 2^-119 in magnitude, with it.
 __device__ __forceinline__ float sigmoid(float g) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));

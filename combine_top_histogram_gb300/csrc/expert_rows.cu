@@ -310,11 +310,9 @@ cudaError_t launch(const ExpertArgs& p, const void* a, const void* b, int num_sm
     const int c = channels * (kWarps / s);
     return segments * ((p.N + c - 1) / c);
   };
-  // The smallest split that still gives three CTAs per SM (measured against two
-  // and four: 0.985 and 0.981 of the time of four in the mean over 38 calls of
-  // one to four tokens; down e4m3, one token of E = 256, top-8, H = 7168,
-  // F = 2048 24.2 / 24.3 / 26.0 us at four / three / two, gated 55.8 / 44.4 /
-  // 44.2); two where the split's CTAs form clusters, which cost more (E = 64,
+  // The smallest split that still gives three CTAs per SM (us at four / three /
+  // two, one token of E = 256, top-8, H = 7168, F = 2048: down e4m3 24.2 / 24.3 /
+  // 26.0, gated e4m3 55.8 / 44.4 / 44.2); two where the split's CTAs form clusters, which cost more (E = 64,
   // H = 2048, F = 1024, top-2: 11.7 / 11.2 / 9.6).
   const long long enough = (OP == kGated && FP8 ? 2ll : 3ll) * num_sms;
   int s = 1;
