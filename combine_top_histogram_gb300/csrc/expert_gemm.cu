@@ -8,9 +8,9 @@
 //   kDgate  dh = dy W2, then dg = dh u s (1 + g (1 - s)), du = dh g s with
 //           s = 1 / (1 + exp(-g))                   A = dy,  B = w2  (N-major)
 //           (dg and du rounded to bf16, which kDx and kDw feed to the tensor
-//           cores: their results are within 0.0024 of 64-bit ones, 0.0017 if
-//           only the results were rounded; in 32 bits their products would be
-//           two or three of bf16 each)
+//           cores: the gradients' relative error against 64 bits is then 0.0024,
+//           with rounded results alone 0.0017; held in two bf16 parts each,
+//           they would double those products)
 //   kDx     dx = [dg du] W13                        A = dgu, B = w13 (N-major)
 //   kDw     dW = a^T b over the segment's rows      A = a (M-major), B = b (N-major)
 //
@@ -31,7 +31,7 @@
 // add up in registers: the accumulators then alternate per block.
 //
 // What bounds it: of bf16 with many rows the tensor pipe (pairs: 94 % of the
-// SMs' active cycles in kGated and kDx, 82 % in kDw; 1.91 PFLOP/s in that case,
+// SMs' active cycles in kGated and kDx, 81 % in kDw; 1.91 PFLOP/s in that case,
 // 1.66 where passes follow each other for long and the card is at its power
 // cap), without pairs shared memory, whose 128 bytes a cycle serve the copies
 // and the products (96 KB for a block's 512 cycles). Of e4m3 with many rows
