@@ -137,7 +137,8 @@ def _normal(gen, *shape, std=1.0):
 
 def _quantised(v):
     """int8 codes and fp32 scales amax/127 of each row of a matrix, of 32-bit values."""
-    s = v.abs().amax(-1) / INT8_MAX
+    amax = v.abs().amax(-1)
+    s = amax / torch.full_like(amax, INT8_MAX)  # a quotient: by a number it would be a product
     q = torch.where(s[..., None] > 0, v / s[..., None], 0.0)
     return torch.round(q).to(torch.int8), s
 
