@@ -17,6 +17,7 @@ from . import build as _build
 
 MOE_BF16 = 0
 MOE_FP8_E4M3 = 1
+MOE_INT8 = 2
 MOE_STATUS_BAD_EXPERT_ID = 0x1
 MOE_STATUS_TIMEOUT = 0x2
 MOE_STATUS_SLOT_OVERFLOW = 0x4
@@ -418,12 +419,12 @@ _types = None
 
 def _element_types():
     """The tensor types of bf16 values, e4m3 codes (as bytes, or as torch's own type), fp32
-    values and int32 offsets."""
+    values, int32 offsets and int8 codes."""
     global _types
     if _types is None:
         import torch
         _types = ((torch.bfloat16,), (torch.uint8, torch.float8_e4m3fn), (torch.float32,),
-                  (torch.int32,))
+                  (torch.int32,), (torch.int8,))
     return _types
 
 
@@ -444,7 +445,7 @@ def moe_combine_backward(h: Handle, dout, y, w, dy, dw, stream=None) -> None:
     every row that it can name."""
     c = h.cfg
     T, rows_h = c.num_ranks * c.tokens_per_rank, h.rows * c.hidden
-    bf16, _, fp32, _ = _element_types()
+    bf16, _, fp32, _, _ = _element_types()
     _check("moe_combine_backward", load_library().moe_combine_backward(
         h.ptr, _buf("dout", dout, T * c.hidden, bf16), _buf("y", y, rows_h, bf16),
         _buf("w", w, T * c.top_k, fp32), _buf("dy", dy, rows_h, bf16),
@@ -467,13 +468,18 @@ class ExpertHandle:
     def __init__(self, cfg: moe_expert_config_t, workspace):
         self.cfg = cfg
         self.workspace = workspace
-        self.fp8 = cfg.dtype == MOE_FP8_E4M3
+        self.fp8, self.int8 = cfg.dtype == MOE_FP8_E4M3, cfg.dtype == MOE_INT8
         E, H, F, R = cfg.num_experts, cfg.hidden, cfg.inter, cfg.rows_max
         #: elements that each tensor must hold, and their types
         self.offsets, self.rows_h, self.rows_f = E + 1, R * H, R * F
         self.w13, self.w2 = E * 2 * F * H, E * H * F
-        self.bf16, codes, self.fp32, self.int32 = _element_types()
-        self.elt = codes if self.fp8 else self.bf16
+        #: scales: of a row's 128 channels and a weight's 128 x 128 blocks, or of a row and a
+        #: weight's output channel
+        self.s_h, self.s_f = (R, R) if self.int8 else (R * H // 128, R * F // 128)
+        self.s13, self.s2 = ((E * 2 * F, E * H) if self.int8 else
+                             (self.w13 // 128 // 128, self.w2 // 128 // 128))
+        self.bf16, e4m3, self.fp32, self.int32, int8 = _element_types()
+        self.elt = e4m3 if self.fp8 else int8 if self.int8 else self.bf16
         h = _c_void_p()
         _check("moe_expert_create", load_library().moe_expert_create(
             ctypes.byref(cfg), _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -508,9 +514,9 @@ def moe_expert_create(cfg: moe_expert_config_t, workspace=None, device=None) -> 
 
 
 def _scale(name: str, x: ExpertHandle, t, count: int) -> Optional[int]:
-    if t is None and not x.fp8:
+    if t is None and not (x.fp8 or x.int8):
         return None
-    return _buf(name, t, count // 128, x.fp32)
+    return _buf(name, t, count, x.fp32)
 
 
 def moe_expert_gated(x: ExpertHandle, expert_offset, inp, inp_scale, w13, w13_scale, hid,
@@ -519,9 +525,9 @@ def moe_expert_gated(x: ExpertHandle, expert_offset, inp, inp_scale, w13, w13_sc
     elt = x.elt
     _check("moe_expert_gated", load_library().moe_expert_gated(
         x.ptr, _buf("expert_offset", expert_offset, x.offsets, x.int32),
-        _buf("inp", inp, x.rows_h, elt), _scale("inp_scale", x, inp_scale, x.rows_h),
-        _buf("w13", w13, x.w13, elt), _scale("w13_scale", x, w13_scale, x.w13 // 128),
-        _buf("hid", hid, x.rows_f, elt), _scale("hid_scale", x, hid_scale, x.rows_f),
+        _buf("inp", inp, x.rows_h, elt), _scale("inp_scale", x, inp_scale, x.s_h),
+        _buf("w13", w13, x.w13, elt), _scale("w13_scale", x, w13_scale, x.s13),
+        _buf("hid", hid, x.rows_f, elt), _scale("hid_scale", x, hid_scale, x.s_f),
         _buf("gate_up", gate_up, 2 * x.rows_f, x.bf16, optional=True), _stream(stream)))
 
 
@@ -531,8 +537,8 @@ def moe_expert_down(x: ExpertHandle, expert_offset, hid, hid_scale, w2, w2_scale
     elt = x.elt
     _check("moe_expert_down", load_library().moe_expert_down(
         x.ptr, _buf("expert_offset", expert_offset, x.offsets, x.int32),
-        _buf("hid", hid, x.rows_f, elt), _scale("hid_scale", x, hid_scale, x.rows_f),
-        _buf("w2", w2, x.w2, elt), _scale("w2_scale", x, w2_scale, x.w2 // 128),
+        _buf("hid", hid, x.rows_f, elt), _scale("hid_scale", x, hid_scale, x.s_f),
+        _buf("w2", w2, x.w2, elt), _scale("w2_scale", x, w2_scale, x.s2),
         _buf("y", y, x.rows_h, x.bf16), _stream(stream)))
 
 

@@ -24,12 +24,15 @@ int validate(const moe_config_t* c) {
     return MOE_ERR_INVALID_ARG;
   if (c->num_experts % c->num_ranks != 0) return MOE_ERR_INVALID_ARG;
   if (c->top_k > c->num_experts) return MOE_ERR_INVALID_ARG;
-  if (c->dispatch_dtype != MOE_BF16 && c->dispatch_dtype != MOE_FP8_E4M3) return MOE_ERR_INVALID_ARG;
+  if (c->dispatch_dtype != MOE_BF16 && c->dispatch_dtype != MOE_FP8_E4M3 &&
+      c->dispatch_dtype != MOE_INT8)
+    return MOE_ERR_INVALID_ARG;
   if (c->combine_dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
   if (c->num_experts > MOE_MAX_EXPERTS || c->top_k > MOE_MAX_TOPK || c->num_ranks > MOE_MAX_RANKS)
     return MOE_ERR_UNSUPPORTED;
   if (c->hidden % 8 != 0) return MOE_ERR_UNSUPPORTED;
   if (c->dispatch_dtype == MOE_FP8_E4M3 && c->hidden % 128 != 0) return MOE_ERR_UNSUPPORTED;
+  if (c->dispatch_dtype == MOE_INT8 && c->hidden % 16 != 0) return MOE_ERR_UNSUPPORTED;
   const long long T = (long long)c->num_ranks * c->tokens_per_rank;
   if (T * c->top_k >= (1ll << 31) - 1) return MOE_ERR_UNSUPPORTED;  // int32 row indices
   // The layout kernels keep their per-warp counters and the per-(source,
@@ -428,9 +431,10 @@ static int dispatch_range(moe_handle_t h, long long g0, long long g1, const void
   if (!h || !x || !w || !recv_x || !meta) return MOE_ERR_INVALID_ARG;
   if (!meta->local_expert || !meta->src_rank || !meta->src_token || !meta->slot || !meta->weight)
     return MOE_ERR_INVALID_ARG;
-  const bool fp8 = h->cfg.dispatch_dtype == MOE_FP8_E4M3;
-  if (fp8 && !recv_scale) return MOE_ERR_INVALID_ARG;
+  const int dtype = h->cfg.dispatch_dtype;
+  if (dtype != MOE_BF16 && !recv_scale) return MOE_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(recv_x, 16)) return MOE_ERR_INVALID_ARG;
+  if (dtype == MOE_INT8 && !aligned(recv_scale, 4)) return MOE_ERR_INVALID_ARG;
   if (h->layout_gen == 0) return MOE_ERR_STATE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // the whole layer into the compact receive rows right after a layout laid
@@ -491,7 +495,7 @@ static int dispatch_range(moe_handle_t h, long long g0, long long g1, const void
     a.tab = tables_args(h);  // the per-source tables, from the totals
     a.tab_ctas = h->cfg.num_ranks;
   }
-  const int rc = cuda_rc(moe::launch_dispatch(a, fp8, h->num_sms, st));
+  const int rc = cuda_rc(moe::launch_dispatch(a, dtype, h->num_sms, st));
   if (rc == MOE_OK) {
     h->dispatch_gen = h->layout_gen;
     h->tables_pending = 0;
@@ -516,8 +520,11 @@ int moe_dispatch_two_stage(moe_handle_t h, const void* x, const float* w, void* 
   if (!h || !x || !w || !send_x || !recv_x || !meta) return MOE_ERR_INVALID_ARG;
   if (!meta->local_expert || !meta->src_rank || !meta->src_token || !meta->slot || !meta->weight)
     return MOE_ERR_INVALID_ARG;
-  const bool fp8 = h->cfg.dispatch_dtype == MOE_FP8_E4M3;
-  if (fp8 && (!recv_scale || !send_scale)) return MOE_ERR_INVALID_ARG;
+  const int dtype = h->cfg.dispatch_dtype;
+  const bool scaled = dtype != MOE_BF16;
+  if (scaled && (!recv_scale || !send_scale)) return MOE_ERR_INVALID_ARG;
+  if (dtype == MOE_INT8 && (!aligned(recv_scale, 4) || !aligned(send_scale, 4)))
+    return MOE_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(recv_x, 16) || !aligned(send_x, 16)) return MOE_ERR_INVALID_ARG;
   if (h->layout_gen == 0) return MOE_ERR_STATE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -557,11 +564,11 @@ int moe_dispatch_two_stage(moe_handle_t h, const void* x, const float* w, void* 
   a.recv_offset = h->recv_offset;
   a.status = h->status;
   a.row_limit = h->rows_max;
-  rc = cuda_rc(moe::launch_dispatch(a, fp8, h->num_sms, st));
+  rc = cuda_rc(moe::launch_dispatch(a, dtype, h->num_sms, st));
   if (rc != MOE_OK) return rc;
   moe::A2avArgs c{};
   c.send = send_x;
-  c.send_scale = fp8 ? send_scale : nullptr;
+  c.send_scale = scaled ? send_scale : nullptr;
   c.recv = recv_x;
   c.recv_scale = recv_scale;
   c.expert_offset = h->expert_offset;
@@ -569,10 +576,10 @@ int moe_dispatch_two_stage(moe_handle_t h, const void* x, const float* w, void* 
   c.send_pos = h->send_pos;
   c.src_base = h->src_base;
   c.rows_max = h->rows_max;
-  c.row_bytes = (long long)h->cfg.hidden * (fp8 ? 1 : 2);
+  c.row_bytes = (long long)h->cfg.hidden * (scaled ? 1 : 2);
   c.P = h->cfg.num_ranks;
   c.E = h->cfg.num_experts;
-  c.nblk = h->cfg.hidden / 128;
+  c.nblk = dtype == MOE_INT8 ? 1 : h->cfg.hidden / 128;
   c.status = h->status;
   rc = cuda_rc(moe::launch_a2av(c, h->num_sms, st));
   if (rc == MOE_OK) {
@@ -602,6 +609,7 @@ int moe_dispatch_allgather(moe_handle_t h, const void* x, const float* w, void* 
   if (!h || !x || !w || !gathered_x || !recv_x || !meta) return MOE_ERR_INVALID_ARG;
   if (!meta->local_expert || !meta->src_rank || !meta->src_token || !meta->slot || !meta->weight)
     return MOE_ERR_INVALID_ARG;
+  if (h->cfg.dispatch_dtype == MOE_INT8) return MOE_ERR_UNSUPPORTED;
   const bool fp8 = h->cfg.dispatch_dtype == MOE_FP8_E4M3;
   if (fp8 && (!recv_scale || !gathered_scale)) return MOE_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(recv_x, 16) || !aligned(gathered_x, 16))
@@ -661,6 +669,7 @@ int moe_layout_dispatch_fused(moe_handle_t h, const float* logits, int32_t* ids,
   if (!h || !ids || !w || !x || !recv_x || !meta) return MOE_ERR_INVALID_ARG;
   if (!meta->local_expert || !meta->src_rank || !meta->src_token || !meta->slot || !meta->weight)
     return MOE_ERR_INVALID_ARG;
+  if (h->cfg.dispatch_dtype == MOE_INT8) return MOE_ERR_UNSUPPORTED;
   const bool fp8 = h->cfg.dispatch_dtype == MOE_FP8_E4M3;
   const bool route = logits != nullptr;
   if (fp8 && !recv_scale) return MOE_ERR_INVALID_ARG;
@@ -740,9 +749,10 @@ int moe_layout_dispatch_fused(moe_handle_t h, const float* logits, int32_t* ids,
 int moe_expert_standin(moe_handle_t h, const void* recv_x, const float* recv_scale,
                        const float* expert_scale, void* y, void* stream) {
   if (!h || !recv_x || !y) return MOE_ERR_INVALID_ARG;
-  const bool fp8 = h->cfg.dispatch_dtype == MOE_FP8_E4M3;
-  if (fp8 && !recv_scale) return MOE_ERR_INVALID_ARG;
+  const int dtype = h->cfg.dispatch_dtype;
+  if (dtype != MOE_BF16 && !recv_scale) return MOE_ERR_INVALID_ARG;
   if (!aligned(recv_x, 16) || !aligned(y, 16)) return MOE_ERR_INVALID_ARG;
+  if (dtype == MOE_INT8 && !aligned(recv_scale, 4)) return MOE_ERR_INVALID_ARG;
   if (h->dispatch_gen == 0 || h->dispatch_gen != h->layout_gen) return MOE_ERR_STATE;
   moe::StandinArgs a{};
   a.recv = recv_x;
@@ -753,7 +763,7 @@ int moe_expert_standin(moe_handle_t h, const void* recv_x, const float* recv_sca
   a.rows_max = h->rows_max;
   a.E = h->cfg.num_experts;
   a.H = h->cfg.hidden;
-  a.fp8 = fp8 ? 1 : 0;
+  a.dtype = dtype;
   a.status = h->status;
   if (h->fixed_rows) {  // the filled rows of every slot region, found through inv
     a.inv = h->inv;
@@ -823,9 +833,10 @@ int moe_expert_standin_tokens(moe_handle_t h, int64_t token_begin, int64_t token
                               const float* expert_scale, void* y, void* stream) {
   if (!h || !recv_x || !y || token_begin < 0 || token_end > h->T || token_begin > token_end)
     return MOE_ERR_INVALID_ARG;
-  const bool fp8 = h->cfg.dispatch_dtype == MOE_FP8_E4M3;
-  if (fp8 && !recv_scale) return MOE_ERR_INVALID_ARG;
+  const int dtype = h->cfg.dispatch_dtype;
+  if (dtype != MOE_BF16 && !recv_scale) return MOE_ERR_INVALID_ARG;
   if (!aligned(recv_x, 16) || !aligned(y, 16)) return MOE_ERR_INVALID_ARG;
+  if (dtype == MOE_INT8 && !aligned(recv_scale, 4)) return MOE_ERR_INVALID_ARG;
   if (h->dispatch_gen == 0 || h->dispatch_gen != h->layout_gen) return MOE_ERR_STATE;
   moe::StandinArgs a{};
   a.inv = h->inv;
@@ -840,7 +851,7 @@ int moe_expert_standin_tokens(moe_handle_t h, int64_t token_begin, int64_t token
   a.rows_max = h->rows_max;
   a.E = h->cfg.num_experts;
   a.H = h->cfg.hidden;
-  a.fp8 = fp8 ? 1 : 0;
+  a.dtype = dtype;
   a.status = h->status;
   if (h->fixed_rows) a.slot_rows = (long long)h->cfg.num_ranks * h->cfg.tokens_per_rank;
   return cuda_rc(moe::launch_standin_tokens(a, h->num_sms, static_cast<cudaStream_t>(stream)));

@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(128) k_standin(const StandinArgs p) {
     uint4* dst = reinterpret_cast<uint4*>(p.y + r * p.H);
     for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
       float f[8];
-      if (p.fp8) {
+      if (p.dtype == MOE_FP8_E4M3) {
         const uint2 q = reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.recv) + r * p.H)[v];
         const float s = __ldg(p.recv_scale + r * (p.H >> 7) + (v >> 4));
         const uint32_t qq[2] = {q.x, q.y};
@@ -159,6 +159,15 @@ __global__ void __launch_bounds__(128) k_standin(const StandinArgs p) {
           const __nv_fp8_storage_t byte = (__nv_fp8_storage_t)((qq[b >> 2] >> (8 * (b & 3))) & 0xffu);
           const __half_raw hr = __nv_cvt_fp8_to_halfraw(byte, __NV_E4M3);
           f[b] = __fmul_rn(c, __fmul_rn(__half2float(__half(hr)), s));
+        }
+      } else if (p.dtype == MOE_INT8) {
+        const uint2 q = reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.recv) + r * p.H)[v];
+        const float s = __ldg(p.recv_scale + r);
+        const uint32_t qq[2] = {q.x, q.y};
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+          const int code = (int)(qq[b >> 2] << (24 - 8 * (b & 3))) >> 24;
+          f[b] = __fmul_rn(c, __fmul_rn((float)code, s));
         }
       } else {
         const uint4 x = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.recv) + r * p.H)[v];
@@ -215,7 +224,7 @@ __global__ void __launch_bounds__(128) k_standin_tokens(const StandinArgs p) {
       uint4* dst = reinterpret_cast<uint4*>(p.y + r * p.H);
       for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
         float f[8];
-        if (p.fp8) {
+        if (p.dtype == MOE_FP8_E4M3) {
           const uint2 q = reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.recv) + r * p.H)[v];
           const float s = __ldg(p.recv_scale + r * (p.H >> 7) + (v >> 4));
           const uint32_t qq[2] = {q.x, q.y};
@@ -224,6 +233,15 @@ __global__ void __launch_bounds__(128) k_standin_tokens(const StandinArgs p) {
             const __nv_fp8_storage_t byte = (__nv_fp8_storage_t)((qq[b >> 2] >> (8 * (b & 3))) & 0xffu);
             const __half_raw hr = __nv_cvt_fp8_to_halfraw(byte, __NV_E4M3);
             f[b] = __fmul_rn(c, __fmul_rn(__half2float(__half(hr)), s));
+          }
+        } else if (p.dtype == MOE_INT8) {
+          const uint2 q = reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.recv) + r * p.H)[v];
+          const float s = __ldg(p.recv_scale + r);
+          const uint32_t qq[2] = {q.x, q.y};
+#pragma unroll
+          for (int b = 0; b < 8; ++b) {
+            const int code = (int)(qq[b >> 2] << (24 - 8 * (b & 3))) >> 24;
+            f[b] = __fmul_rn(c, __fmul_rn((float)code, s));
           }
         } else {
           const uint4 x = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.recv) + r * p.H)[v];

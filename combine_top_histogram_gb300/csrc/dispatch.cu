@@ -1,5 +1,6 @@
 // dispatch.cu -- permute + pack + all-to-all-v scatter, with optional fused
-// FP8 e4m3 quantisation (per token and 128-channel block, fp32 scale).
+// FP8 e4m3 quantisation (per token and 128-channel block, fp32 scale) or int8
+// quantisation (per token, fp32 scale).
 //
 // Pages: "[Infra-10] All-to-All Optimization", 4.3 (write the permutation
 // straight into the destination-contiguous communication buffer, no temporary
@@ -735,6 +736,94 @@ __global__ void __launch_bounds__(kDispatchThreads, 5) k_dispatch_fp8b(const Dis
   cp_async_wait_all();  // no copy outlives the CTA
 }
 
+// int8 rows: the scale is the whole token's, so its row is read into registers
+// (16 values a thread and chunk; H up to 2048 * CPT, beyond which the rest is
+// read again for the codes), the CTA's largest magnitude is taken in the
+// barrier that also publishes the token's receive rows, and the codes are
+// stored to those.
+template <int CPT, bool DIRECT>
+__global__ void __launch_bounds__(kDispatchThreads, 8) k_dispatch_int8(const DispatchArgs p) {
+  // the k receive rows of the current token and its warps' largest magnitudes; two buffers,
+  // alternating per token
+  __shared__ int rows_buf[2][MOE_MAX_TOPK];
+  __shared__ uint32_t amax_buf[2][kDispatchThreads / 32];
+  extern __shared__ int dsm[];  // tables CTAs and direct mode
+  const int nch = p.H >> 4;     // chunks of 16 values
+  const int tid = threadIdx.x;
+  bool waited = false, offsets_done = false;
+  unsigned ticket = 0u;
+  if ((int)blockIdx.x < p.tab_ctas) {
+    if (DIRECT) direct_tables_cta(p, dsm);
+    else tables_cta(p);
+    return;
+  }
+  const bool wide = (reinterpret_cast<uintptr_t>(p.x) & 31) == 0;
+  auto load = [&](const uint16_t* src, int c, uint4& a, uint4& b) {
+    if (c >= nch) {
+      a = b = make_uint4(0u, 0u, 0u, 0u);
+    } else if (wide) {
+      ld_stream32(src + 16 * c, a, b);
+    } else {
+      a = ld_stream(reinterpret_cast<const uint4*>(src + 16 * c));
+      b = ld_stream(reinterpret_cast<const uint4*>(src + 16 * c) + 1);
+    }
+  };
+  int par = 0;
+  const long long nb = gridDim.x - p.tab_ctas;
+  SlotIn si_next = DIRECT ? SlotIn{-1, 0.0f} : load_slot(p, p.g0 + blockIdx.x - p.tab_ctas);
+  for (long long g = p.g0 + blockIdx.x - p.tab_ctas; g < p.T; g += nb) {
+    int* rows_s = rows_buf[par];
+    SlotIn si = si_next;
+    if (!DIRECT && g + nb < p.T) si_next = load_slot(p, g + nb);
+    const uint16_t* src = p.x + g * p.H;
+    uint4 va[CPT], vb[CPT];
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) load(src, i * kDispatchThreads + tid, va[i], vb[i]);
+    if (!waited) {
+      pdl_wait();
+      pdl_trigger();
+      waited = true;
+    }
+    resolve_token<DIRECT>(p, g, rows_s, si, dsm, offsets_done);
+    if (DIRECT && g + nb >= p.T) ticket = direct_count_out(p);
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) m = absmax_bits(absmax_bits(m, va[i]), vb[i]);
+    for (int c = CPT * kDispatchThreads + tid; c < nch; c += kDispatchThreads) {
+      uint4 a, b;
+      load(src, c, a, b);
+      m = absmax_bits(absmax_bits(m, a), b);
+    }
+    m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+    if ((tid & 31) == 0) amax_buf[par][tid >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kDispatchThreads / 32; ++i) m = max(m, amax_buf[par][i]);
+    const float s = int8_scale(m);
+    if (tid < p.k && rows_s[tid] >= 0) p.recv_scale[rows_s[tid]] = s;
+    auto store = [&](int c, const uint4 code) {
+      for (int j = 0; j < p.k; ++j) {
+        const int r = rows_s[j];
+        if (r >= 0)
+          reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.recv) + (long long)r * p.H)[c] = code;
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+      const int c = i * kDispatchThreads + tid;
+      const uint4 code = int8_codes(va[i], vb[i], m, s);
+      if (c < nch) store(c, code);
+    }
+    for (int c = CPT * kDispatchThreads + tid; c < nch; c += kDispatchThreads) {
+      uint4 a, b;
+      load(src, c, a, b);
+      store(c, int8_codes(a, b, m, s));
+    }
+    par ^= 1;  // token n+2 rewrites these buffers only after token n+1's barrier
+  }
+  if (DIRECT) direct_end(p, ticket);
+}
+
 // AllGather comparator, stage 1: every token row (quantised once for FP8) is
 // written to all P ranks' gathered copies, rows d*T + g.
 template <bool FP8, int VPT>
@@ -854,7 +943,16 @@ cudaError_t launch_vec(const DispatchArgs& a, dim3 grid, dim3 block, size_t smem
   return launch_pdl(k_dispatch_bf16<8, DIRECT>, grid, block, smem, st, a);
 }
 
-cudaError_t launch_dispatch(const DispatchArgs& a, bool fp8, int num_sms, cudaStream_t st) {
+template <bool DIRECT>
+cudaError_t launch_int8(const DispatchArgs& a, dim3 grid, dim3 block, size_t smem, cudaStream_t st) {
+  const int nch = a.H >> 4;
+  if (nch <= 128) return launch_pdl(k_dispatch_int8<1, DIRECT>, grid, block, smem, st, a);
+  if (nch <= 256) return launch_pdl(k_dispatch_int8<2, DIRECT>, grid, block, smem, st, a);
+  return launch_pdl(k_dispatch_int8<4, DIRECT>, grid, block, smem, st, a);
+}
+
+cudaError_t launch_dispatch(const DispatchArgs& a, int dtype, int num_sms, cudaStream_t st) {
+  const bool fp8 = dtype == MOE_FP8_E4M3;
   long long blocks = a.T - a.g0 < 0 ? 0 : a.T - a.g0;
   const long long cap = (long long)num_sms * 16;  // 16 CTAs of 128 threads fill an SM
   if (blocks > cap) blocks = cap;
@@ -863,6 +961,9 @@ cudaError_t launch_dispatch(const DispatchArgs& a, bool fp8, int num_sms, cudaSt
   const dim3 grid((int)(blocks + a.tab_ctas)), block(kDispatchThreads);
   const size_t smem = a.direct ? (size_t)direct_smem_ints(a.E) * sizeof(int)
                       : a.tab_ctas > 0 ? (size_t)(a.tab.E + 32) * sizeof(int) : 0;
+  if (dtype == MOE_INT8)
+    return a.direct ? launch_int8<true>(a, grid, block, smem, st)
+                    : launch_int8<false>(a, grid, block, smem, st);
   if (fp8 && (reinterpret_cast<uintptr_t>(a.x) & 31) == 0) {
     const int nch = a.H >> 4;
     // at least 16 tokens per CTA and two rows fit in shared memory: stage rows

@@ -20,12 +20,12 @@ int validate(const moe_expert_config_t* c) {
   if (!c) return MOE_ERR_INVALID_ARG;
   if (c->num_experts < 1 || c->hidden < 1 || c->inter < 1 || c->rows_max < 1)
     return MOE_ERR_INVALID_ARG;
-  if (c->dtype != MOE_BF16 && c->dtype != MOE_FP8_E4M3) return MOE_ERR_INVALID_ARG;
+  if (c->dtype != MOE_BF16 && c->dtype != MOE_FP8_E4M3 && c->dtype != MOE_INT8)
+    return MOE_ERR_INVALID_ARG;
   if (c->train != 0 && c->train != 1) return MOE_ERR_INVALID_ARG;
-  const bool fp8 = c->dtype == MOE_FP8_E4M3;
-  const int unit = fp8 ? 128 : 8;
+  const int unit = c->dtype == MOE_FP8_E4M3 ? 128 : c->dtype == MOE_INT8 ? 16 : 8;
   if (c->num_experts > MOE_MAX_EXPERTS || c->hidden % unit != 0 || c->inter % unit != 0 ||
-      (fp8 && c->train))
+      (c->dtype != MOE_BF16 && c->train))
     return MOE_ERR_UNSUPPORTED;
   // int32 row indices with room for a tile past the end, and int32 columns of
   // the joint gate and up projection
@@ -42,7 +42,7 @@ int validate(const moe_expert_config_t* c) {
 }
 
 size_t workspace_bytes(const moe_expert_config_t* c) {
-  return kAlign + (c->train ? (size_t)c->rows_max * 2 * c->inter * 2 : 0);
+  return kAlign + (c->train || c->dtype == MOE_INT8 ? (size_t)c->rows_max * c->inter * 4 : 0);
 }
 
 moe::ExpertArgs expert_args(moe_expert_t x, const int32_t* offset) {
@@ -73,10 +73,11 @@ bool use_rows(moe_expert_t x, moe::ExpertOp op) {
 
 cudaError_t forward(moe_expert_t x, moe::ExpertOp op, const moe::ExpertArgs& a, const void* in,
                     const void* w, void* stream) {
-  const bool fp8 = x->cfg.dtype == MOE_FP8_E4M3;
+  const moe::ExpertType type = static_cast<moe::ExpertType>(x->cfg.dtype);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return use_rows(x, op) ? moe::launch_expert_rows(op, fp8, a, in, w, x->num_sms, st)
-                     : moe::launch_expert_gemm(op, fp8, a, in, w, x->num_sms, st);
+  return use_rows(x, op) || type == moe::kInt8
+             ? moe::launch_expert_rows(op, type, a, in, w, x->num_sms, st)
+             : moe::launch_expert_gemm(op, type == moe::kE4m3, a, in, w, x->num_sms, st);
 }
 
 }  // namespace
@@ -110,6 +111,9 @@ int moe_expert_create(const moe_expert_config_t* cfg, void* d_workspace, size_t 
   x->status = static_cast<uint32_t*>(d_workspace);
   x->dgu = cfg->train ? reinterpret_cast<uint16_t*>(static_cast<char*>(d_workspace) + kAlign)
                       : nullptr;
+  x->h32 = cfg->dtype == MOE_INT8
+               ? reinterpret_cast<float*>(static_cast<char*>(d_workspace) + kAlign)
+               : nullptr;
   x->wait_limit = 1ll << 32;
   *out = x;
   return MOE_OK;
@@ -124,9 +128,9 @@ int moe_expert_gated(moe_expert_t x, const int32_t* expert_offset, const void* i
                      const float* in_scale, const void* w13, const float* w13_scale, void* hid,
                      float* hid_scale, void* gate_up, void* stream) {
   if (!x || !expert_offset || !in || !w13 || !hid) return MOE_ERR_INVALID_ARG;
-  const bool fp8 = x->cfg.dtype == MOE_FP8_E4M3;
-  if (fp8 ? (!in_scale || !w13_scale || !hid_scale || gate_up)
-          : (in_scale || w13_scale || hid_scale))
+  const bool scaled = x->cfg.dtype != MOE_BF16;
+  if (scaled ? (!in_scale || !w13_scale || !hid_scale || gate_up)
+             : (in_scale || w13_scale || hid_scale))
     return MOE_ERR_INVALID_ARG;
   if (!aligned(in, 16) || !aligned(w13, 16) || !aligned(hid, 16) || !aligned(gate_up, 16) ||
       !aligned(expert_offset, 4) || !aligned(in_scale, 4) || !aligned(w13_scale, 4) ||
@@ -140,15 +144,21 @@ int moe_expert_gated(moe_expert_t x, const int32_t* expert_offset, const void* i
   a.out = hid;
   a.out_scale = hid_scale;
   a.gu_out = static_cast<uint16_t*>(gate_up);
-  return cuda_rc(forward(x, moe::kGated, a, in, w13, stream));
+  if (x->cfg.dtype != MOE_INT8) return cuda_rc(forward(x, moe::kGated, a, in, w13, stream));
+  a.out = x->h32;
+  cudaError_t e = forward(x, moe::kGated, a, in, w13, stream);
+  if (e == cudaSuccess)
+    e = moe::launch_expert_quantise(a, x->h32, static_cast<int8_t*>(hid), hid_scale, x->num_sms,
+                                    static_cast<cudaStream_t>(stream));
+  return cuda_rc(e);
 }
 
 int moe_expert_down(moe_expert_t x, const int32_t* expert_offset, const void* hid,
                     const float* hid_scale, const void* w2, const float* w2_scale, void* y,
                     void* stream) {
   if (!x || !expert_offset || !hid || !w2 || !y) return MOE_ERR_INVALID_ARG;
-  const bool fp8 = x->cfg.dtype == MOE_FP8_E4M3;
-  if (fp8 ? (!hid_scale || !w2_scale) : (hid_scale || w2_scale)) return MOE_ERR_INVALID_ARG;
+  const bool scaled = x->cfg.dtype != MOE_BF16;
+  if (scaled ? (!hid_scale || !w2_scale) : (hid_scale || w2_scale)) return MOE_ERR_INVALID_ARG;
   if (!aligned(hid, 16) || !aligned(w2, 16) || !aligned(y, 16) || !aligned(expert_offset, 4) ||
       !aligned(hid_scale, 4) || !aligned(w2_scale, 4))
     return MOE_ERR_INVALID_ARG;

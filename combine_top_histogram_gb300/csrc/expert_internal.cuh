@@ -19,6 +19,9 @@ enum ExpertOp : int {
   kDw = 4,     // W gradient: a^T b over the rows of a segment
 };
 
+// Types of the operands, by the C ABI's numbers.
+enum ExpertType : int { kBf16 = MOE_BF16, kE4m3 = MOE_FP8_E4M3, kInt8 = MOE_INT8 };
+
 struct ExpertArgs {
   const int32_t* offset;   // [E+1] first row of each segment
   int E;
@@ -29,9 +32,9 @@ struct ExpertArgs {
   int nt;                  // tiles along N
   int F;                   // kGated, kDgate: up columns start F after gate columns
   int a_box;               // rows of one row-operand copy
-  const float* sa;         // FP8: scales of the row operand [rows, K/128]
-  const float* sb;         // FP8: scales of the weights
-  void* out;
+  const float* sa;         // scales of the row operand: FP8 [rows, K/128], INT8 [rows]
+  const float* sb;         // scales of the weights: FP8 per 128 x 128, INT8 per channel
+  void* out;               // kGated, INT8: h in fp32 [rows, F]
   float* out_scale;        // kGated, FP8: scales of h [rows, F/128]
   uint16_t* gu_out;        // kGated, bf16: kept pre-activations [rows, 2F], or null
   const uint16_t* gu;      // kDgate: kept pre-activations
@@ -44,8 +47,11 @@ struct ExpertArgs {
 cudaError_t launch_expert_gemm(ExpertOp op, bool fp8, const ExpertArgs& args, const void* a,
                                const void* b, int num_sms, cudaStream_t st);
 // kGated or kDown for a few rows (expert_rows.cu).
-cudaError_t launch_expert_rows(ExpertOp op, bool fp8, const ExpertArgs& args, const void* a,
+cudaError_t launch_expert_rows(ExpertOp op, ExpertType type, const ExpertArgs& args, const void* a,
                                const void* b, int num_sms, cudaStream_t st);
+// INT8: codes [rows, F] and scales [rows] of the segments' rows of h (expert_quantise.cu).
+cudaError_t launch_expert_quantise(const ExpertArgs& args, const float* h, int8_t* codes,
+                                   float* scale, int num_sms, cudaStream_t st);
 // Opts the kernels in to their shared memory and checks their register split.
 cudaError_t expert_gemm_prepare();
 
@@ -59,5 +65,6 @@ struct moe_expert {
   int num_sms;
   uint32_t* status;
   uint16_t* dgu;           // [rows_max, 2F] (training only)
+  float* h32;              // [rows_max, F] (INT8 only)
   long long wait_limit;
 };

@@ -20,6 +20,9 @@
 // the row's and the weight block's fp32 scales before they are added. The 128
 // channels that share a scale of h are the S CTAs of one cluster, which
 // exchange their rows' largest magnitudes through distributed shared memory.
+// int8: codes become fp16 in registers (exact, and so are their products), 5
+// instructions for four; whole sums, then the row's and the channel's scale. h
+// leaves in fp32, for its scale is the whole row's (expert_quantise.cu).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -37,11 +40,16 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kAhead = 2;  // pieces loaded before the first product
 
-template <bool FP8>
+template <int TYPE>
 __device__ __forceinline__ void mma16x8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  if constexpr (FP8)
+  if constexpr (TYPE == kE4m3)
     asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else if constexpr (TYPE == kInt8)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -50,6 +58,26 @@ __device__ __forceinline__ void mma16x8(float (&c)[4], uint32_t a0, uint32_t a1,
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The products of 16 bytes of each of a lane's weight rows g and g + 8 with as
+// many of its receive row. int8 codes become fp16, four k of a word to one
+// product of 16 k.
+template <int TYPE>
+__device__ __forceinline__ void mma_piece(float (&c)[4], const uint4& a, const uint4& b,
+                                          const uint4& x) {
+  if constexpr (TYPE == kInt8) {
+    const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w},
+                   xw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint2 fa = int8_to_f16(aw[i]), fb = int8_to_f16(bw[i]), fx = int8_to_f16(xw[i]);
+      mma16x8<TYPE>(c, fa.x, fb.x, fa.y, fb.y, fx.x, fx.y);
+    }
+  } else {
+    mma16x8<TYPE>(c, a.x, b.x, a.y, b.y, x.x, x.y);
+    mma16x8<TYPE>(c, a.z, b.z, a.w, b.w, x.z, x.w);
+  }
 }
 
 __device__ __forceinline__ uint4 load_if(const uint8_t* p, bool ok) {
@@ -118,9 +146,10 @@ __device__ __forceinline__ Segment find_segment(const ExpertArgs& p, int a) {
   return found;
 }
 
-template <int OP, bool FP8, int S>
+template <int OP, int TYPE, int S>
 __global__ void __launch_bounds__(kThreads, 2)
     k_expert_rows(const ExpertArgs p, const void* a_rows, const void* weights) {
+  constexpr bool FP8 = TYPE == kE4m3, INT8 = TYPE == kInt8;
   constexpr bool kQuant = OP == kGated && FP8;
   constexpr int kGroups = kWarps / S;                       // pairs of groups of this CTA
   constexpr int kChannels = kGroups * (OP == kGated ? 16 : 32);
@@ -134,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int cta0 = (blockIdx.x % per_expert) * kChannels;  // the CTA's first channel
   const int c0 = cta0 + warp / S * (OP == kGated ? 16 : 32), ks = warp % S;
   // weight rows of this lane: g and g + 8 of each group of 16
-  const long long kbytes = (long long)p.K * (FP8 ? 1 : 2);
+  const long long kbytes = (long long)p.K * (TYPE == kBf16 ? 2 : 1);
   const int b_rows = OP == kGated ? 2 * p.F : p.N;
   const uint8_t* wp[4];
   bool w_ok[4];
@@ -193,9 +222,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           float(&d)[4] = FP8 ? v : acc[j];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint4 &a = w[u][2 * j][h], &b = w[u][2 * j + 1][h], &xv = x[u][h];
-            mma16x8<FP8>(d, a.x, b.x, a.y, b.y, xv.x, xv.y);
-            mma16x8<FP8>(d, a.z, b.z, a.w, b.w, xv.z, xv.w);
+            mma_piece<TYPE>(d, w[u][2 * j][h], w[u][2 * j + 1][h], x[u][h]);
           }
           if constexpr (FP8) {
 #pragma unroll
@@ -229,12 +256,22 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       const bool mine = r < rows && cta0 + ch < p.N;
       const long long o = (row0 + r) * p.N + cta0 + ch;
+      if constexpr (INT8) {  // whole sums of codes, then the row's and the channel's scales
+        if (mine) {
+          const float sr = __ldg(p.sa + row0 + r);
+          const float* sc = p.sb + (long long)seg.e * b_rows + cta0 + ch;
+          v = v * sr * __ldg(sc);
+          if (OP == kGated) v1 = v1 * sr * __ldg(sc + p.F);
+        }
+      }
       if constexpr (OP == kDown) {
         if (mine) static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(v);
       } else {
         out[i] = silu(v) * v1;
         if constexpr (kQuant) {  // the largest magnitude, by its bits: NaN is above all
           if (mine) atomicMax(&amax[r], __float_as_int(fabsf(out[i])));
+        } else if constexpr (INT8) {
+          if (mine) static_cast<float*>(p.out)[o] = out[i];
         } else if (mine) {
           static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(out[i]);
           if (p.gu_out) {
@@ -282,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-template <int OP, bool FP8, int S>
+template <int OP, int TYPE, int S>
 cudaError_t launch(long long grid, const ExpertArgs& p, const void* a, const void* b,
                    cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
@@ -297,11 +334,11 @@ cudaError_t launch(long long grid, const ExpertArgs& p, const void* a, const voi
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = OP == kGated && FP8 && S > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k_expert_rows<OP, FP8, S>, p, a, b);
+  cfg.numAttrs = OP == kGated && TYPE == kE4m3 && S > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, k_expert_rows<OP, TYPE, S>, p, a, b);
 }
 
-template <int OP, bool FP8>
+template <int OP, int TYPE>
 cudaError_t launch(const ExpertArgs& p, const void* a, const void* b, int num_sms,
                    cudaStream_t st) {
   const int channels = OP == kGated ? 16 : 32;  // of a warp
@@ -314,26 +351,33 @@ cudaError_t launch(const ExpertArgs& p, const void* a, const void* b, int num_sm
   // two, one token of E = 256, top-8, H = 7168, F = 2048: down e4m3 24.2 / 24.3 /
   // 26.0, gated e4m3 55.8 / 44.4 / 44.2); two where the split's CTAs form clusters, which cost more (E = 64,
   // H = 2048, F = 1024, top-2: 11.7 / 11.2 / 9.6).
-  const long long enough = (OP == kGated && FP8 ? 2ll : 3ll) * num_sms;
+  const long long enough = (OP == kGated && TYPE == kE4m3 ? 2ll : 3ll) * num_sms;
   int s = 1;
   while (s < 8 && ctas(s) < enough) s *= 2;
   switch (s) {
-    case 1: return launch<OP, FP8, 1>(ctas(1), p, a, b, st);
-    case 2: return launch<OP, FP8, 2>(ctas(2), p, a, b, st);
-    case 4: return launch<OP, FP8, 4>(ctas(4), p, a, b, st);
-    default: return launch<OP, FP8, 8>(ctas(8), p, a, b, st);
+    case 1: return launch<OP, TYPE, 1>(ctas(1), p, a, b, st);
+    case 2: return launch<OP, TYPE, 2>(ctas(2), p, a, b, st);
+    case 4: return launch<OP, TYPE, 4>(ctas(4), p, a, b, st);
+    default: return launch<OP, TYPE, 8>(ctas(8), p, a, b, st);
   }
 }
 
 }  // namespace
 
-cudaError_t launch_expert_rows(ExpertOp op, bool fp8, const ExpertArgs& p, const void* a,
+cudaError_t launch_expert_rows(ExpertOp op, ExpertType type, const ExpertArgs& p, const void* a,
                                const void* b, int num_sms, cudaStream_t st) {
-  if (op == kGated)
-    return fp8 ? launch<kGated, true>(p, a, b, num_sms, st)
-               : launch<kGated, false>(p, a, b, num_sms, st);
-  return fp8 ? launch<kDown, true>(p, a, b, num_sms, st)
-             : launch<kDown, false>(p, a, b, num_sms, st);
+  const bool gated = op == kGated;
+  switch (type) {
+    case kE4m3:
+      return gated ? launch<kGated, kE4m3>(p, a, b, num_sms, st)
+                   : launch<kDown, kE4m3>(p, a, b, num_sms, st);
+    case kInt8:
+      return gated ? launch<kGated, kInt8>(p, a, b, num_sms, st)
+                   : launch<kDown, kInt8>(p, a, b, num_sms, st);
+    default:
+      return gated ? launch<kGated, kBf16>(p, a, b, num_sms, st)
+                   : launch<kDown, kBf16>(p, a, b, num_sms, st);
+  }
 }
 
 }  // namespace moe

@@ -90,8 +90,8 @@ struct DispatchArgs {
   const int32_t* hist;    // [E][nchunks] exclusive chunk bases
   const int32_t* expert_offset;
   int32_t* inv;           // [T*k]
-  void* recv;             // bf16 [rows*H] or e4m3 [rows*H]
-  float* recv_scale;      // [rows*H/128] (FP8)
+  void* recv;             // bf16, e4m3 or int8 [rows*H]
+  float* recv_scale;      // [rows*H/128] (FP8), [rows] (INT8)
   int32_t* m_local_expert;
   int32_t* m_src_rank;
   int32_t* m_src_token;
@@ -158,7 +158,7 @@ struct AllGatherArgs {
 
 struct A2avArgs {
   const void* send;          // send pool rows
-  const float* send_scale;   // FP8 scale rows of the send pool, or null
+  const float* send_scale;   // scale rows of the send pool (nblk each), or null
   void* recv;
   float* recv_scale;
   const int32_t* expert_offset;
@@ -201,13 +201,13 @@ struct StandinArgs {
   const int32_t* inv;      // token-range form: rows of assignments [a0, a1)
   long long a0, a1;
   int k;
-  const void* recv;        // bf16 or e4m3 [rows*H]
-  const float* recv_scale; // FP8 scales
+  const void* recv;        // bf16, e4m3 or int8 [rows*H]
+  const float* recv_scale; // scales of FP8 or INT8 rows
   const float* expert_scale; // [E] or null
   const int32_t* expert_offset; // [E+1]
   uint16_t* y;
   long long rows_max;
-  int E, H, fp8;
+  int E, H, dtype;         // dtype: MOE_BF16, MOE_FP8_E4M3 or MOE_INT8
   long long slot_rows;     // fixed-slot layout: rows per expert region (P*T_r); 0 = compact
   uint32_t* status;        // MOE_STATUS_BOUNDS (debug bounds checks)
 };
@@ -272,7 +272,8 @@ size_t layout_smem_bytes(int E, int tpc, int k, int P);
 size_t scan_smem_bytes(int E, int P);
 cudaError_t layout_prepare(int E, int tpc, int k, int P);
 cudaError_t layout_prepare_all(size_t* layout_dyn_max, size_t* scan_dyn_max);
-cudaError_t launch_dispatch(const DispatchArgs& a, bool fp8, int num_sms, cudaStream_t st);
+// dtype: MOE_BF16, MOE_FP8_E4M3 or MOE_INT8
+cudaError_t launch_dispatch(const DispatchArgs& a, int dtype, int num_sms, cudaStream_t st);
 cudaError_t launch_tables(const TablesArgs& t, cudaStream_t st);
 cudaError_t launch_combine(const CombineArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_combine_backward(const CombineBackwardArgs& a, int num_sms, cudaStream_t st);

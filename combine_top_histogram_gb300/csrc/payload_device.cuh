@@ -162,6 +162,61 @@ __device__ __forceinline__ uint4 quant16(const uint4 a, const uint4 b, float s, 
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
+// ---- int8 codes of a whole row ---------------------------------------------
+// Scale of a row whose largest magnitude has the bf16 bits m (as integers
+// those order like the magnitudes, infinity above every number and NaN above
+// that): RN(m / 127), or m itself where it is infinite or NaN.
+__device__ __forceinline__ float int8_scale(uint32_t m) {
+  const float a = __uint_as_float(m << 16);
+  return m >= 0x7f80u ? a : __fdiv_rn(a, 127.0f);
+}
+
+// Largest magnitude of 8 bf16 values, by their bits, folded into m (two
+// 16-bit maxima in one word).
+__device__ __forceinline__ uint32_t absmax_bits(uint32_t m, const uint4 x) {
+  const uint32_t k = 0x7fff7fffu;
+  return __vmaxu2(__vmaxu2(m, __vmaxu2(x.x & k, x.y & k)), __vmaxu2(x.z & k, x.w & k));
+}
+
+// int8 codes of 16 bf16 values (in order) of a row with amax bits m and scale
+// s: the fp32 quotient x / s rounded to an integer, ties to even. The quotient
+// comes from one correction of the product by the reciprocal, as in
+// quant_words; for s = RN(m / 127) it is the IEEE quotient for every bf16 m from
+// 2^-64 up and every bf16 |x| <= m whose quotient is 2^-20 or more, below which
+// the code is 0 either way (tests/int8_emulation.c: all values of every row
+// whose amax has an exponent at an end of the range, or one of some inside it).
+// Adding 1.5 * 2^23 rounds it to an integer, whose low byte is the code.
+__device__ __forceinline__ uint4 int8_codes(const uint4 a, const uint4 b, uint32_t m, float s) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t out[4] = {0u, 0u, 0u, 0u};
+  if (m == 0u || m >= 0x7f80u) return make_uint4(0u, 0u, 0u, 0u);
+  const bool quick = m >= 0x1F80u;  // 2^-64: the reciprocal far from overflow
+  const float y = quick ? __frcp_rn(s) : 0.0f;
+  const unsigned long long y2 = f32x2(y, y), ns2 = f32x2(-s, -s);
+  const float big = 12582912.0f;
+#pragma unroll
+  for (int q = 0; q < 8; q += 2) {
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float lo = bf16_lo(w[q + i]), hi = bf16_hi(w[q + i]);
+      if (quick) {
+        const unsigned long long x2 = f32x2(lo, hi);
+        const unsigned long long q0 = mul_f32x2(x2, y2);
+        const unsigned long long qq = fma_f32x2(fma_f32x2(ns2, q0, x2), y2, q0);
+        c[2 * i] = __float_as_uint(__fadd_rn(__uint_as_float((uint32_t)qq), big));
+        c[2 * i + 1] = __float_as_uint(__fadd_rn(__uint_as_float((uint32_t)(qq >> 32)), big));
+      } else {
+        c[2 * i] = __float_as_uint(__fadd_rn(__fdiv_rn(lo, s), big));
+        c[2 * i + 1] = __float_as_uint(__fadd_rn(__fdiv_rn(hi, s), big));
+      }
+    }
+    out[q >> 1] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040),
+                              0x5410);
+  }
+  return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
 // Per-lane bf16 maximum of two bf16x2 words (one instruction); a NaN lane
 // yields the other operand, as fmaxf does.
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {

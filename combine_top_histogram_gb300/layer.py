@@ -18,7 +18,8 @@ class ExpertBlock:
     between the two products (and, for training, what the backward pass needs).
 
     w13 [E, 2F, H] (the F gate rows, then the F up rows) and w2 [E, H, F]: bf16,
-    or e4m3 codes (uint8) with fp32 scales for each 128 x 128 block.
+    e4m3 codes (uint8) with fp32 scales for each 128 x 128 block, or int8 codes
+    with fp32 scales for each output channel ([E, 2F] and [E, H]).
     """
 
     def __init__(self, w13, w2, rows: int, w13_scale=None, w2_scale=None, train: bool = False):
@@ -29,23 +30,27 @@ class ExpertBlock:
             raise ValueError(f"w13 {tuple(w13.shape)} and w2 {tuple(w2.shape)} do not belong "
                              "together: expected [E, 2F, H] and [E, H, F]")
         codes = (torch.uint8, torch.float8_e4m3fn)
-        self.fp8 = w13.dtype in codes
-        if w13.dtype not in (*codes, torch.bfloat16) or w2.dtype not in (
-                codes if self.fp8 else (torch.bfloat16,)):
-            raise ValueError(f"weights of {w13.dtype} and {w2.dtype}: both are bfloat16, or both "
-                             "e4m3 codes (uint8 or float8_e4m3fn)")
-        if self.fp8 and (w13_scale is None or w2_scale is None):
-            raise ValueError("e4m3 weights need their scales")
+        self.fp8, self.int8 = w13.dtype in codes, w13.dtype == torch.int8
+        if w13.dtype not in (*codes, torch.int8, torch.bfloat16) or w2.dtype not in (
+                codes if self.fp8 else (w13.dtype,)):
+            raise ValueError(f"weights of {w13.dtype} and {w2.dtype}: both are bfloat16, both "
+                             "e4m3 codes (uint8 or float8_e4m3fn), or both int8 codes")
+        if (self.fp8 or self.int8) and (w13_scale is None or w2_scale is None):
+            raise ValueError("e4m3 and int8 weights need their scales")
         self.w13, self.w2, self.w13_scale, self.w2_scale = w13, w2, w13_scale, w2_scale
         self.rows, self.train = rows, train
         self.handle = B.moe_expert_create(B.make_expert_config(
-            self.E, self.H, self.F, rows, B.MOE_FP8_E4M3 if self.fp8 else B.MOE_BF16, train),
+            self.E, self.H, self.F, rows,
+            B.MOE_FP8_E4M3 if self.fp8 else B.MOE_INT8 if self.int8 else B.MOE_BF16, train),
             device=w13.device)
         bf = dict(dtype=torch.bfloat16, device=w13.device)
         if self.fp8:
             self.hid = torch.empty((rows, self.F), dtype=torch.uint8, device=w13.device)
             self.hid_scale = torch.empty((rows, self.F // 128), dtype=torch.float32,
                                          device=w13.device)
+        elif self.int8:
+            self.hid = torch.empty((rows, self.F), dtype=torch.int8, device=w13.device)
+            self.hid_scale = torch.empty(rows, dtype=torch.float32, device=w13.device)
         else:
             self.hid, self.hid_scale = torch.empty((rows, self.F), **bf), None
         self.gate_up = torch.empty((rows, 2 * self.F), **bf) if train else None
@@ -86,18 +91,13 @@ class MoeLayer:
         import torch
         self.P, self.Tr, self.E, self.k, self.H = P, Tr, E, k, H
         self.T = P * Tr
-        self.fp8 = dispatch_dtype == B.MOE_FP8_E4M3
+        self.fp8, self.int8 = dispatch_dtype == B.MOE_FP8_E4M3, dispatch_dtype == B.MOE_INT8
         self.cfg = B.make_config(P, Tr, E, k, H, dispatch_dtype, cap)
         self.handle = B.moe_handle_create(self.cfg, device=device)
         self.rows = B.moe_recv_rows_max(self.cfg)
         dev = torch.device(device)
         rows, T = self.rows, self.T
-        if self.fp8:
-            self.recv_x = torch.empty((rows, H), dtype=torch.uint8, device=dev)
-            self.recv_scale = torch.empty((rows, H // 128), dtype=torch.float32, device=dev)
-        else:
-            self.recv_x = torch.empty((rows, H), dtype=torch.bfloat16, device=dev)
-            self.recv_scale = None
+        self.recv_x, self.recv_scale = self._rows(rows, dev)
         self.meta = {
             "local_expert": torch.empty(rows, dtype=torch.int32, device=dev),
             "src_rank": torch.empty(rows, dtype=torch.int32, device=dev),
@@ -114,9 +114,20 @@ class MoeLayer:
         self.experts = None  # an ExpertBlock in the stand-in's place
         self.grads = None    # backward's buffers, of experts built for training
 
+    def _rows(self, n: int, device):
+        """Buffers of n rows in the dispatch's type, and of their scales (None of bf16)."""
+        import torch
+        dt = torch.uint8 if self.fp8 else torch.int8 if self.int8 else torch.bfloat16
+        scale = None
+        if self.fp8 or self.int8:
+            scale = torch.empty((n, self.H // 128) if self.fp8 else (n,), dtype=torch.float32,
+                                device=device)
+        return torch.empty((n, self.H), dtype=dt, device=device), scale
+
     def set_experts(self, w13, w2, w13_scale=None, w2_scale=None, train: bool = False):
         """Gated feed-forward experts in the stand-in's place (None: the stand-in again).
-        Their type is the dispatch's: bf16, or e4m3 codes with 128 x 128 block scales.
+        Their type is the dispatch's: bf16, e4m3 codes with 128 x 128 block scales, or int8
+        codes with output-channel scales.
         Allocates what forward and backward need and waits for the device, so that both can
         follow on any stream and the former experts' buffers are free. Outside stream capture."""
         import torch
@@ -125,6 +136,8 @@ class MoeLayer:
                 torch.cuda.synchronize(self.out.device)
             self.experts = self.grads = None
             return None
+        if (w13.dtype == torch.int8) != self.int8:  # before their workspace, of int8 a large one
+            raise ValueError("the experts' type is that of the layer")
         experts = ExpertBlock(w13, w2, self.rows, w13_scale, w2_scale, train)
         if (experts.E, experts.H, experts.fp8) != (self.E, self.H, self.fp8):
             raise ValueError("the experts' number, width and type are those of the layer")
@@ -166,12 +179,10 @@ class MoeLayer:
             if rows == 0:
                 raise ValueError("fixed slots need a configuration without capacity")
             dev = self.out.device
-            sx = torch.empty((rows, self.H), dtype=torch.uint8 if self.fp8 else torch.bfloat16,
-                             device=dev)
+            sx, scale = self._rows(rows, dev)
             self.slots = {
                 "x": sx,
-                "scale": (torch.empty((rows, self.H // 128), dtype=torch.float32, device=dev)
-                          if self.fp8 else None),
+                "scale": scale,
                 "meta": {n: torch.empty(rows, dtype=torch.float32 if n == "weight" else torch.int32,
                                         device=dev)
                          for n in ("local_expert", "src_rank", "src_token", "slot", "weight")},
@@ -195,20 +206,18 @@ class MoeLayer:
 
     def dispatch_allgather(self, x, w, stream=None):
         """The AllGather comparator: all tokens to every rank, then a local filter."""
-        import torch
+        if self.int8:
+            raise ValueError("the AllGather comparator has no int8 form")
         if getattr(self, "gathered_x", None) is None:
-            dt = torch.uint8 if self.fp8 else torch.bfloat16
-            self.gathered_x = torch.empty((self.P * self.T, self.H), dtype=dt,
-                                          device=self.out.device)
-            self.gathered_scale = (torch.empty((self.P * self.T, self.H // 128),
-                                               dtype=torch.float32, device=self.out.device)
-                                   if self.fp8 else None)
+            self.gathered_x, self.gathered_scale = self._rows(self.P * self.T, self.out.device)
         B.moe_dispatch_allgather(self.handle, x, w, self.gathered_x, self.gathered_scale,
                                  self.recv_x, self.recv_scale, self.meta, stream)
         self.fixed = False
 
     def layout_dispatch_fused(self, x, ids=None, w=None, logits=None, stream=None):
         """One persistent launch: route (logits) or take ids/w, lay out, dispatch."""
+        if self.int8:
+            raise ValueError("the single-launch dispatch has no int8 form")
         if logits is not None:
             ids, w = self.ids, self.w
         B.moe_layout_dispatch_fused(self.handle, logits, ids, w, x, self.recv_x, self.recv_scale,

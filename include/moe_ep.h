@@ -75,12 +75,14 @@ extern "C" {
 /* ---- dtypes ------------------------------------------------------------ */
 #define MOE_BF16 0
 #define MOE_FP8_E4M3 1
+#define MOE_INT8 2  /* 8-bit integers with one fp32 scale for each row (token) and, of weights,
+                       for each output channel */
 
 /* ---- return codes -------------------------------------------------------- */
 #define MOE_OK 0
 #define MOE_ERR_INVALID_ARG (-1)  /* null pointer, negative size, E % P != 0, k > E ... */
 #define MOE_ERR_UNSUPPORTED (-2)  /* a size beyond the MOE_MAX_* limits, H % 8, FP8 with H % 128,
-                                     or layout tables beyond shared memory: about
+                                     INT8 with H % 16 or a call it does not have, or layout tables beyond shared memory: about
                                      (P+1)*E + P*P + 2*E > 40000 int32 */
 #define MOE_ERR_WORKSPACE (-3)    /* workspace too small or not 256-byte aligned */
 #define MOE_ERR_CUDA (-4)         /* a CUDA runtime call or launch failed */
@@ -103,8 +105,9 @@ typedef struct {
     int32_t tokens_per_rank; /* T_r >= 1 */
     int32_t num_experts;     /* E, a multiple of P, <= MOE_MAX_EXPERTS */
     int32_t top_k;           /* k, 1 <= k <= min(E, MOE_MAX_TOPK) */
-    int32_t hidden;          /* H, a multiple of 8; a multiple of 128 for FP8 */
-    int32_t dispatch_dtype;  /* MOE_BF16 or MOE_FP8_E4M3 (per-128-channel fp32 scales) */
+    int32_t hidden;          /* H, a multiple of 8; of 128 for FP8, of 16 for INT8 */
+    int32_t dispatch_dtype;  /* MOE_BF16, MOE_FP8_E4M3 (per-128-channel fp32 scales) or
+                                MOE_INT8 (per-token fp32 scales) */
     int32_t combine_dtype;   /* MOE_BF16 (the only combine dtype) */
     int32_t expert_capacity; /* per-expert row limit c; 0 = unlimited ([A2A] 8.1) */
 } moe_config_t;
@@ -241,6 +244,13 @@ int moe_get_layout(moe_handle_t h, moe_layout_view_t *out);
  * MOE_FP8_E4M3. recv_scale: fp32 [rows_max, H/128] for FP8 (per token and
  * 128-channel block: s = amax/448 in fp32, codes = e4m3 RNE satfinite of
  * x/s; an all-zero block has s = 0 and zero codes), NULL for BF16.
+ * MOE_INT8: recv_x holds int8 codes and recv_scale one fp32 per row
+ * [rows_max]: s = amax/127 over the token's H values in fp32, codes = x/s
+ * (fp32 quotient) rounded to the nearest integer, ties to even, in [-127, 127];
+ * an all-zero token has s = 0 and zero codes; one that holds an infinity or a
+ * NaN has that as its s (a NaN before an infinity) and zero codes, so that its
+ * values code * s are NaN. moe_dispatch_allgather and
+ * moe_layout_dispatch_fused do not have it (MOE_ERR_UNSUPPORTED).
  * meta: per-row metadata arrays. Also writes the layout's inv[T*k]. */
 int moe_dispatch(moe_handle_t h, const void *x, const float *w, void *recv_x,
                  float *recv_scale, const moe_recv_meta_t *meta, void *stream);
@@ -318,8 +328,8 @@ int moe_dispatch_two_stage(moe_handle_t h, const void *x, const float *w, void *
 
 /* a6 -- expert stand-in (the pages' grouped GEMM is out of scope): for every
  * kept receive row r of expert e, y[r] = bf16(c[e] * x_r), where x_r is the
- * bf16 payload (c = NULL means c[e] = 1) or, for FP8, the dequantised value
- * e4m3(q) * s. y: bf16 [rows_max, H]. Needs a preceding moe_dispatch with the
+ * bf16 payload (c = NULL means c[e] = 1) or, for FP8 and INT8, the
+ * dequantised value code * s. y: bf16 [rows_max, H]. Needs a preceding moe_dispatch with the
  * same recv_x / recv_scale. */
 int moe_expert_standin(moe_handle_t h, const void *recv_x, const float *recv_scale,
                        const float *expert_scale, void *y, void *stream);
@@ -413,6 +423,14 @@ int moe_combine_tokens(moe_handle_t h, int64_t token_begin, int64_t token_end, c
  * codes e4m3 RNE satfinite of h/s, an all-zero block has s = 0 and zero codes;
  * a NaN makes its block's s NaN); y is bf16. Sums are fp32; FP8 sums are exact products of codes added up
  * within each 128-channel block, then scaled and added in fp32.
+ * MOE_INT8 (serving): x, h, w13 and w2 are int8 codes (all 256 of them); x and
+ * h carry one fp32 scale per row (x_scale [rows_max], as moe_dispatch writes
+ * it, h_scale [rows_max]), the weights one per output channel (w13_scale
+ * [E, 2F], w2_scale [E, H]). Products of codes are added up in fp32, which is
+ * exact while every partial sum stays below 2^24 in magnitude (which takes 1024
+ * products of the largest codes at least), then multiplied by the two scales.
+ * h is held in fp32 and quantised with the dispatch's rule, over the F values
+ * of a row.
  * expert_offset is int32 [E+1] on the device: the layout's expert_offset of a
  * compact dispatch (moe_dispatch and its comparators; not the fixed-slot
  * layout, whose regions it does not describe), or the caller's own
@@ -424,9 +442,9 @@ int moe_combine_tokens(moe_handle_t h, int64_t token_begin, int64_t token_end, c
  * and on one handle must be ordered on one stream. */
 typedef struct {
     int32_t num_experts; /* E >= 1, <= MOE_MAX_EXPERTS */
-    int32_t hidden;      /* H, a multiple of 8; of 128 for FP8 */
-    int32_t inter;       /* F, a multiple of 8; of 128 for FP8 */
-    int32_t dtype;       /* MOE_BF16 or MOE_FP8_E4M3 */
+    int32_t hidden;      /* H, a multiple of 8; of 128 for FP8, of 16 for INT8 */
+    int32_t inter;       /* F, a multiple of 8; of 128 for FP8, of 16 for INT8 */
+    int32_t dtype;       /* MOE_BF16, MOE_FP8_E4M3 or MOE_INT8 */
     int64_t rows_max;    /* rows every row buffer holds (moe_recv_rows_max) */
     int32_t train;       /* 1: the handle also runs moe_expert_backward (MOE_BF16 only) */
 } moe_expert_config_t;
@@ -434,7 +452,8 @@ typedef struct {
 typedef struct moe_expert *moe_expert_t;
 
 /* Bytes of device workspace of a handle (0 if *cfg is invalid): control words
- * and, for training, the gradient of the pre-activations [rows_max, 2F]. */
+ * and, for training, the gradient of the pre-activations [rows_max, 2F], or,
+ * for INT8, h before its quantisation (fp32 [rows_max, F]). */
 size_t moe_expert_workspace_bytes(const moe_expert_config_t *cfg);
 
 /* Creates a handle over d_workspace (256-byte aligned, the caller's). As
