@@ -75,9 +75,9 @@ cudaError_t forward(moe_expert_t x, moe::ExpertOp op, const moe::ExpertArgs& a, 
                     const void* w, void* stream) {
   const moe::ExpertType type = static_cast<moe::ExpertType>(x->cfg.dtype);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return use_rows(x, op) || type == moe::kInt8
-             ? moe::launch_expert_rows(op, type, a, in, w, x->num_sms, st)
-             : moe::launch_expert_gemm(op, type == moe::kE4m3, a, in, w, x->num_sms, st);
+  if (use_rows(x, op)) return moe::launch_expert_rows(op, type, a, in, w, x->num_sms, st);
+  if (type == moe::kInt8) return moe::launch_expert_int8(op, a, in, w, x->num_sms, st);
+  return moe::launch_expert_gemm(op, type == moe::kE4m3, a, in, w, x->num_sms, st);
 }
 
 }  // namespace
@@ -99,7 +99,7 @@ int moe_expert_create(const moe_expert_config_t* cfg, void* d_workspace, size_t 
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-      moe::expert_gemm_prepare() != cudaSuccess ||
+      moe::expert_gemm_prepare() != cudaSuccess || moe::expert_int8_prepare() != cudaSuccess ||
       cudaMemset(d_workspace, 0, kAlign) != cudaSuccess ||
       cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess)  // before work on any stream
     return MOE_ERR_CUDA;

@@ -54,6 +54,7 @@
 #include "expert_internal.cuh"
 #include "expert_math.cuh"
 #include "expert_ptx.cuh"
+#include "expert_walk.cuh"
 #include "internal.cuh"
 
 namespace moe {
@@ -79,7 +80,6 @@ struct Plan {
   static constexpr int kEpiBytes = 8 * kWarpBytes;
 };
 constexpr int kMaxStages = 6;
-constexpr int kGroupM = 8;             // row tiles that share weight tiles in L2
 
 struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages];
@@ -110,152 +110,8 @@ constexpr int smem_bytes() {
   return bytes;
 }
 
-struct Tile {
-  int e;
-  int row0;     // this CTA's first row (kDw: first row of the segment)
-  int rows;     // rows of the segment from row0 on (kDw: the reduction length)
-  int m0;       // kDw: this CTA's first gradient row
-  int n0;       // column tile
-  int kb;       // reduction blocks
-};
-
-// The tiles of one CTA (or pair), in order: tile0, tile0 + step, ... of the
-// launch. Row tiles of one expert are taken in groups of kGroupM that walk the
-// columns together, so that concurrent CTAs share both operands in L2. Each
-// role walks for itself; a step costs two divisions and, within an expert or
-// to one of the next few, no search.
-// kDw's tiles take as long as their expert has rows. Where some have many more
-// than others, the experts come by falling rows (sort_segments) and every
-// second step goes backwards over the CTAs, so that those with the long tiles
-// of one step get the short ones of the next (Zipf(1.2) over 8 experts, 76
-// pairs: the last pair ends 7 and 6 % after the mean for dW2 and dW13 of the
-// skewed training layer, without 17 and 8 %; its backward pass 2640 / 2570 us).
-// Even ones keep the plain order, which costs less to walk (E = 64 of 256 rows
-// each: 464 / 480 us).
 template <int OP, int CG>
-struct Walk {
-  static constexpr int kRows = kTileM * CG;
-  const ExpertArgs& p;
-  const Shared& s;
-  const int k_elems, rank, first, step, mt_w;
-  int t, e, base, per;  // tile, its expert, the expert's first tile and tiles
-  int place = 0;        // kDw: the expert's place by falling rows
-  bool uneven, back = true;  // kDw: some experts' rows are many more; this step goes backwards
-
-  __device__ __forceinline__ Walk(const ExpertArgs& pa, const Shared& sh, int ke, int rk, int tile0,
-                                  int st)
-      : p(pa), s(sh), k_elems(ke), rank(rk), first(tile0), step(st),
-        mt_w(OP == kDw ? (pa.M + kRows - 1) / kRows : 0), t(tile0 - st), e(0), base(0) {
-    per = tiles(0);
-    uneven = OP == kDw && sh.uneven;
-    if (uneven) e = sh.pre[0];
-  }
-
-  __device__ __forceinline__ int tiles(int x) const {
-    return (OP == kDw ? mt_w : s.pre[x + 1] - s.pre[x]) * p.nt;
-  }
-
-  __device__ __forceinline__ bool next(Tile& o) {
-    t += step;
-    uint32_t local;  // tile of the expert
-    if (OP == kDw) {
-      int at = t;
-      if (uneven) {
-        back = !back;
-        if (back) at += step - 1 - 2 * first;
-      }
-      if (at >= mt_w * p.E * p.nt) return false;
-      if (at < base || at - base >= per) {
-        place = at / per;
-        base = place * per;
-        e = uneven ? s.pre[place] : place;
-      }
-      local = at - base;
-    } else {
-      if (t >= s.pre[p.E] * p.nt) return false;
-      for (int i = 0; i < 4 && t - base >= per; ++i) {
-        base += per;
-        per = tiles(++e);
-      }
-      if (t - base >= per) {
-        int lo = e, hi = p.E - 1;  // largest e with pre[e] * nt <= t
-        while (lo < hi) {
-          const int mid = (lo + hi + 1) >> 1;
-          if (s.pre[mid] * p.nt <= t) lo = mid;
-          else hi = mid - 1;
-        }
-        e = lo;
-        base = s.pre[e] * p.nt;
-        per = tiles(e);
-      }
-      local = t - base;
-    }
-    const int mt = OP == kDw ? mt_w : s.pre[e + 1] - s.pre[e];
-    const uint32_t group = kGroupM * p.nt;
-    const uint32_t g = local / group, idx = local - g * group;
-    const uint32_t gs = min(kGroupM, mt - (int)g * kGroupM);
-    const uint32_t n = gs == kGroupM ? idx / kGroupM : idx / gs;
-    const int m = (int)(g * kGroupM + idx - n * gs) * kRows + rank * kTileM;
-    o.e = e;
-    o.n0 = (int)n;
-    if (OP == kDw) {
-      o.row0 = s.off[e];
-      o.rows = s.off[e + 1] - o.row0;
-      o.m0 = m;
-      o.kb = (o.rows + 63) >> 6;
-    } else {
-      o.row0 = s.off[e] + m;
-      o.rows = s.off[e + 1] - o.row0;
-      o.m0 = 0;
-      o.kb = (p.K + k_elems - 1) / k_elems;
-    }
-    return true;
-  }
-};
-
-// The segments and the row tiles before each expert, once per CTA. Offsets
-// are held to [0, rows_max] and to ascending order, so no row index that
-// follows from them leaves a row buffer.
-template <int CG>
-__device__ __forceinline__ void load_segments(const ExpertArgs& p, Shared& s) {
-  for (int e = threadIdx.x; e <= p.E; e += kThreads) {
-    const long long o = p.offset[e];
-    s.off[e] = (int)(o < 0 ? 0 : o > p.rows_max ? p.rows_max : o);
-  }
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
-    int carry = 0, top = s.off[0];
-    for (int e0 = 0; e0 < p.E; e0 += 32) {
-      const int e = e0 + lane;
-      int end = e < p.E ? s.off[e + 1] : 0;
-      for (int d = 1; d < 32; d <<= 1) {  // running maximum: ascending ends
-        const int v = __shfl_up_sync(~0u, end, d);
-        if (lane >= d) end = max(end, v);
-      }
-      end = max(end, top);
-      int begin = __shfl_up_sync(~0u, end, 1);
-      if (lane == 0) begin = top;
-      top = __shfl_sync(~0u, end, 31);
-      const int n = e < p.E ? max(end - begin, 0) : 0;
-      const int tiles = (n + kTileM * CG - 1) / (kTileM * CG);
-      int sum = tiles;
-      for (int d = 1; d < 32; d <<= 1) {
-        const int v = __shfl_up_sync(~0u, sum, d);
-        if (lane >= d) sum += v;
-      }
-      __syncwarp();
-      if (e < p.E) {
-        s.pre[e] = carry + sum - tiles;
-        s.off[e + 1] = max(end, begin);
-      }
-      carry += __shfl_sync(~0u, sum, 31);
-      __syncwarp();
-    }
-    if (lane == 0) s.pre[p.E] = carry;
-  }
-  __syncthreads();
-}
+using Tiles = Walk<OP == kDw, kTileM * CG, Shared>;
 
 // kDw: whether some expert has more than 1.5 times the mean of the rows, among
 // up to 256 experts (of more, one expert's tiles weigh little) of more than two
@@ -671,7 +527,7 @@ __device__ __forceinline__ void settle_pair(Shared& s, int rank) {
 // the issuing warp of the same register share then missed: 2 % slower).
 template <int OP, int CG>
 __device__ __forceinline__ void scale_warp(const ExpertArgs& p, Shared& s, const WaitCtl& ctl,
-                                           Walk<OP, CG>& walk, int j) {
+                                           Tiles<OP, CG>& walk, int j) {
   constexpr int kAhead = 2;
   int as = 0;
   uint32_t ph = 1;
@@ -783,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (P::kOut) tma_prefetch_map(&map_c);
   }
   pdl_wait();  // the segments and the operands come from earlier kernels
-  load_segments<CG>(p, s);
+  load_segments<kTileM * CG, kThreads>(p, s);
   if constexpr (OP == kDw) sort_segments(p, s);
   tc_fence_before();
   if constexpr (kPair) cluster_sync();  // both CTAs' barriers exist
@@ -792,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = s.tmem;
   const WaitCtl ctl{&s.abort, kPair ? cluster_addr(smem_u32(&s.abort), rank ^ 1) : 0u, p.wait_limit,
                     p.status};
-  Walk<OP, CG> walk(p, s, kElems, rank, blockIdx.x / CG, gridDim.x / CG);
+  Tiles<OP, CG> walk(p, s, kElems, rank * kTileM, blockIdx.x / CG, gridDim.x / CG);
 
   if (warp < kEpiWarp0) {
     give_registers<FP8>();
@@ -1115,8 +971,8 @@ EncodeTiled encode_tiled() {
   return fn;
 }
 
-// A row-major tensor [planes][rows][cols] of bf16 or bytes; copies of
-// box_rows rows x 128 bytes, 128-byte swizzle, zeros outside.
+}  // namespace
+
 cudaError_t make_map(CUtensorMap* m, const void* base, bool fp8, long long cols, long long rows,
                      long long planes, int box_rows) {
   const EncodeTiled enc = encode_tiled();
@@ -1133,6 +989,8 @@ cudaError_t make_map(CUtensorMap* m, const void* base, bool fp8, long long cols,
           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return rc == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
+
+namespace {
 
 // Row tiles are at most one per `rows` rows plus one per segment; the host
 // knows no more.

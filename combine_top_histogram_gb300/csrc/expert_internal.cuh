@@ -3,6 +3,7 @@
 // Not installed; the public interface is include/moe_ep.h.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -52,8 +53,17 @@ cudaError_t launch_expert_rows(ExpertOp op, ExpertType type, const ExpertArgs& a
 // INT8: codes [rows, F] and scales [rows] of the segments' rows of h (expert_quantise.cu).
 cudaError_t launch_expert_quantise(const ExpertArgs& args, const float* h, int8_t* codes,
                                    float* scale, int num_sms, cudaStream_t st);
-// Opts the kernels in to their shared memory and checks their register split.
+// INT8: kGated (to fp32 h) or kDown on the tensor cores (expert_int8.cu).
+cudaError_t launch_expert_int8(ExpertOp op, const ExpertArgs& args, const void* a, const void* b,
+                               int num_sms, cudaStream_t st);
+// Opt the kernels in to their shared memory and check their register split.
 cudaError_t expert_gemm_prepare();
+cudaError_t expert_int8_prepare();
+
+// TMA map of a row-major tensor [planes][rows][cols] of bf16, or of bytes; copies of
+// box_rows rows x 128 bytes, 128-byte swizzle, zeros outside. planes = 0: two-dimensional.
+cudaError_t make_map(CUtensorMap* m, const void* base, bool bytes, long long cols, long long rows,
+                     long long planes, int box_rows);
 
 }  // namespace moe
 

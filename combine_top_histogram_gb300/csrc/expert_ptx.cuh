@@ -323,6 +323,36 @@ __device__ __forceinline__ void tc_loaded(uint32_t (&v)[32]) {
                  "+r"(v[30]), "+r"(v[31]));
 }
 
+// 16 consecutive columns of this warp's 32 lanes: column i of the thread's lane
+// = v[i]. Asynchronous until tc_wait_st.
+__device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tc_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Elected. One product of 16 k with A in tensor memory (fp16, two k a column).
+template <int CG>
+__device__ __forceinline__ void tc_mma_ta(uint32_t d, uint32_t a, uint64_t db, uint32_t idesc,
+                                          bool accumulate) {
+#define MOE_TC_MMA_TA(GROUP)                                                                       \
+  asm volatile("{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\t"                        \
+               "setp.ne.b32 p, %4, 0;\n\t"                                                         \
+               "@q tcgen05.mma.cta_group::" GROUP ".kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"( \
+                   d),                                                                             \
+               "r"(a), "l"(db), "r"(idesc), "r"((uint32_t)accumulate)                              \
+               : "memory")
+  if constexpr (CG == 2) MOE_TC_MMA_TA("2");
+  else MOE_TC_MMA_TA("1");
+#undef MOE_TC_MMA_TA
+}
+
 // Shared-memory descriptor of an operand tile with 128-byte swizzled rows.
 // K-major (lbo unused): rows of 128 bytes along K, 8-row groups sbo apart.
 // MN-major: lines of 128 bytes along M or N, one per k, groups of 8 k sbo
@@ -332,8 +362,8 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
          ((uint64_t)(sbo >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-// Instruction descriptor: fp32 accumulator, A and B of one type (bf16, or
-// e4m3), their majors, M and N.
+// Instruction descriptor: fp32 accumulator, A and B of one type (bf16; or the
+// first of the kind, e4m3 of f8f6f4 and fp16 of f16), their majors, M and N.
 __host__ __device__ constexpr uint32_t mma_desc(bool fp8, bool a_mn, bool b_mn, int M, int N) {
   return (1u << 4) | (fp8 ? 0u : (1u << 7) | (1u << 10)) | ((a_mn ? 1u : 0u) << 15) |
          ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
