@@ -9,29 +9,36 @@
 // below 2^24: the codes stay 8 bits wide in memory and on their way to the SM,
 // and become fp16 there.
 //
-// What that costs is shared memory's 128 bytes a cycle: 64 k of a CTA's 256
-// channels and 128 tokens are 512 cycles of products. The weights are therefore the A
-// operand, which the tensor cores can take from tensor memory: converted codes
-// go there straight from registers and use no shared memory again. Tokens are
-// the B operand: their fp16 has to be written to shared memory and read by the products.
+// What that costs is the 128 bytes a cycle between an SM's warps, its shared
+// memory and its tensor memory: stores to tensor memory count like those to
+// shared memory, and so do the products' reads of B (measured by leaving parts
+// out: the times follow the sum of the bytes to 5 %). For 64 k and n tokens,
+// whose products with 256 channels take 4 n cycles, that is
+//   weights (A)  16 KB in, 16 out to be converted, 32 of fp16 to tensor memory
+//   tokens (B)   64 n in, 64 n out, 128 n of fp16 to shared memory, 256 n for the
+//                products of two blocks of 128 channels
+// so tokens are many: 192, with 384 columns of accumulators and 128 of fp16
+// weights the tensor memory is full. 160 KB then stand beside 768 cycles of
+// products, at 128 tokens 128 KB beside 512. The weights are the A operand
+// because the tensor cores take that one from tensor memory: as fp16 in shared
+// memory they would be read there again. CTA pairs that share a tile of tokens
+// save only half of the tokens' conversion (the products of both SMs read all
+// of B): 452 / 424 us at 128 tokens (gated, E = 16, 512 rows each, H = 7168,
+// F = 2048), for a hand-over between the CTAs at every step.
 //
-// One persistent CTA per SM (CG = 1), or two that share a tile of tokens
-// (CG = 2: each converts half of the tokens, which the products of both read, and
-// its own channels). A CTA's tile is two blocks of 128 channels (kGated: gate and
-// up of the same ones, kDown: neighbours) by up to 128 tokens:
-//   warp 0       copies codes with TMA into a ring of stages (128 k)
-//   warp 1       issues the products (CG = 2: of both CTAs; the second CTA's
-//                passes on that its operands are ready)
-//   warps 4-11   convert: weights to tensor memory, tokens to shared memory, in
-//                four buffers of 64 k
-//   warps 12-19  read the accumulators (256 columns: with the operand's 256 the
-//                tensor memory is full, so there is one pair of them) into
-//                registers, hand them back, and scale and store the results
-//                beside the next tile's products
+// One persistent CTA per SM. Its tile is two blocks of 128 channels (kGated:
+// gate and up of the same ones, kDown: neighbours) by up to 192 tokens:
+//   warps 0, 3   copy codes with TMA into rings of stages (128 k), of weights and of tokens
+//   warp 1       issues the products
+//   warps 4-19   convert: weights to tensor memory, tokens to shared memory, in
+//                four steps of 32 k; eight warps take every other one, so that one step's
+//                loads, conversions and stores run beside the next one's
+//   warps 20-27  read the accumulators, hand them back, and scale and store
+//                the results, the last third beside the next tile's products
 // Channels lie along the accumulator's lanes and tokens along its columns, so
 // a warp stores 32 neighbouring channels of one token at a time, and a short
 // segment shortens everything but the weights: its tokens are copied,
-// converted, multiplied and stored 32 at a time (CG = 2: 64).
+// converted, multiplied and stored 32 at a time.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -48,49 +55,54 @@
 namespace moe {
 namespace {
 
-constexpr int kTokens = 128;           // of a tile: columns of an accumulator
 constexpr int kBlock = 128;            // channels of a block: lanes of an accumulator
 constexpr int kBoxTokens = 32;         // tokens of one copy
-constexpr int kThreads = 640;
-constexpr int kConvWarp0 = 4, kEpiWarp0 = 12, kWarps = 8;  // 8 warps each
+constexpr int kConvWarp0 = 4, kConvWarps = 16, kEpiWarp0 = 20, kEpiWarps = 8;
+constexpr int kThreads = 896;
 constexpr int kStageK = 128;           // k of a stage, 128 bytes a row
-constexpr int kStepK = 64;             // k of an fp16 buffer, 128 bytes a row
-constexpr int kSteps = 4;              // fp16 buffers
-constexpr int kWeightBytes = 2 * kBlock * kStageK;
-constexpr uint32_t kAcc = kTokens;     // tensor-memory columns of an accumulator
-constexpr uint32_t kOperand = 256;     // first column of the fp16 weights
-constexpr uint32_t kBlockColumns = kStepK / 2, kStepColumns = 2 * kBlockColumns;
+constexpr int kWBytes = 2 * kBlock * kStageK;
+constexpr int kMaxTokens = 192, kMaxStages = 4, kMaxSteps = 6;
 
-// Registers of a thread: the launch's 20 warps x 96, split between the copying
-// and issuing warps (4), the converting (8) and the epilogue's (8), which hold 128 sums:
-// 4 * 48 + 8 * 64 + 8 * 152 = 20 * 96.
-constexpr int kRegisters = 96;
-
-template <int CG>
+// TOKENS of a tile, k of a step, steps that are converted and not yet
+// multiplied, and stages of weights and of tokens.
+template <int TOKENS, int STEP_K, int STEPS, int W_STAGES, int X_STAGES>
 struct Plan {
-  static constexpr int kOwnTokens = kTokens / CG;  // tokens whose codes this CTA converts
-  static constexpr int kStageBytes = kWeightBytes + kOwnTokens * kStageK;
-  static constexpr int kStages = CG == 1 ? 3 : 4;
-  static constexpr int kStepBytes = kOwnTokens * 128;
+  static constexpr int kTokens = TOKENS, kStepK = STEP_K, kSteps = STEPS;
+  static constexpr int kWStages = W_STAGES, kXStages = X_STAGES;
+  static constexpr int kXBytes = kTokens * kStageK;
+  // fp16 of the tokens: 64 k, 128 bytes a token
+  static constexpr int kPerBuffer = 64 / kStepK, kBufferBytes = kTokens * 128;
+  static constexpr uint32_t kAcc = kTokens;       // tensor-memory columns of an accumulator
+  static constexpr uint32_t kOperand = 2 * kAcc;  // first column of the fp16 weights
+  static constexpr uint32_t kBlockColumns = kStepK / 2, kStepColumns = 2 * kBlockColumns;
+  static constexpr int kRingBytes =
+      kWStages * kWBytes + kXStages * kXBytes + kSteps / kPerBuffer * kBufferBytes;
+  static_assert(kOperand + kSteps * kStepColumns <= 512, "tensor memory");
+  static_assert(kWStages <= kMaxStages && kXStages <= kMaxStages && kSteps <= kMaxSteps, "");
+  static_assert(kSteps % kPerBuffer == 0 && kTokens <= kMaxTokens && kTokens % 64 == 0, "");
 };
-constexpr int kMaxStages = 4;
+using Many = Plan<192, 32, 4, 3, 2>;
+using Few = Plan<64, 64, 6, 4, 3>;
+
+// Registers of a thread: the launch's 28 warps x 72, split between the copying
+// and issuing warps (4), the converting (16) and the epilogue's (8), which hold
+// 64 sums at a time: 4 * 56 + 16 * 64 + 8 * 96 = 28 * 72.
+constexpr int kRegisters = 72;
 
 struct Shared {
-  uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t ready[kSteps], used[kSteps];
+  uint64_t wfull[kMaxStages], wempty[kMaxStages], xfull[kMaxStages], xempty[kMaxStages];
+  uint64_t ready[kMaxSteps], used[kMaxSteps];
   uint64_t dfull, dempty, drain;
-  float scale[kWarps][64];             // of an epilogue warp's tokens
+  float scale[kEpiWarps][kMaxTokens / 2];  // of an epilogue warp's tokens
   uint32_t tmem;
   int abort;
   int off[MOE_MAX_EXPERTS + 1];
   int pre[MOE_MAX_EXPERTS + 1];        // row tiles before expert e
 };
 
-template <int CG>
+template <class P>
 constexpr int smem_bytes() {
-  using P = Plan<CG>;
-  constexpr int bytes =
-      1024 + P::kStages * P::kStageBytes + kSteps * P::kStepBytes + (int)sizeof(Shared);
+  constexpr int bytes = 1024 + P::kRingBytes + (int)sizeof(Shared);
   static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
   // more than half of an SM's: a second CTA, and with it a second allocation
   // of the tensor memory, never shares it
@@ -99,11 +111,10 @@ constexpr int smem_bytes() {
 }
 
 // Tokens of a tile that are copied, converted and multiplied: the segment's, up
-// to a whole number of copies for each CTA.
-template <int CG>
+// to a whole number of copies.
+template <class P>
 __device__ __forceinline__ int tile_tokens(int rows) {
-  constexpr int unit = kBoxTokens * CG;
-  return (min(rows, kTokens) + unit - 1) / unit * unit;
+  return (min(rows, P::kTokens) + kBoxTokens - 1) / kBoxTokens * kBoxTokens;
 }
 
 // A place in a ring of N buffers, and the parity of its phase.
@@ -119,274 +130,309 @@ struct Ring {
   }
 };
 
-template <int OP, int CG>
+// Waits for the copies of the last `announced` stages of a ring, of as many as it has.
+template <int N>
+__device__ __forceinline__ void drain_ring(const uint64_t* full, uint32_t announced) {
+  const uint32_t left = announced < N ? announced : N;
+  for (uint32_t i = announced - left; i != announced; ++i)
+    mbar_drain(smem_u32(&full[i % N]), (i / N) & 1);
+}
+
+template <int OP, class P>
 __global__ void __launch_bounds__(kThreads, 1)
     k_expert_int8(const __grid_constant__ CUtensorMap map_x,
                   const __grid_constant__ CUtensorMap map_w, const ExpertArgs p) {
-  using P = Plan<CG>;
-  constexpr bool kPair = CG == 2;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint8_t* steps = smem + P::kStages * P::kStageBytes;
-  Shared& s = *reinterpret_cast<Shared*>(steps + kSteps * P::kStepBytes);
+  uint8_t* wring = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* xring = wring + P::kWStages * kWBytes;
+  uint8_t* buffers = xring + P::kXStages * P::kXBytes;
+  Shared& s = *reinterpret_cast<Shared*>(wring + P::kRingBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = kPair ? (int)(blockIdx.x & 1) : 0;  // clusters are pairs of neighbours
 
-  if (warp == 2) tc_alloc<CG>(smem_u32(&s.tmem), 512);
+  if (warp == 2) tc_alloc<1>(smem_u32(&s.tmem), 512);
   if (threadIdx.x == 0) {
     s.abort = 0;
-    for (int i = 0; i < P::kStages; ++i) {
-      mbar_init(smem_u32(&s.full[i]), 1);
-      mbar_init(smem_u32(&s.empty[i]), kWarps);
+    for (int i = 0; i < P::kWStages; ++i) {
+      mbar_init(smem_u32(&s.wfull[i]), 1);
+      mbar_init(smem_u32(&s.wempty[i]), kConvWarps);
     }
-    for (int i = 0; i < kSteps; ++i) {
-      // the converting warps, and in the first CTA of a pair the second one's word
-      mbar_init(smem_u32(&s.ready[i]), kWarps + (kPair && rank == 0 ? 1 : 0));
+    for (int i = 0; i < P::kXStages; ++i) {
+      mbar_init(smem_u32(&s.xfull[i]), 1);
+      mbar_init(smem_u32(&s.xempty[i]), kConvWarps);
+    }
+    for (int i = 0; i < P::kSteps; ++i) {
+      mbar_init(smem_u32(&s.ready[i]), kConvWarps / 2);
       mbar_init(smem_u32(&s.used[i]), 1);
     }
     mbar_init(smem_u32(&s.dfull), 1);
-    mbar_init(smem_u32(&s.dempty), kWarps * CG);
+    mbar_init(smem_u32(&s.dempty), kEpiWarps);
     mbar_init(smem_u32(&s.drain), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     tma_prefetch_map(&map_x);
     tma_prefetch_map(&map_w);
   }
   pdl_wait();  // the segments and the operands come from earlier kernels
-  load_segments<kTokens, kThreads>(p, s);
+  load_segments<P::kTokens, kThreads>(p, s);
   tc_fence_before();
-  if constexpr (kPair) cluster_sync();  // both CTAs' barriers exist
-  else __syncthreads();
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s.tmem;
-  const WaitCtl ctl{&s.abort, kPair ? cluster_addr(smem_u32(&s.abort), rank ^ 1) : 0u, p.wait_limit,
-                    p.status};
-  Walk<false, kTokens, Shared> walk(p, s, kStageK, 0, blockIdx.x / CG, gridDim.x / CG);
-  const int step_count = (p.K + kStepK - 1) / kStepK;  // of a tile
-  // this CTA's first channel within a tile's, and a tile's channels
-  constexpr int kOwn = OP == kGated ? kBlock : 2 * kBlock, kAll = kOwn * CG;
-  const int own = rank * kOwn;
+  const WaitCtl ctl{&s.abort, 0u, p.wait_limit, p.status};
+  Walk<false, P::kTokens, Shared> walk(p, s, kStageK, 0, blockIdx.x, gridDim.x);
+  const int step_count = (p.K + P::kStepK - 1) / P::kStepK;  // of a tile
+  constexpr int kChannels = OP == kGated ? kBlock : 2 * kBlock;  // a tile's output channels
 
   if (warp < kConvWarp0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-    if (warp == 0) {
-      Ring<P::kStages> ring;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 0) {  // weights
+      Ring<P::kWStages> ring;
       uint32_t announced = 0;
       bool ok = true;
       Tile t;
       while (ok && walk.next(t)) {
         // uniform, and known to be
         const int blocks = __shfl_sync(~0u, t.kb, 0), e = __shfl_sync(~0u, t.e, 0);
-        const int n = tile_tokens<CG>(__shfl_sync(~0u, t.rows, 0)) / CG;  // of this CTA
-        const int row0 = __shfl_sync(~0u, t.row0, 0) + rank * n;
-        const int c0 = __shfl_sync(~0u, t.n0, 0) * kAll + own;
-        const uint32_t bytes = kWeightBytes + n * kStageK;
+        const int c0 = __shfl_sync(~0u, t.n0, 0) * kChannels;
+        const int c1 = OP == kGated ? p.F + c0 : c0 + kBlock;
         for (int kb = 0; kb < blocks; ++kb) {
-          ok = __all_sync(~0u, mbar_wait<kPair>(smem_u32(&s.empty[ring.i]), ring.phase ^ 1, ctl));
+          ok = __all_sync(~0u, mbar_wait<false>(smem_u32(&s.wempty[ring.i]), ring.phase ^ 1, ctl));
           if (!ok) break;
-          const uint32_t bar = smem_u32(&s.full[ring.i]);
-          const uint32_t w = smem_u32(smem) + ring.i * P::kStageBytes, x = w + kWeightBytes;
-          mbar_expect_elected(bar, bytes);
+          const uint32_t bar = smem_u32(&s.wfull[ring.i]), w = smem_u32(wring) + ring.i * kWBytes;
+          mbar_expect_elected(bar, kWBytes);
           tma_load_3d<1>(w, &map_w, bar, kb * kStageK, c0, e);
-          tma_load_3d<1>(w + kBlock * kStageK, &map_w, bar, kb * kStageK,
-                         OP == kGated ? p.F + c0 : c0 + kBlock, e);
+          tma_load_3d<1>(w + kBlock * kStageK, &map_w, bar, kb * kStageK, c1, e);
+          ++announced;
+          ring.next();
+        }
+      }
+      // copies in flight land before the CTA ends, also when a wait gave up
+      drain_ring<P::kWStages>(s.wfull, announced);
+      __syncwarp();
+    } else if (warp == 3) {  // tokens
+      Ring<P::kXStages> ring;
+      uint32_t announced = 0;
+      bool ok = true;
+      Tile t;
+      while (ok && walk.next(t)) {
+        const int blocks = __shfl_sync(~0u, t.kb, 0), row0 = __shfl_sync(~0u, t.row0, 0);
+        const int n = tile_tokens<P>(__shfl_sync(~0u, t.rows, 0));
+        for (int kb = 0; kb < blocks; ++kb) {
+          ok = __all_sync(~0u, mbar_wait<false>(smem_u32(&s.xempty[ring.i]), ring.phase ^ 1, ctl));
+          if (!ok) break;
+          const uint32_t bar = smem_u32(&s.xfull[ring.i]), x = smem_u32(xring) + ring.i * P::kXBytes;
+          mbar_expect_elected(bar, n * kStageK);
           for (int i = 0; i < n; i += kBoxTokens)
             tma_load_2d<1>(x + i * kStageK, &map_x, bar, kb * kStageK, row0 + i);
           ++announced;
           ring.next();
         }
       }
-      // copies in flight land before the CTA ends, also when a wait gave up
-      const uint32_t left = announced < P::kStages ? announced : P::kStages;
-      for (uint32_t i = announced - left; i != announced; ++i)
-        mbar_drain(smem_u32(&s.full[i % P::kStages]), (i / P::kStages) & 1);
+      drain_ring<P::kXStages>(s.xfull, announced);
       __syncwarp();
-    } else if (warp == 1 && rank == 0) {
-      Ring<kSteps> ring;
+    } else if (warp == 1) {
+      Ring<P::kSteps> ring;
       uint32_t dphase = 1;
       bool ok = true;
       Tile t;
       while (ok && walk.next(t)) {
-        const int n = tile_tokens<CG>(__shfl_sync(~0u, t.rows, 0));
-        const uint32_t idesc = mma_desc(true, false, false, kBlock * CG, n);
-        ok = __all_sync(~0u, mbar_wait<kPair>(smem_u32(&s.dempty), dphase, ctl));
+        const uint32_t idesc =
+            mma_desc(true, false, false, kBlock, tile_tokens<P>(__shfl_sync(~0u, t.rows, 0)));
+        ok = __all_sync(~0u, mbar_wait<false>(smem_u32(&s.dempty), dphase, ctl));
         if (!ok) break;
         dphase ^= 1;
         for (int j = 0; j < step_count; ++j) {
-          ok = __all_sync(~0u, mbar_wait<kPair>(smem_u32(&s.ready[ring.i]), ring.phase, ctl));
+          ok = __all_sync(~0u, mbar_wait<false>(smem_u32(&s.ready[ring.i]), ring.phase, ctl));
           if (!ok) break;
           tc_fence_after();
-          const uint32_t a = tmem + kOperand + ring.i * kStepColumns;
-          const uint64_t b = smem_desc(smem_u32(steps) + ring.i * P::kStepBytes, 16, 1024);
+          const uint32_t a = tmem + P::kOperand + ring.i * P::kStepColumns;
+          const uint64_t b =
+              smem_desc(smem_u32(buffers) + ring.i / P::kPerBuffer * P::kBufferBytes +
+                            ring.i % P::kPerBuffer * (2 * P::kStepK),
+                        16, 1024);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {  // 16 k: 8 columns of A, 32 bytes of a row of B
-            tc_mma_ta<CG>(tmem, a + 8 * k, b + 2 * k, idesc, j > 0 || k > 0);
-            tc_mma_ta<CG>(tmem + kAcc, a + kBlockColumns + 8 * k, b + 2 * k, idesc, j > 0 || k > 0);
+          for (int k = 0; k < P::kStepK / 16; ++k) {  // 16 k: 8 columns of A, 32 bytes of a row of B
+            tc_mma_ta<1>(tmem, a + 8 * k, b + 2 * k, idesc, j > 0 || k > 0);
+            tc_mma_ta<1>(tmem + P::kAcc, a + P::kBlockColumns + 8 * k, b + 2 * k, idesc, j > 0 || k > 0);
           }
-          tc_commit<CG>(smem_u32(&s.used[ring.i]));
+          tc_commit<1>(smem_u32(&s.used[ring.i]));
           ring.next();
         }
-        if (ok) tc_commit<CG>(smem_u32(&s.dfull));
+        if (ok) tc_commit<1>(smem_u32(&s.dfull));
       }
       __syncwarp();
-      tc_commit<CG>(smem_u32(&s.drain));  // products in flight end before TMEM is freed
+      tc_commit<1>(smem_u32(&s.drain));  // products in flight end before TMEM is freed
       mbar_drain(smem_u32(&s.drain), 0);
-      __syncwarp();
-    } else if (warp == 1) {
-      // the second CTA's operands are ready: a word to the first, whose products read them
-      Ring<kSteps> ring;
-      bool ok = true;
-      Tile t;
-      while (ok && walk.next(t)) {
-        for (int j = 0; j < step_count; ++j) {
-          ok = __all_sync(~0u, mbar_wait<kPair>(smem_u32(&s.ready[ring.i]), ring.phase, ctl));
-          if (!ok) break;
-          tc_fence_after();
-          tc_fence_before();
-          if (lane == 0) mbar_arrive_release(cluster_addr(smem_u32(&s.ready[ring.i]), 0));
-          __syncwarp();
-          ring.next();
-        }
-      }
       __syncwarp();
     }
   } else if (warp < kEpiWarp0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    const int cw = warp - kConvWarp0, block = cw >> 2;
+    const int cw = warp - kConvWarp0, group = cw >> 3, block = (cw >> 2) & 1;
     const int row = (warp & 3) * 32 + lane;  // of the weight block: its lane of tensor memory
-    const uint32_t to = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kOperand + block * kBlockColumns;
-    // token and first 16-byte unit of its 64 k: CG = 1 two units a thread, else one
-    const int ct = cw * 32 + lane, token = ct % P::kOwnTokens, unit0 = ct / P::kOwnTokens * (2 / CG);
-    Ring<P::kStages> ring;
-    Ring<kSteps> step;
+    const uint32_t to =
+        tmem + ((uint32_t)((warp & 3) * 32) << 16) + P::kOperand + block * P::kBlockColumns;
+    const int ct = (cw & 7) * 32 + lane;     // thread of the group
+    // a step's 16-byte units: kWUnits of this thread's channel; of the tokens those
+    // numbered ct + 256 i, all first units before all second ones
+    constexpr int kWUnits = P::kStepK / 16, kXUnits = P::kTokens * kWUnits;
+    constexpr int kPer = (kXUnits + 255) / 256;
+    Ring<P::kWStages> wr;
+    Ring<P::kXStages> xr;
+    uint32_t base = 0;     // steps of the tiles before this one
+    int pending = -1;      // the step whose stores are under way
+    // its stores are done and the products may read them
+    const auto finish = [&] {
+      if (pending < 0) return;
+      fence_async_smem();
+      tc_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&s.ready[pending]));
+      pending = -1;
+    };
     bool ok = true;
     Tile t;
-    while (ok && walk.next(t)) {
-      const bool mine = token < tile_tokens<CG>(t.rows) / CG;
-      for (int j = 0; j < step_count; ++j) {
-        const int half = j & 1;  // of the stage
-        if (half == 0)
-          ok = mbar_wait<kPair>(smem_u32(&s.full[ring.i]), ring.phase, ctl);
-        ok = ok && mbar_wait<kPair>(smem_u32(&s.used[step.i]), step.phase ^ 1, ctl);
-        ok = __all_sync(~0u, ok);
-        if (!ok) break;
-        tc_fence_after();
-        const uint8_t* stage = smem + ring.i * P::kStageBytes;
-        const uint4* w = reinterpret_cast<const uint4*>(stage + (block * kBlock + row) * kStageK);
-        const uint4* x = reinterpret_cast<const uint4*>(stage + kWeightBytes + token * kStageK);
-        uint4* out = reinterpret_cast<uint4*>(steps + step.i * P::kStepBytes + token * 128);
+    for (; ok && walk.next(t); base += step_count) {
+      const int n = tile_tokens<P>(t.rows);
+      for (int j0 = 0; j0 < step_count; j0 += kStageK / P::kStepK) {
+        const uint32_t wbar = smem_u32(&s.wfull[wr.i]), xbar = smem_u32(&s.xfull[xr.i]);
+        if (!__all_sync(~0u, mbar_test(wbar, wr.phase) && mbar_test(xbar, xr.phase))) {
+          finish();
+          ok = mbar_wait<false>(wbar, wr.phase, ctl) && mbar_wait<false>(xbar, xr.phase, ctl);
+          ok = __all_sync(~0u, ok);
+          if (!ok) break;
+        }
+        const uint4* w = reinterpret_cast<const uint4*>(wring + wr.i * kWBytes +
+                                                        (block * kBlock + row) * kStageK);
+        const uint4* x = reinterpret_cast<const uint4*>(xring + xr.i * P::kXBytes);
+#pragma unroll 1
+        for (int h = group; h < kStageK / P::kStepK; h += 2) {
+          if (j0 + h >= step_count) break;
+          const uint32_t number = base + j0 + h, at = number % P::kSteps;
+          uint4 c[kPer];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {  // 32 k of the weights
-          uint32_t v[16];
+          for (int i = 0; i < kPer; ++i) {
+            const int unit = (ct + 256 * i) / P::kTokens, token = (ct + 256 * i) % P::kTokens;
+            if (ct + 256 * i < kXUnits && token < n)
+              c[i] = x[token * 8 + ((kWUnits * h + unit) ^ (token & 7))];
+          }
+          uint32_t v[kWUnits / 2][16];  // 32 k of a channel each
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const uint4 c = w[(half * 4 + 2 * i + u) ^ (row & 7)];
-            const uint32_t cc[4] = {c.x, c.y, c.z, c.w};
+          for (int u = 0; u < kWUnits; ++u) {
+            const uint4 q = w[(kWUnits * h + u) ^ (row & 7)];
+            const uint32_t cc[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint2 f = int8_to_f16(cc[q]);
-              v[8 * u + 2 * q] = f.x;
-              v[8 * u + 2 * q + 1] = f.y;
+            for (int b = 0; b < 4; ++b) {
+              const uint2 f = int8_to_f16(cc[b]);
+              v[u / 2][u % 2 * 8 + 2 * b] = f.x;
+              v[u / 2][u % 2 * 8 + 2 * b + 1] = f.y;
             }
           }
-          tc_st16(to + step.i * kStepColumns + 16 * i, v);
-        }
-        if (mine) {
+          finish();  // the step before, beside whose stores this one's codes were converted
+          ok = __all_sync(~0u, mbar_wait<false>(smem_u32(&s.used[at]),
+                                                (number / P::kSteps & 1) ^ 1, ctl));
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
-          for (int i = 0; i < 2 / CG; ++i) {  // 16 k of a token: 32 bytes of fp16
-            const int u = unit0 + i;
-            const uint4 c = x[(half * 4 + u) ^ (token & 7)];
-            const uint2 f0 = int8_to_f16(c.x), f1 = int8_to_f16(c.y), f2 = int8_to_f16(c.z),
-                        f3 = int8_to_f16(c.w);
-            out[(2 * u) ^ (token & 7)] = make_uint4(f0.x, f0.y, f1.x, f1.y);
-            out[(2 * u + 1) ^ (token & 7)] = make_uint4(f2.x, f2.y, f3.x, f3.y);
+          for (int i = 0; i < kWUnits / 2; ++i) tc_st16(to + at * P::kStepColumns + 16 * i, v[i]);
+          uint4* out = reinterpret_cast<uint4*>(buffers + at / P::kPerBuffer * P::kBufferBytes);
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {  // 16 k of a token: 32 bytes of fp16
+            const int unit = (ct + 256 * i) / P::kTokens, token = (ct + 256 * i) % P::kTokens;
+            if (ct + 256 * i < kXUnits && token < n) {
+              const int u = 2 * (at % P::kPerBuffer * kWUnits + unit);
+              const uint2 f0 = int8_to_f16(c[i].x), f1 = int8_to_f16(c[i].y),
+                          f2 = int8_to_f16(c[i].z), f3 = int8_to_f16(c[i].w);
+              out[token * 8 + (u ^ (token & 7))] = make_uint4(f0.x, f0.y, f1.x, f1.y);
+              out[token * 8 + ((u + 1) ^ (token & 7))] = make_uint4(f2.x, f2.y, f3.x, f3.y);
+            }
           }
+          pending = (int)at;
         }
-        tc_wait_st();
-        fence_async_smem();
-        tc_fence_before();
+        if (!ok) break;
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(smem_u32(&s.ready[step.i]));
-          if (half == 1 || j == step_count - 1) mbar_arrive(smem_u32(&s.empty[ring.i]));
+          mbar_arrive(smem_u32(&s.wempty[wr.i]));
+          mbar_arrive(smem_u32(&s.xempty[xr.i]));
         }
-        if (half == 1 || j == step_count - 1) ring.next();
-        step.next();
+        wr.next();
+        xr.next();
       }
+      finish();
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+    constexpr int kHalf = P::kTokens / 2;  // tokens of a warp
     const int quarter = warp & 3, half = (warp - kEpiWarp0) >> 2;
-    const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16) + half * 64;
+    const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16) + half * kHalf;
+    float* scale = s.scale[warp - kEpiWarp0];
     uint32_t dphase = 0;
     bool ok = true;
     Tile t;
     while (ok && walk.next(t)) {
-      const int left = t.rows - half * 64;  // tokens of this warp: columns half * 64 on
-      const int c = t.n0 * kAll + own + quarter * 32 + lane;  // channel, of the first block
+      const int left = t.rows - half * kHalf;  // tokens of this warp: columns half * kHalf on
+      const int c = t.n0 * kChannels + quarter * 32 + lane;  // channel, of the first block
       const int c1 = OP == kGated ? c + p.F : c + kBlock;
       const int channels = OP == kGated ? 2 * p.F : p.N;
       const bool in0 = c < p.N, in1 = OP == kGated ? in0 : c1 < p.N;
       const float* sw = p.sb + (long long)t.e * channels;
       const float w0 = in0 ? __ldg(sw + c) : 0.0f, w1 = in1 ? __ldg(sw + c1) : 0.0f;
-      const float* sx = p.sa + t.row0 + half * 64;
-      float* scale = s.scale[warp - kEpiWarp0];
+      const float* sx = p.sa + t.row0 + half * kHalf;
 #pragma unroll
-      for (int i = 0; i < 64; i += 32) scale[lane + i] = lane + i < left ? __ldg(sx + lane + i) : 0.0f;
-      ok = __all_sync(~0u, mbar_wait<kPair>(smem_u32(&s.dfull), dphase, ctl));
+      for (int i = 0; i < kHalf; i += 32) scale[lane + i] = lane + i < left ? __ldg(sx + lane + i) : 0.0f;
+      ok = __all_sync(~0u, mbar_wait<false>(smem_u32(&s.dfull), dphase, ctl));
       if (!ok) break;
       dphase ^= 1;
       tc_fence_after();
-      uint32_t v[4][32];  // first block's 64 columns, then the second's
-#pragma unroll
-      for (int q = 0; q < 4; ++q) tc_ld32(v[q], from + (q & 1) * 32 + (q >> 1) * kAcc);
-      tc_wait_ld();
-#pragma unroll
-      for (int q = 0; q < 4; ++q) tc_loaded(v[q]);
-      tc_fence_before();
-      __syncwarp();  // the scales are written, too
-      if (lane == 0) {
-        if constexpr (kPair) mbar_arrive_relaxed(cluster_addr(smem_u32(&s.dempty), 0));
-        else mbar_arrive(smem_u32(&s.dempty));
-      }
       // one token after the other: of 32 neighbouring channels a warp writes 128 bytes of h, or 64
       // of y in each block
       using Out = std::conditional_t<OP == kGated, float, __nv_bfloat16>;
-      Out* out = static_cast<Out*>(p.out) + ((long long)t.row0 + half * 64) * p.N + c;
+      Out* out = static_cast<Out*>(p.out) + ((long long)t.row0 + half * kHalf) * p.N + c;
+      const int rounds = left <= 0 ? 0 : min((left + 31) / 32, kHalf / 32);
+      __syncwarp();  // the scales are written
+#pragma unroll 1
+      for (int q = 0; q < rounds; ++q) {
+        uint32_t v0[32], v1[32];  // 32 tokens of the first block, and of the second
+        tc_ld32(v0, from + q * 32);
+        tc_ld32(v1, from + P::kAcc + q * 32);
+        tc_wait_ld();
+        tc_loaded(v0);
+        tc_loaded(v1);
+        if (q == rounds - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&s.dempty));
+        }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (left > q * 16) {
-#pragma unroll
-          for (int i = q * 16; i < q * 16 + 16; ++i) {
-            const float sr = scale[i];
-            const float a = __uint_as_float(v[i >> 5][i & 31]) * sr * w0;
-            const float b = __uint_as_float(v[2 + (i >> 5)][i & 31]) * sr * w1;
-            if constexpr (OP == kGated) {
-              if (in0 && i < left) *out = silu(a) * b;
-            } else {
-              if (in0 && i < left) *out = __float2bfloat16_rn(a);
-              if (in1 && i < left) out[kBlock] = __float2bfloat16_rn(b);
-            }
-            out += p.N;
+        for (int i = 0; i < 32; ++i) {
+          const float sr = scale[q * 32 + i];
+          const float a = __uint_as_float(v0[i]) * sr * w0;
+          const float b = __uint_as_float(v1[i]) * sr * w1;
+          if constexpr (OP == kGated) {
+            if (in0 && q * 32 + i < left) *out = silu(a) * b;
+          } else {
+            if (in0 && q * 32 + i < left) *out = __float2bfloat16_rn(a);
+            if (in1 && q * 32 + i < left) out[kBlock] = __float2bfloat16_rn(b);
           }
+          out += p.N;
         }
       }
+      if (rounds == 0 && lane == 0) mbar_arrive(smem_u32(&s.dempty));
       __syncwarp();  // read, before the next tile's are written
     }
   }
   __syncwarp();
   tc_fence_before();
-  if constexpr (kPair) cluster_sync();  // neither CTA's memory is used any more
-  else __syncthreads();
+  __syncthreads();
   tc_fence_after();
-  if (warp == 2) tc_dealloc<CG>(tmem, 512);
+  if (warp == 2) tc_dealloc<1>(tmem, 512);
 }
 
 // ---- host side -------------------------------------------------------------
-template <int OP, int CG>
+template <int OP, class P>
 cudaError_t launch(const ExpertArgs& args, const void* a, const void* b, int num_sms,
                    cudaStream_t st) {
   ExpertArgs p = args;
-  constexpr int channels = (OP == kGated ? kBlock : 2 * kBlock) * CG;
+  constexpr int channels = OP == kGated ? kBlock : 2 * kBlock;
   p.nt = (p.N + channels - 1) / channels;
   CUtensorMap mx, mw;
   cudaError_t e = make_map(&mx, a, true, p.K, p.rows_max, 0, kBoxTokens);
@@ -394,29 +440,21 @@ cudaError_t launch(const ExpertArgs& args, const void* a, const void* b, int num
     e = make_map(&mw, b, true, p.K, OP == kGated ? 2ll * p.F : p.N, p.E, kBlock);
   if (e != cudaSuccess) return e;
   const long long segments = p.E < p.rows_max ? p.E : p.rows_max;
-  const long long tiles = (p.rows_max / kTokens + segments) * p.nt, most = num_sms / CG;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((tiles < most ? tiles : most) * CG));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem_bytes<CG>();
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = CG;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = CG == 2 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k_expert_int8<OP, CG>, mx, mw, p);
+  const long long tiles = (p.rows_max / P::kTokens + segments) * p.nt;
+  return launch_pdl(k_expert_int8<OP, P>, dim3((unsigned)(tiles < num_sms ? tiles : num_sms)),
+                    dim3(kThreads), smem_bytes<P>(), st, mx, mw, p);
 }
 
-template <int OP, int CG>
+#ifndef FEWROWS
+#define FEWROWS 64
+#endif
+bool use_few(const ExpertArgs& p) { return p.rows_max <= (long long)FEWROWS * p.E; }
+
+template <int OP, class P>
 cudaError_t prepare() {
-  const auto kernel = k_expert_int8<OP, CG>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       smem_bytes<CG>());
+  const auto kernel = k_expert_int8<OP, P>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<P>());
   if (e != cudaSuccess) return e;
   cudaFuncAttributes attr;
   e = cudaFuncGetAttributes(&attr, kernel);
@@ -427,15 +465,20 @@ cudaError_t prepare() {
 }  // namespace
 
 cudaError_t expert_int8_prepare() {
-  cudaError_t e = prepare<kGated, 1>();
-  if (e == cudaSuccess) e = prepare<kDown, 1>();
+  cudaError_t e = prepare<kGated, Many>();
+  if (e == cudaSuccess) e = prepare<kDown, Many>();
+  if (e == cudaSuccess) e = prepare<kGated, Few>();
+  if (e == cudaSuccess) e = prepare<kDown, Few>();
   return e;
 }
 
 cudaError_t launch_expert_int8(ExpertOp op, const ExpertArgs& p, const void* a, const void* b,
                                int num_sms, cudaStream_t st) {
-  return op == kGated ? launch<kGated, 1>(p, a, b, num_sms, st)
-                      : launch<kDown, 1>(p, a, b, num_sms, st);
+  if (use_few(p))
+    return op == kGated ? launch<kGated, Few>(p, a, b, num_sms, st)
+                        : launch<kDown, Few>(p, a, b, num_sms, st);
+  return op == kGated ? launch<kGated, Many>(p, a, b, num_sms, st)
+                      : launch<kDown, Many>(p, a, b, num_sms, st);
 }
 
 }  // namespace moe

@@ -128,6 +128,7 @@ CASES = {
     "few_rows_one_expert": ([7, 0], 272, 80),
     "ragged": ([130, 1, 0, 257, 64], 208, 336),
     "tile_edges": ([128, 127, 129, 0, 256, 255], 192, 256),
+    "wide_tile_edges": ([192, 191, 193, 0, 384, 33, 32, 1, 97], 224, 400),
     "long": ([1500, 3], 320, 144),
     "many_experts": ([(7 * e) % 23 for e in range(200)], 128, 96),
     "wide": ([33, 65], 2064, 1040),
