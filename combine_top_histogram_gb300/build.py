@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(BUILD_DIR, "libmoe_ep.so")
 DEBUG_LIB_PATH = os.path.join(BUILD_DIR, "libmoe_ep_debug.so")
 SOURCES = ["api.cu", "layout.cu", "dispatch.cu", "combine.cu", "layout_noalloc.cu", "two_stage.cu",
            "fused.cu", "combine_backward.cu", "expert_api.cu", "expert_gemm.cu",
-           "expert_rows.cu", "expert_quantise.cu", "expert_int8.cu"]
+           "expert_rows.cu", "expert_codes.cu", "expert_int8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 VARIANTS = {"release": ([], BUILD_DIR, LIB_PATH),
             "debug": (["-DMOE_DEBUG_BOUNDS"], os.path.join(BUILD_DIR, "debug"), DEBUG_LIB_PATH)}

@@ -1,16 +1,22 @@
-// expert_quantise.cu -- int8 codes and scales of h, the gated experts' result:
-// for each row of the segments s = amax/127 over its F values and
-// codes = RNE(h / s).
+// expert_codes.cu -- what the int8 experts do in memory beside their products.
 //
-// The scale needs the whole row, whose columns many CTAs computed, so h comes
+// k_expert_quantise: codes and scales of h, the gated experts' result: for each
+// row of the segments s = amax/127 over its F values and codes = RNE(h / s). The
+// scale needs the whole row, whose columns many CTAs computed, so h comes
 // through memory in fp32 (a rounded h would move codes that lie near a tie). One
 // CTA takes a row at a time, holds it in registers (up to 16 values a thread)
 // while its largest magnitude is found, and writes the codes: every value is
 // read once.
+//
+// k_widen: codes as fp16, for the products of many rows an expert. It moves three
+// bytes a code at HBM's rate; the products that read them then run at the fp16
+// rate, while the kernel that converts on its way is bound by its SM's shared
+// memory at 0.6 of it (expert_int8.cu).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include "expert_internal.cuh"
+#include "expert_math.cuh"
 #include "internal.cuh"
 
 namespace moe {
@@ -47,20 +53,64 @@ __device__ __forceinline__ uint32_t cta_max(uint32_t m, uint32_t* buf) {
   return m;
 }
 
+// The segments' rows: from the first offset to the largest, held to
+// [0, rows_max], as the products hold them.
+__device__ __forceinline__ void segment_rows(const ExpertArgs& p, uint32_t* buf, int& first,
+                                             int& end) {
+  const int most = (int)p.rows_max;
+  first = min(max(__ldg(p.offset), 0), most);
+  end = 0;
+  for (int e = threadIdx.x; e <= p.E; e += kThreads) end = max(end, min(__ldg(p.offset + e), most));
+  end = (int)cta_max((uint32_t)end, buf);
+}
+
+// 16 codes to 32 bytes of fp16. The rows of all segments (per: units of a row),
+// or with WEIGHTS the matrix of expert blockIdx.y (per: its units), unless it
+// has no rows: where the offset after it is not above its own, none can be in range.
+template <bool WEIGHTS>
+__global__ void __launch_bounds__(kThreads)
+    k_widen(const ExpertArgs p, const uint4* __restrict__ in, uint4* __restrict__ out,
+            long long per) {
+  __shared__ uint32_t buf[kWarps];
+  pdl_wait();
+  long long at, end;
+  if (WEIGHTS) {
+    if (__ldg(p.offset + blockIdx.y + 1) <= __ldg(p.offset + blockIdx.y)) return;
+    at = per * blockIdx.y;
+    end = at + per;
+  } else {
+    int first, last;
+    segment_rows(p, buf, first, last);
+    at = per * first;
+    end = per * last;
+  }
+  constexpr int kAhead = 4;
+  for (at += (long long)blockIdx.x * kAhead * kThreads + threadIdx.x; at < end;
+       at += (long long)gridDim.x * kAhead * kThreads) {
+    uint4 c[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      c[i] = at + i * kThreads < end ? __ldcs(in + at + i * kThreads) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (at + i * kThreads >= end) break;
+      const uint2 a = int8_to_f16(c[i].x), b = int8_to_f16(c[i].y), d = int8_to_f16(c[i].z),
+                  e = int8_to_f16(c[i].w);
+      uint4* o = out + 2 * (at + i * kThreads);
+      o[0] = make_uint4(a.x, a.y, b.x, b.y);
+      o[1] = make_uint4(d.x, d.y, e.x, e.y);
+    }
+  }
+}
+
 __global__ void __launch_bounds__(kThreads)
     k_expert_quantise(const ExpertArgs p, const float* __restrict__ h, int8_t* __restrict__ codes,
                       float* __restrict__ scale) {
   __shared__ uint32_t buf[3][kWarps];
   const int tid = threadIdx.x, n = p.F >> 2;
   pdl_wait();
-  // the segments' rows are those from the first offset to the largest, held to
-  // [0, rows_max], as the products hold them
-  const int most = (int)p.rows_max;
-  const int first = min(max(__ldg(p.offset), 0), most);
-  int end = 0;
-  for (int e = tid; e <= p.E; e += kThreads) end = max(end, min(__ldg(p.offset + e), most));
-  end = (int)cta_max((uint32_t)end, buf[2]);
-  int par = 0;
+  int first, end, par = 0;
+  segment_rows(p, buf[2], first, end);
   for (long long r = (long long)first + blockIdx.x; r < end; r += gridDim.x, par ^= 1) {
     const float4* row = reinterpret_cast<const float4*>(h + r * p.F);
     float4 v[kHeld];
@@ -90,6 +140,19 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 }  // namespace
+
+cudaError_t launch_expert_widen(const ExpertArgs& p, long long weight_rows, const void* a,
+                                const void* b, uint16_t* x16, uint16_t* w16, int num_sms,
+                                cudaStream_t st) {
+  const unsigned wide = 16u * num_sms, each = (wide + p.E - 1) / p.E;
+  const long long row = p.K / 16;
+  const cudaError_t e =
+      launch_pdl(k_widen<false>, dim3(wide), dim3(kThreads), 0, st, p,
+                 static_cast<const uint4*>(a), reinterpret_cast<uint4*>(x16), row);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_widen<true>, dim3(each, p.E), dim3(kThreads), 0, st, p,
+                    static_cast<const uint4*>(b), reinterpret_cast<uint4*>(w16), weight_rows * row);
+}
 
 cudaError_t launch_expert_quantise(const ExpertArgs& p, const float* h, int8_t* codes,
                                    float* scale, int num_sms, cudaStream_t st) {

@@ -2,7 +2,7 @@
 // the 5th-generation tensor cores.
 //
 // Rows of expert e are the segment [offset[e], offset[e+1]) of a row buffer.
-// Five products share one kernel skeleton:
+// These products share one kernel skeleton:
 //   kGated  h  = silu(x Wg^T) * (x Wu^T)            A = x,   B = w13 (K-major)
 //   kDown   y  = h W2^T                             A = h,   B = w2  (K-major)
 //   kDgate  dh = dy W2, then dg = dh u s (1 + g (1 - s)), du = dh g s with
@@ -13,6 +13,8 @@
 //           they would double those products)
 //   kDx     dx = [dg du] W13                        A = dgu, B = w13 (N-major)
 //   kDw     dW = a^T b over the segment's rows      A = a (M-major), B = b (N-major)
+//   kGatedCodes, kDownCodes  as the first two, of int8 codes that were widened to
+//           fp16 (which holds them exactly), with their scales in the epilogue
 //
 // One persistent CTA per SM. A CTA computes 128 x 256 tiles, or the two CTAs
 // of a cluster compute 256 x 256 tiles together (CG = 2): each holds its 128
@@ -109,6 +111,9 @@ constexpr int smem_bytes() {
   static_assert(bytes > 114 * 1024, "one CTA per SM");
   return bytes;
 }
+
+__host__ __device__ constexpr bool gated(int op) { return op == kGated || op == kGatedCodes; }
+__host__ __device__ constexpr bool of_codes(int op) { return op == kGatedCodes || op == kDownCodes; }
 
 template <int OP, int CG>
 using Tiles = Walk<OP == kDw, kTileM * CG, Shared>;
@@ -268,7 +273,52 @@ __device__ __forceinline__ void epilogue_bf16(const ExpertArgs& p, const Tile& t
                                               int half, int quarter, int lane, uint4* buf,
                                               bool zero, GateUp& pre, const CUtensorMap& map_c) {
   const int wrow = quarter * 32;
-  if constexpr (OP == kGated) {
+  if constexpr (of_codes(OP)) {
+    // whole sums of codes, then the row's scale (of this lane) and the channel's (of lane i for
+    // column i)
+    const int rows = t.rows - wrow;
+    const long long row = (long long)t.row0 + wrow;
+    const float sr = lane < rows ? __ldg(p.sa + row + lane) : 0.0f;
+    const float* sw = p.sb + (long long)t.e * (gated(OP) ? 2 * p.F : p.N);
+#pragma unroll 1
+    for (int j = 0; j < TN / (gated(OP) ? 128 : 64); ++j) {
+      if constexpr (gated(OP)) {
+        const int at = half * (TN / 4) + j * 32, c = t.n0 * (TN / 2) + at;
+        const bool in = c + lane < p.F;
+        const float wg = in ? __ldg(sw + c + lane) : 0.0f, wu = in ? __ldg(sw + p.F + c + lane) : 0.0f;
+        uint32_t g[32], u[32], h[16];
+        tc_ld32(g, taddr + at);
+        tc_ld32(u, taddr + TN / 2 + at);
+        tc_wait_ld();
+        tc_loaded(g);
+        tc_loaded(u);
+        float* out = static_cast<float*>(p.out) + row * p.F + c;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {  // 16 columns, 64 bytes of a row
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float a = __uint_as_float(g[16 * q + i]) * sr * __shfl_sync(~0u, wg, 16 * q + i);
+            const float b = __uint_as_float(u[16 * q + i]) * sr * __shfl_sync(~0u, wu, 16 * q + i);
+            h[i] = __float_as_uint(silu(a) * b);
+          }
+          put_store(buf, lane, h, reinterpret_cast<uint16_t*>(out + 16 * q), 2ll * p.F, rows,
+                    2 * (p.F - c - 16 * q));
+        }
+      } else {
+        const int at = half * (TN / 2) + j * 32, c = t.n0 * TN + at;
+        const float wc = c + lane < p.N ? __ldg(sw + c + lane) : 0.0f;
+        uint32_t d[32], o[16];
+        tc_ld32(d, taddr + at);
+        tc_wait_ld();
+        tc_loaded(d);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          o[i] = bf16x2(__uint_as_float(d[2 * i]) * sr * __shfl_sync(~0u, wc, 2 * i),
+                        __uint_as_float(d[2 * i + 1]) * sr * __shfl_sync(~0u, wc, 2 * i + 1));
+        put_store(buf, lane, o, static_cast<uint16_t*>(p.out) + row * p.N + c, p.N, rows, p.N - c);
+      }
+    }
+  } else if constexpr (OP == kGated) {
     const int rows = t.rows - wrow;
     const long long row = (long long)t.row0 + wrow;
 #pragma unroll 1
@@ -422,10 +472,10 @@ __device__ __forceinline__ void take_registers() {
 
 // The warp that issues the products: its place in the ring of stages and in
 // the two accumulators.
-template <class PLAN, int CG, int TN, bool FP8, bool AMN, bool BMN>
+template <class PLAN, int CG, int TN, bool FP8, bool CODES, bool AMN, bool BMN>
 struct Issuer {
   static constexpr int kStages = PLAN::kStages, kStageBytes = PLAN::kStageBytes;
-  static constexpr uint32_t kIdesc = mma_desc(FP8, AMN, BMN, kTileM * CG, TN);
+  static constexpr uint32_t kIdesc = mma_desc(FP8 || CODES, AMN, BMN, kTileM * CG, TN);
   // 16 k of bf16 (32 of e4m3): 32 bytes along K, or 16 lines of 128 bytes
   static constexpr uint64_t kA = (AMN ? 2048 : 32) >> 4, kB = (BMN ? 2048 : 32) >> 4;
   const uint32_t full0, empty0, tfull0, tempty0, tmem;
@@ -713,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 2 / CG; ++i) {
               const int half = i + rank;  // kGated: gate columns, then up columns
-              const int n = OP == kGated ? half * p.F + n0 * (TN / 2) : n0 * TN + half * (TN / 2);
+              const int n = gated(OP) ? half * p.F + n0 * (TN / 2) : n0 * TN + half * (TN / 2);
               tma_load_3d<CG>(b + i * (TN / 2 * 128), &map_b, bar, kb * kElems, n, e);
             }
           }
@@ -761,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     } else if (warp == 1) {
-      Issuer<P, CG, TN, FP8, kAmn, kBmn> io(s, smem, tmem, ctl);
+      Issuer<P, CG, TN, FP8, of_codes(OP), kAmn, kBmn> io(s, smem, tmem, ctl);
       bool ok = true;
       Tile t;
       while (ok && walk.next(t)) {
@@ -1002,7 +1052,7 @@ long long most_tiles(const ExpertArgs& p, int rows, int nt) {
 
 template <int OP>
 int column_tiles(const ExpertArgs& p, int tn) {
-  const int n = OP == kGated ? p.F : p.N, w = OP == kGated ? tn / 2 : tn;
+  const int n = gated(OP) ? p.F : p.N, w = gated(OP) ? tn / 2 : tn;
   return (n + w - 1) / w;
 }
 
@@ -1022,8 +1072,8 @@ cudaError_t launch(const ExpertArgs& args, const void* a, const void* b, int num
   } else {
     e = make_map(&ma, a, FP8, p.K, p.rows_max, 0, p.a_box);
     if (e == cudaSuccess) {
-      if (OP == kGated) e = make_map(&mb, b, FP8, p.K, 2ll * p.F, p.E, TN / 2);
-      else if (OP == kDown) e = make_map(&mb, b, FP8, p.K, p.N, p.E, TN / 2);
+      if (gated(OP)) e = make_map(&mb, b, FP8, p.K, 2ll * p.F, p.E, TN / 2);
+      else if (OP == kDown || OP == kDownCodes) e = make_map(&mb, b, FP8, p.K, p.N, p.E, TN / 2);
       else e = make_map(&mb, b, false, p.N, p.K, p.E, 64);
     }
   }
@@ -1129,6 +1179,9 @@ cudaError_t expert_gemm_prepare() {
   if (e == cudaSuccess) e = prepare<kDgate, false>();
   if (e == cudaSuccess) e = prepare<kDx, false>();
   if (e == cudaSuccess) e = prepare<kDw, false>();
+  // only of many rows an expert
+  if (e == cudaSuccess) e = prepare<kGatedCodes, false, 2, 256>();
+  if (e == cudaSuccess) e = prepare<kDownCodes, false, 2, 256>();
   return e;
 }
 
@@ -1143,6 +1196,8 @@ cudaError_t launch_expert_gemm(ExpertOp op, bool fp8, const ExpertArgs& args, co
     case kDown:
       return fp8 ? launch<kDown, true>(pair, p, a, b, num_sms, st)
                  : launch<kDown, false>(pair, p, a, b, num_sms, st);
+    case kGatedCodes: return launch<kGatedCodes, false, 2, 256>(p, a, b, num_sms, st);
+    case kDownCodes: return launch<kDownCodes, false, 2, 256>(p, a, b, num_sms, st);
     case kDgate: return launch<kDgate, false>(pair, p, a, b, num_sms, st);
     case kDx: return launch<kDx, false>(pair, p, a, b, num_sms, st);
     default: return launch<kDw, false>(pair, p, a, b, num_sms, st);

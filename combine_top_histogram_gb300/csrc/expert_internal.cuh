@@ -18,6 +18,8 @@ enum ExpertOp : int {
   kDgate = 2,  // dh = dy W2, then d(gate), d(up) from dh and the kept pre-activations
   kDx = 3,     // dx = [d(gate), d(up)] W13
   kDw = 4,     // W gradient: a^T b over the rows of a segment
+  kGatedCodes = 5,  // kGated and kDown of int8 codes widened to fp16, with their scales in the
+  kDownCodes = 6,   // epilogue; h is fp32
 };
 
 // Types of the operands, by the C ABI's numbers.
@@ -35,7 +37,7 @@ struct ExpertArgs {
   int a_box;               // rows of one row-operand copy
   const float* sa;         // scales of the row operand: FP8 [rows, K/128], INT8 [rows]
   const float* sb;         // scales of the weights: FP8 per 128 x 128, INT8 per channel
-  void* out;               // kGated, INT8: h in fp32 [rows, F]
+  void* out;               // INT8: h in fp32 [rows, F]
   float* out_scale;        // kGated, FP8: scales of h [rows, F/128]
   uint16_t* gu_out;        // kGated, bf16: kept pre-activations [rows, 2F], or null
   const uint16_t* gu;      // kDgate: kept pre-activations
@@ -50,7 +52,12 @@ cudaError_t launch_expert_gemm(ExpertOp op, bool fp8, const ExpertArgs& args, co
 // kGated or kDown for a few rows (expert_rows.cu).
 cudaError_t launch_expert_rows(ExpertOp op, ExpertType type, const ExpertArgs& args, const void* a,
                                const void* b, int num_sms, cudaStream_t st);
-// INT8: codes [rows, F] and scales [rows] of the segments' rows of h (expert_quantise.cu).
+// INT8: kGated or kDown in two steps, codes widened to fp16 in memory (x16 [rows, K], w16: all
+// weights) and then a product of fp16 (expert_codes.cu, expert_gemm.cu).
+cudaError_t launch_expert_widen(const ExpertArgs& args, long long weight_rows, const void* a,
+                                const void* b, uint16_t* x16, uint16_t* w16, int num_sms,
+                                cudaStream_t st);
+// INT8: codes [rows, F] and scales [rows] of the segments' rows of h (expert_codes.cu).
 cudaError_t launch_expert_quantise(const ExpertArgs& args, const float* h, int8_t* codes,
                                    float* scale, int num_sms, cudaStream_t st);
 // INT8: kGated (to fp32 h) or kDown on the tensor cores (expert_int8.cu).
@@ -76,5 +83,6 @@ struct moe_expert {
   uint32_t* status;
   uint16_t* dgu;           // [rows_max, 2F] (training only)
   float* h32;              // [rows_max, F] (INT8 only)
+  uint16_t *x16, *w16;     // fp16 codes of rows and weights (INT8 with many rows only)
   long long wait_limit;
 };

@@ -22,7 +22,7 @@
 // exchange their rows' largest magnitudes through distributed shared memory.
 // int8: codes become fp16 in registers (exact, and so are their products), 5
 // instructions for four; whole sums, then the row's and the channel's scale. h
-// leaves in fp32, for its scale is the whole row's (expert_quantise.cu).
+// leaves in fp32, for its scale is the whole row's (expert_codes.cu).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
