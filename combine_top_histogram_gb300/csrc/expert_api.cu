@@ -11,9 +11,6 @@
 namespace {
 
 constexpr size_t kAlign = 256;
-#ifndef WIDEROWS
-#define WIDEROWS 1024ll
-#endif
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -46,9 +43,12 @@ int validate(const moe_expert_config_t* c) {
 
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
-// INT8 with many rows an expert: codes are widened to fp16 in memory.
-bool wide(const moe_expert_config_t* c) {
-  return c->dtype == MOE_INT8 && c->rows_max >= WIDEROWS * c->num_experts;
+// INT8 with many rows an expert: the codes of rows and weights are widened to
+// fp16 in memory for the products (see forward()). By the rows a configuration
+// can have: a call of fewer takes the same way.
+bool widens(const moe_expert_config_t* c) {
+  return c->dtype == MOE_INT8 && c->rows_max >= 1024ll * c->num_experts &&
+         (double)c->rows_max * c->hidden * c->inter >= 0x1p34;
 }
 size_t x16_bytes(const moe_expert_config_t* c) {
   return align_up((size_t)c->rows_max * (c->hidden > c->inter ? c->hidden : c->inter) * 2);
@@ -59,7 +59,7 @@ size_t w16_bytes(const moe_expert_config_t* c) {
 
 size_t workspace_bytes(const moe_expert_config_t* c) {
   size_t n = kAlign + (c->train || c->dtype == MOE_INT8 ? (size_t)c->rows_max * c->inter * 4 : 0);
-  if (wide(c)) n = align_up(n) + x16_bytes(c) + w16_bytes(c);
+  if (widens(c)) n = align_up(n) + x16_bytes(c) + w16_bytes(c);
   return n;
 }
 
@@ -94,15 +94,16 @@ cudaError_t forward(moe_expert_t x, moe::ExpertOp op, const moe::ExpertArgs& a, 
   const moe::ExpertType type = static_cast<moe::ExpertType>(x->cfg.dtype);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (use_rows(x, op)) return moe::launch_expert_rows(op, type, a, in, w, x->num_sms, st);
-  if (x->x16) {
+  if (type == moe::kInt8 && !x->x16) return moe::launch_expert_int8(op, a, in, w, x->num_sms, st);
+  if (type == moe::kInt8) {
     const bool gated = op == moe::kGated;
-    const cudaError_t e = moe::launch_expert_widen(a, gated ? 2ll * a.F : a.N, in, w, x->x16,
-                                                   x->w16, x->num_sms, st);
-    if (e != cudaSuccess) return e;
-    return moe::launch_expert_gemm(gated ? moe::kGatedCodes : moe::kDownCodes, false, a, x->x16,
-                                   x->w16, x->num_sms, st);
+    cudaError_t e = moe::launch_widen_rows(a, in, x->x16, x->num_sms, st);
+    if (e == cudaSuccess)
+      e = moe::launch_widen_weights(a, gated ? 2ll * a.F : a.N, w, x->w16, x->num_sms, st);
+    return e != cudaSuccess ? e
+                            : moe::launch_expert_gemm(gated ? moe::kGatedCodes : moe::kDownCodes,
+                                                      false, a, x->x16, x->w16, x->num_sms, st);
   }
-  if (type == moe::kInt8) return moe::launch_expert_int8(op, a, in, w, x->num_sms, st);
   return moe::launch_expert_gemm(op, type == moe::kE4m3, a, in, w, x->num_sms, st);
 }
 
@@ -140,7 +141,7 @@ int moe_expert_create(const moe_expert_config_t* cfg, void* d_workspace, size_t 
   x->h32 = cfg->dtype == MOE_INT8
                ? reinterpret_cast<float*>(static_cast<char*>(d_workspace) + kAlign)
                : nullptr;
-  if (wide(cfg)) {
+  if (widens(cfg)) {
     char* at = static_cast<char*>(d_workspace) +
                align_up(kAlign + (size_t)cfg->rows_max * cfg->inter * 4);
     x->x16 = reinterpret_cast<uint16_t*>(at);

@@ -33,14 +33,34 @@ __device__ __forceinline__ uint32_t max4(uint32_t m, const float4 v) {
   return max(max(m, max(abs_bits(v.x), abs_bits(v.y))), max(abs_bits(v.z), abs_bits(v.w)));
 }
 
+// Two quotients v / s rounded to nearest, y = RN(1 / s): two corrections of the
+// product by the reciprocal, as minus_quotient in expert_gemm.cu has them, for s
+// between 2^-64 and 2^64 (with an IEEE division of each value this kernel takes
+// 46 us, with these 20: 10944 rows of 2048).
+__device__ __forceinline__ float2 quotient(float2 v, float s, float y) {
+  const float2 ns = make_float2(-s, -s), yy = make_float2(y, y);
+  float2 q = __fmul2_rn(v, yy);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) q = __ffma2_rn(__ffma2_rn(ns, q, v), yy, q);
+  return q;
+}
+
 // |v / s| is at most 127 or so: adding 1.5 * 2^23 rounds it to an integer,
 // ties to even, whose low byte is the code.
-__device__ __forceinline__ uint32_t code_bits(float v, float s) {
-  return __float_as_uint(__fadd_rn(__fdiv_rn(v, s), 12582912.0f));
-}
-__device__ __forceinline__ uint32_t codes4(const float4 v, float s) {
-  return __byte_perm(__byte_perm(code_bits(v.x, s), code_bits(v.y, s), 0x0040),
-                     __byte_perm(code_bits(v.z, s), code_bits(v.w, s), 0x0040), 0x5410);
+__device__ __forceinline__ uint32_t codes4(const float4 v, float s, float y) {
+  float2 a, b;
+  if (y != 0.0f) {
+    a = quotient(make_float2(v.x, v.y), s, y);
+    b = quotient(make_float2(v.z, v.w), s, y);
+  } else {
+    a = make_float2(__fdiv_rn(v.x, s), __fdiv_rn(v.y, s));
+    b = make_float2(__fdiv_rn(v.z, s), __fdiv_rn(v.w, s));
+  }
+  const float2 big = make_float2(12582912.0f, 12582912.0f);
+  a = __fadd2_rn(a, big);
+  b = __fadd2_rn(b, big);
+  return __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
+                     __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
 }
 
 // The maximum over the CTA; `buf` is not written again before the next barrier but one.
@@ -127,31 +147,34 @@ __global__ void __launch_bounds__(kThreads)
     const bool finite = m < 0x7f800000u;
     const float s = finite ? __fdiv_rn(__uint_as_float(m), 127.0f) : __uint_as_float(m);
     const bool any = finite && s > 0.0f;
+    const float y = s >= 0x1p-64f && s <= 0x1p64f ? __frcp_rn(s) : 0.0f;
     uint32_t* out = reinterpret_cast<uint32_t*>(codes + r * p.F);
     if (tid == 0) scale[r] = s;
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
       const int c = tid + i * kThreads;
-      if (c < n) out[c] = any ? codes4(v[i], s) : 0u;
+      if (c < n) out[c] = any ? codes4(v[i], s, y) : 0u;
     }
     for (int c = tid + kHeld * kThreads; c < n; c += kThreads)
-      out[c] = any ? codes4(__ldg(row + c), s) : 0u;
+      out[c] = any ? codes4(__ldg(row + c), s, y) : 0u;
   }
 }
 
 }  // namespace
 
-cudaError_t launch_expert_widen(const ExpertArgs& p, long long weight_rows, const void* a,
-                                const void* b, uint16_t* x16, uint16_t* w16, int num_sms,
-                                cudaStream_t st) {
-  const unsigned wide = 16u * num_sms, each = (wide + p.E - 1) / p.E;
-  const long long row = p.K / 16;
-  const cudaError_t e =
-      launch_pdl(k_widen<false>, dim3(wide), dim3(kThreads), 0, st, p,
-                 static_cast<const uint4*>(a), reinterpret_cast<uint4*>(x16), row);
-  if (e != cudaSuccess) return e;
+cudaError_t launch_widen_rows(const ExpertArgs& p, const void* a, uint16_t* x16, int num_sms,
+                              cudaStream_t st) {
+  return launch_pdl(k_widen<false>, dim3(16u * num_sms), dim3(kThreads), 0, st, p,
+                    static_cast<const uint4*>(a), reinterpret_cast<uint4*>(x16),
+                    (long long)p.K / 16);
+}
+
+cudaError_t launch_widen_weights(const ExpertArgs& p, long long weight_rows, const void* b,
+                                 uint16_t* w16, int num_sms, cudaStream_t st) {
+  const unsigned each = (16u * num_sms + p.E - 1) / p.E;
   return launch_pdl(k_widen<true>, dim3(each, p.E), dim3(kThreads), 0, st, p,
-                    static_cast<const uint4*>(b), reinterpret_cast<uint4*>(w16), weight_rows * row);
+                    static_cast<const uint4*>(b), reinterpret_cast<uint4*>(w16),
+                    weight_rows * (p.K / 16));
 }
 
 cudaError_t launch_expert_quantise(const ExpertArgs& p, const float* h, int8_t* codes,

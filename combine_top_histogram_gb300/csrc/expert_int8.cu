@@ -82,11 +82,12 @@ struct Plan {
   static_assert(kSteps % kPerBuffer == 0 && kTokens <= kMaxTokens && kTokens % 64 == 0, "");
 };
 using Many = Plan<192, 32, 4, 3, 2>;
-using Few = Plan<64, 64, 6, 4, 3>;
+using Some = Plan<128, 64, 4, 3, 2>;
+using Few = Plan<64, 64, 6, 3, 3>;
 
 // Registers of a thread: the launch's 28 warps x 72, split between the copying
 // and issuing warps (4), the converting (16) and the epilogue's (8), which hold
-// 64 sums at a time: 4 * 56 + 16 * 64 + 8 * 96 = 28 * 72.
+// 64 sums at a time: 4 * 40 + 16 * 64 + 8 * 104 = 28 * 72.
 constexpr int kRegisters = 72;
 
 struct Shared {
@@ -117,6 +118,33 @@ __device__ __forceinline__ int tile_tokens(int rows) {
   return (min(rows, P::kTokens) + kBoxTokens - 1) / kBoxTokens * kBoxTokens;
 }
 
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, const uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+
+// A store under a predicate, without a branch around it.
+__device__ __forceinline__ void store_if(void* p, uint32_t v, bool ok) {
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q st.global.b32 [%0], %1;\n\t}" ::"l"(
+                   p),
+               "r"(v), "r"((int)ok)
+               : "memory");
+}
+
+__device__ __forceinline__ uint32_t bf16x2(uint32_t lo, uint32_t hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(lo), __uint_as_float(hi));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 // A place in a ring of N buffers, and the parity of its phase.
 template <int N>
 struct Ring {
@@ -125,6 +153,12 @@ struct Ring {
   __device__ __forceinline__ void next() {
     if (++i == N) {
       i = 0;
+      phase ^= 1;
+    }
+  }
+  __device__ __forceinline__ void back() {
+    if (--i < 0) {
+      i = N - 1;
       phase ^= 1;
     }
   }
@@ -183,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kChannels = OP == kGated ? kBlock : 2 * kBlock;  // a tile's output channels
 
   if (warp < kConvWarp0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0) {  // weights
       Ring<P::kWStages> ring;
       uint32_t announced = 0;
@@ -271,13 +305,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t to =
         tmem + ((uint32_t)((warp & 3) * 32) << 16) + P::kOperand + block * P::kBlockColumns;
     const int ct = (cw & 7) * 32 + lane;     // thread of the group
-    // a step's 16-byte units: kWUnits of this thread's channel; of the tokens those
-    // numbered ct + 256 i, all first units before all second ones
+    // A step's 16-byte units: kWUnits of this thread's channel, and of the tokens
+    // those numbered ct + 256 i, all first units before all second ones. Unit u
+    // of a row lies at (u ^ row & 7) of its 128 bytes, so that the address of
+    // another unit is that of the first one (of this group's first step) with some bits turned.
     constexpr int kWUnits = P::kStepK / 16, kXUnits = P::kTokens * kWUnits;
-    constexpr int kPer = (kXUnits + 255) / 256;
+    constexpr int kPer = (kXUnits + 255) / 256, kOwnSteps = kStageK / P::kStepK / 2;
+    const uint32_t w0 = smem_u32(wring) + (block * kBlock + row) * kStageK +
+                        (((group * kWUnits) ^ (row & 7)) << 4);
+    uint32_t x0[kPer], o0[kPer];
+    int token[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int unit = (ct + 256 * i) / P::kTokens;
+      token[i] = ct + 256 * i < kXUnits ? (ct + 256 * i) % P::kTokens : P::kTokens;
+      const uint32_t r = token[i] * 128, m = token[i] & 7;
+      x0[i] = smem_u32(xring) + r + (((group * kWUnits + unit) ^ m) << 4);
+      o0[i] = smem_u32(buffers) + r + (((2 * unit) ^ m) << 4);
+    }
     Ring<P::kWStages> wr;
     Ring<P::kXStages> xr;
-    uint32_t base = 0;     // steps of the tiles before this one
+    Ring<P::kSteps> step;  // this group's next one
+    if (group == 1) step.next();
     int pending = -1;      // the step whose stores are under way
     // its stores are done and the products may read them
     const auto finish = [&] {
@@ -291,62 +340,64 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     bool ok = true;
     Tile t;
-    for (; ok && walk.next(t); base += step_count) {
+    while (ok && walk.next(t)) {
       const int n = tile_tokens<P>(t.rows);
       for (int j0 = 0; j0 < step_count; j0 += kStageK / P::kStepK) {
         const uint32_t wbar = smem_u32(&s.wfull[wr.i]), xbar = smem_u32(&s.xfull[xr.i]);
         if (!__all_sync(~0u, mbar_test(wbar, wr.phase) && mbar_test(xbar, xr.phase))) {
           finish();
-          ok = mbar_wait<false>(wbar, wr.phase, ctl) && mbar_wait<false>(xbar, xr.phase, ctl);
+          ok = mbar_wait<false>(wbar, wr.phase, ctl) &&
+               mbar_wait<false>(xbar, xr.phase, ctl);
           ok = __all_sync(~0u, ok);
           if (!ok) break;
         }
-        const uint4* w = reinterpret_cast<const uint4*>(wring + wr.i * kWBytes +
-                                                        (block * kBlock + row) * kStageK);
-        const uint4* x = reinterpret_cast<const uint4*>(xring + xr.i * P::kXBytes);
-#pragma unroll 1
-        for (int h = group; h < kStageK / P::kStepK; h += 2) {
-          if (j0 + h >= step_count) break;
-          const uint32_t number = base + j0 + h, at = number % P::kSteps;
-          uint4 c[kPer];
+        const uint32_t w = w0 + wr.i * kWBytes, x = xr.i * P::kXBytes;
 #pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            const int unit = (ct + 256 * i) / P::kTokens, token = (ct + 256 * i) % P::kTokens;
-            if (ct + 256 * i < kXUnits && token < n)
-              c[i] = x[token * 8 + ((kWUnits * h + unit) ^ (token & 7))];
-          }
-          uint32_t v[kWUnits / 2][16];  // 32 k of a channel each
+        for (int h = 0; h < kOwnSteps; ++h) {
+          if (j0 + 2 * h + group < step_count) {
+            constexpr int kTurn = 2 * kWUnits * 16;  // to the group's next step
+            uint4 c[kPer];
 #pragma unroll
-          for (int u = 0; u < kWUnits; ++u) {
-            const uint4 q = w[(kWUnits * h + u) ^ (row & 7)];
-            const uint32_t cc[4] = {q.x, q.y, q.z, q.w};
+            for (int i = 0; i < kPer; ++i)
+              if (token[i] < n) c[i] = lds128((x + x0[i]) ^ (h * kTurn));
+            uint32_t v[kWUnits / 2][16];  // 32 k of a channel each
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const uint2 f = int8_to_f16(cc[b]);
-              v[u / 2][u % 2 * 8 + 2 * b] = f.x;
-              v[u / 2][u % 2 * 8 + 2 * b + 1] = f.y;
+            for (int u = 0; u < kWUnits; ++u) {
+              const uint4 q = lds128(w ^ (h * kTurn + 16 * u));
+              const uint32_t cc[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+              for (int b = 0; b < 4; ++b) {
+                const uint2 f = int8_to_f16(cc[b]);
+                v[u / 2][u % 2 * 8 + 2 * b] = f.x;
+                v[u / 2][u % 2 * 8 + 2 * b + 1] = f.y;
+              }
             }
-          }
-          finish();  // the step before, beside whose stores this one's codes were converted
-          ok = __all_sync(~0u, mbar_wait<false>(smem_u32(&s.used[at]),
-                                                (number / P::kSteps & 1) ^ 1, ctl));
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll
-          for (int i = 0; i < kWUnits / 2; ++i) tc_st16(to + at * P::kStepColumns + 16 * i, v[i]);
-          uint4* out = reinterpret_cast<uint4*>(buffers + at / P::kPerBuffer * P::kBufferBytes);
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) {  // 16 k of a token: 32 bytes of fp16
-            const int unit = (ct + 256 * i) / P::kTokens, token = (ct + 256 * i) % P::kTokens;
-            if (ct + 256 * i < kXUnits && token < n) {
-              const int u = 2 * (at % P::kPerBuffer * kWUnits + unit);
-              const uint2 f0 = int8_to_f16(c[i].x), f1 = int8_to_f16(c[i].y),
-                          f2 = int8_to_f16(c[i].z), f3 = int8_to_f16(c[i].w);
-              out[token * 8 + (u ^ (token & 7))] = make_uint4(f0.x, f0.y, f1.x, f1.y);
-              out[token * 8 + ((u + 1) ^ (token & 7))] = make_uint4(f2.x, f2.y, f3.x, f3.y);
+            finish();  // the step before, beside whose stores this one's codes were converted
+            if (!__all_sync(~0u, mbar_test(smem_u32(&s.used[step.i]), step.phase ^ 1))) {
+              ok = __all_sync(
+                  ~0u, mbar_wait<false>(smem_u32(&s.used[step.i]), step.phase ^ 1, ctl));
+              if (!ok) break;
             }
+            tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < kWUnits / 2; ++i)
+              tc_st16(to + step.i * P::kStepColumns + 16 * i, v[i]);
+            const uint32_t buffer = step.i / P::kPerBuffer * P::kBufferBytes,
+                           turn = step.i % P::kPerBuffer * (2 * P::kStepK);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {  // 16 k of a token: 32 bytes of fp16
+              if (token[i] < n) {
+                const uint2 f0 = int8_to_f16(c[i].x), f1 = int8_to_f16(c[i].y),
+                            f2 = int8_to_f16(c[i].z), f3 = int8_to_f16(c[i].w);
+                const uint32_t o = (buffer + o0[i]) ^ turn;
+                sts128(o, make_uint4(f0.x, f0.y, f1.x, f1.y));
+                sts128(o ^ 16, make_uint4(f2.x, f2.y, f3.x, f3.y));
+              }
+            }
+            pending = step.i;
+            step.next();
+            step.next();
           }
-          pending = (int)at;
         }
         if (!ok) break;
         __syncwarp();
@@ -358,9 +409,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         xr.next();
       }
       finish();
+      // an odd number of steps: each group took every other one up to the last, so the first one's
+      // next is one too far and the second's one short
+      if (step_count & 1) {
+        if (group == 0) step.back();
+        else step.next();
+      }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     constexpr int kHalf = P::kTokens / 2;  // tokens of a warp
     const int quarter = warp & 3, half = (warp - kEpiWarp0) >> 2;
     const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16) + half * kHalf;
@@ -383,20 +440,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       dphase ^= 1;
       tc_fence_after();
-      // one token after the other: of 32 neighbouring channels a warp writes 128 bytes of h, or 64
-      // of y in each block
+      // Rounds of 32 tokens: all values, then all stores. A store before another token's value
+      // would hold that one's scale, which the compiler cannot tell from what is stored, until the
+      // first is done (gated, E = 19, 576 rows each, H = 1024, F = 2048: 142 / 135 us).
       using Out = std::conditional_t<OP == kGated, float, __nv_bfloat16>;
-      Out* out = static_cast<Out*>(p.out) + ((long long)t.row0 + half * kHalf) * p.N + c;
+      const int odd = OP == kGated ? 0 : lane & 1;
+      Out* out = static_cast<Out*>(p.out) + ((long long)t.row0 + half * kHalf + odd) * p.N + c - odd;
       const int rounds = left <= 0 ? 0 : min((left + 31) / 32, kHalf / 32);
       __syncwarp();  // the scales are written
 #pragma unroll 1
       for (int q = 0; q < rounds; ++q) {
-        uint32_t v0[32], v1[32];  // 32 tokens of the first block, and of the second
-        tc_ld32(v0, from + q * 32);
-        tc_ld32(v1, from + P::kAcc + q * 32);
+        uint32_t a[32], b[32];  // 32 tokens of the first block, and of the second
+        tc_ld32(a, from + q * 32);
+        tc_ld32(b, from + P::kAcc + q * 32);
         tc_wait_ld();
-        tc_loaded(v0);
-        tc_loaded(v1);
+        tc_loaded(a);
+        tc_loaded(b);
         if (q == rounds - 1) {
           tc_fence_before();
           __syncwarp();
@@ -405,15 +464,32 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           const float sr = scale[q * 32 + i];
-          const float a = __uint_as_float(v0[i]) * sr * w0;
-          const float b = __uint_as_float(v1[i]) * sr * w1;
+          const float f = __uint_as_float(a[i]) * sr * w0, g = __uint_as_float(b[i]) * sr * w1;
           if constexpr (OP == kGated) {
-            if (in0 && q * 32 + i < left) *out = silu(a) * b;
+            a[i] = __float_as_uint(silu(f) * g);
           } else {
-            if (in0 && q * 32 + i < left) *out = __float2bfloat16_rn(a);
-            if (in1 && q * 32 + i < left) out[kBlock] = __float2bfloat16_rn(b);
+            a[i] = __float_as_uint(f);
+            b[i] = __float_as_uint(g);
           }
-          out += p.N;
+        }
+        if constexpr (OP == kGated) {  // 32 channels of a token: 128 bytes
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            store_if(out, a[i], in0 && q * 32 + i < left);
+            out += p.N;
+          }
+        } else {
+          // Two tokens at a time: neighbouring lanes exchange theirs, and each holds two channels of
+          // one token (32 channels: 64 bytes of each of the two)
+          const uint32_t sel = odd ? 0x3276u : 0x5410u;
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const bool in = q * 32 + i + odd < left;
+            const uint32_t pa = bf16x2(a[i], a[i + 1]), pb = bf16x2(b[i], b[i + 1]);
+            store_if(out, __byte_perm(pa, __shfl_xor_sync(~0u, pa, 1), sel), in0 && in);
+            store_if(out + kBlock, __byte_perm(pb, __shfl_xor_sync(~0u, pb, 1), sel), in1 && in);
+            out += 2ll * p.N;
+          }
         }
       }
       if (rounds == 0 && lane == 0) mbar_arrive(smem_u32(&s.dempty));
@@ -445,10 +521,12 @@ cudaError_t launch(const ExpertArgs& args, const void* a, const void* b, int num
                     dim3(kThreads), smem_bytes<P>(), st, mx, mw, p);
 }
 
-#ifndef FEWROWS
-#define FEWROWS 64
-#endif
-bool use_few(const ExpertArgs& p) { return p.rows_max <= (long long)FEWROWS * p.E; }
+template <class P>
+cudaError_t launch(ExpertOp op, const ExpertArgs& p, const void* a, const void* b, int num_sms,
+                   cudaStream_t st) {
+  return op == kGated ? launch<kGated, P>(p, a, b, num_sms, st)
+                      : launch<kDown, P>(p, a, b, num_sms, st);
+}
 
 template <int OP, class P>
 cudaError_t prepare() {
@@ -467,6 +545,8 @@ cudaError_t prepare() {
 cudaError_t expert_int8_prepare() {
   cudaError_t e = prepare<kGated, Many>();
   if (e == cudaSuccess) e = prepare<kDown, Many>();
+  if (e == cudaSuccess) e = prepare<kGated, Some>();
+  if (e == cudaSuccess) e = prepare<kDown, Some>();
   if (e == cudaSuccess) e = prepare<kGated, Few>();
   if (e == cudaSuccess) e = prepare<kDown, Few>();
   return e;
@@ -474,11 +554,16 @@ cudaError_t expert_int8_prepare() {
 
 cudaError_t launch_expert_int8(ExpertOp op, const ExpertArgs& p, const void* a, const void* b,
                                int num_sms, cudaStream_t st) {
-  if (use_few(p))
-    return op == kGated ? launch<kGated, Few>(p, a, b, num_sms, st)
-                        : launch<kDown, Few>(p, a, b, num_sms, st);
-  return op == kGated ? launch<kGated, Many>(p, a, b, num_sms, st)
-                      : launch<kDown, Many>(p, a, b, num_sms, st);
+  // By average rows per expert (the host knows no others): an expert's weights are
+  // converted once for each of its tiles, so most should fit one, but what a
+  // tile could hold costs steps. us of Few / Some / Many, uniform routing (gated,
+  // E = 64, H = 7168, F = 2048): 366 / 410 / 472 at 32 rows, 438 / 443 / 494 at 56,
+  // 545 / 446 / 505 at 64, - / 457 / 535 at 96, - / 519 / 543 at 112,
+  // - / 646 / 551 at 128, - / 889 / 571 at 160, - / 1056 / 1122 at 256; 512 rows
+  // each of E = 19: - / 518 / 494.
+  if (p.rows_max <= 56ll * p.E) return launch<Few>(op, p, a, b, num_sms, st);
+  if (p.rows_max <= 112ll * p.E) return launch<Some>(op, p, a, b, num_sms, st);
+  return launch<Many>(op, p, a, b, num_sms, st);
 }
 
 }  // namespace moe

@@ -52,11 +52,12 @@ cudaError_t launch_expert_gemm(ExpertOp op, bool fp8, const ExpertArgs& args, co
 // kGated or kDown for a few rows (expert_rows.cu).
 cudaError_t launch_expert_rows(ExpertOp op, ExpertType type, const ExpertArgs& args, const void* a,
                                const void* b, int num_sms, cudaStream_t st);
-// INT8: kGated or kDown in two steps, codes widened to fp16 in memory (x16 [rows, K], w16: all
-// weights) and then a product of fp16 (expert_codes.cu, expert_gemm.cu).
-cudaError_t launch_expert_widen(const ExpertArgs& args, long long weight_rows, const void* a,
-                                const void* b, uint16_t* x16, uint16_t* w16, int num_sms,
-                                cudaStream_t st);
+// INT8: codes as fp16, of the segments' rows [rows, K], and of the weights [E, weight_rows, K] of
+// the experts that have rows (expert_codes.cu).
+cudaError_t launch_widen_rows(const ExpertArgs& args, const void* a, uint16_t* x16, int num_sms,
+                              cudaStream_t st);
+cudaError_t launch_widen_weights(const ExpertArgs& args, long long weight_rows, const void* b,
+                                 uint16_t* w16, int num_sms, cudaStream_t st);
 // INT8: codes [rows, F] and scales [rows] of the segments' rows of h (expert_codes.cu).
 cudaError_t launch_expert_quantise(const ExpertArgs& args, const float* h, int8_t* codes,
                                    float* scale, int num_sms, cudaStream_t st);

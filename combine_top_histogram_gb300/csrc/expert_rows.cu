@@ -189,45 +189,61 @@ __global__ void __launch_bounds__(kThreads, 2)
     const float* sa0 = p.sa + (row0 + min(2 * t, rows - 1)) * pieces;
     const float* sa1 = p.sa + (row0 + min(2 * t + 1, rows - 1)) * pieces;
     float acc[2][4] = {};
-    for (int c = ks; c < pieces; c += S * kAhead) {
-      uint4 w[kAhead][4][2], x[kAhead][2];
-      float s[kAhead][4];
+    uint4 w[kAhead][4][2], x[kAhead][2];
+    float s[kAhead][4];
+    const auto load = [&](int u, int cu) {
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int cu = c + u * S;
+      for (int h = 0; h < 2; ++h) {
+        const long long at = (long long)cu * 128 + h * 64 + t * 16;
+        const bool in = at < kbytes;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const long long at = (long long)cu * 128 + h * 64 + t * 16;
-          const bool in = at < kbytes;
+        for (int i = 0; i < 4; ++i) w[u][i][h] = stream_if(wp[i] + at, in && w_ok[i]);
+        x[u][h] = load_if(xp + at, in && g < rows);
+      }
+      if constexpr (FP8) {
+        const int k = min(cu, pieces - 1);
+        const float a0 = __ldg(sa0 + k), a1 = __ldg(sa1 + k);
+        const float b0 = __ldg(sb0 + k), b1 = __ldg(sb1 + k);
+        s[u][0] = a0 * b0;
+        s[u][1] = a1 * b0;
+        s[u][2] = a0 * b1;
+        s[u][3] = a1 * b1;
+      }
+    };
+    const auto multiply = [&](int u) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) w[u][i][h] = stream_if(wp[i] + at, in && w_ok[i]);
-          x[u][h] = load_if(xp + at, in && g < rows);
-        }
+      for (int j = 0; j < 2; ++j) {
+        float v[4] = {};
+        float(&d)[4] = FP8 ? v : acc[j];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) mma_piece<TYPE>(d, w[u][2 * j][h], w[u][2 * j + 1][h], x[u][h]);
         if constexpr (FP8) {
-          const int k = min(cu, pieces - 1);
-          const float a0 = __ldg(sa0 + k), a1 = __ldg(sa1 + k);
-          const float b0 = __ldg(sb0 + k), b1 = __ldg(sb1 + k);
-          s[u][0] = a0 * b0;
-          s[u][1] = a1 * b0;
-          s[u][2] = a0 * b1;
-          s[u][3] = a1 * b1;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[j][i] = fmaf(v[i], s[u][2 * j + (i & 1)], acc[j][i]);
         }
       }
+    };
+    if constexpr (INT8) {
+      // The conversions keep a warp busy for long, so the next piece is loaded into
+      // a place as soon as that is free (down of one token, E = 256, top-8, H = 7168,
+      // F = 2048: 37.9 / 24.5 us; the other types lose by it, gated e4m3 51 / 59 us).
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        if (c + u * S >= pieces) break;
+      for (int u = 0; u < kAhead; ++u) load(u, ks + u * S);
+      for (int c = ks; c < pieces; c += S * kAhead) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float v[4] = {};
-          float(&d)[4] = FP8 ? v : acc[j];
+        for (int u = 0; u < kAhead; ++u) {
+          if (c + u * S < pieces) multiply(u);
+          load(u, c + (u + kAhead) * S);
+        }
+      }
+    } else {
+      for (int c = ks; c < pieces; c += S * kAhead) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            mma_piece<TYPE>(d, w[u][2 * j][h], w[u][2 * j + 1][h], x[u][h]);
-          }
-          if constexpr (FP8) {
+        for (int u = 0; u < kAhead; ++u) load(u, c + u * S);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[j][i] = fmaf(v[i], s[u][2 * j + (i & 1)], acc[j][i]);
-          }
+        for (int u = 0; u < kAhead; ++u) {
+          if (c + u * S >= pieces) break;
+          multiply(u);
         }
       }
     }
@@ -351,7 +367,10 @@ cudaError_t launch(const ExpertArgs& p, const void* a, const void* b, int num_sm
   // two, one token of E = 256, top-8, H = 7168, F = 2048: down e4m3 24.2 / 24.3 /
   // 26.0, gated e4m3 55.8 / 44.4 / 44.2); two where the split's CTAs form clusters, which cost more (E = 64,
   // H = 2048, F = 1024, top-2: 11.7 / 11.2 / 9.6).
-  const long long enough = (OP == kGated && TYPE == kE4m3 ? 2ll : 3ll) * num_sms;
+  // int8 warps, which keep loading while they convert, need one (at three / one, L2 cold: gated
+  // 55 / 53, down 33 / 31).
+  const long long enough =
+      (TYPE == kInt8 ? 1ll : OP == kGated && TYPE == kE4m3 ? 2ll : 3ll) * num_sms;
   int s = 1;
   while (s < 8 && ctas(s) < enough) s *= 2;
   switch (s) {
