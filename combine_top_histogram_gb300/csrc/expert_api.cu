@@ -47,8 +47,8 @@ size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 // fp16 in memory for the products (see forward()). By the rows a configuration
 // can have: a call of fewer takes the same way.
 bool widens(const moe_expert_config_t* c) {
-  return c->dtype == MOE_INT8 && c->rows_max >= 1024ll * c->num_experts &&
-         (double)c->rows_max * c->hidden * c->inter >= 0x1p34;
+  return c->dtype == MOE_INT8 && c->rows_max >= 1280ll * c->num_experts &&
+         (double)c->rows_max * c->hidden * c->inter >= 0x1p32;
 }
 size_t x16_bytes(const moe_expert_config_t* c) {
   return align_up((size_t)c->rows_max * (c->hidden > c->inter ? c->hidden : c->inter) * 2);

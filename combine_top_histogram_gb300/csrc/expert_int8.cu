@@ -42,6 +42,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include <type_traits>
@@ -552,18 +553,34 @@ cudaError_t expert_int8_prepare() {
   return e;
 }
 
+// The plan with the least waves x time of a tile (single waves of gated, E = 1,
+// H = 4096, F = 2048, at 64 / 128 / 192 tokens a tile: 38 / 42 / 51 us, of which 9
+// are not the tile's). An expert's weights are converted once for each of its tiles, so a
+// tile should hold most experts' rows; where tiles are few, small ones spread
+// over more SMs. The host knows the rows and the experts, and takes the rows of
+// one to be within a standard deviation of a random choice of the experts. us of
+// Few / Some / Many, gated, H = 7168, F = 2048, random: E = 64, 32 rows 366 / 410 /
+// 472, 56 rows 438 / 443 / 494, 96 rows 757 / 457 / 535, 160 rows 1102 / 889 / 571,
+// 256 rows 1641 / 1056 / 1122; down, E = 1, 1024 rows 51 / 41 / 52; gated, E = 8,
+// H = 1024, F = 512, 512 rows 27 / 22 / 24. What it gives away: experts of
+// very unlike rows, and 256 rows each of E = 4, H = 2048, F = 1024 (24 / 27 / 31).
+template <class P>
+static double plan_cost(ExpertOp op, const ExpertArgs& p, int num_sms, double tile) {
+  const double experts = p.E < p.rows_max ? p.E : (double)p.rows_max, rows = p.rows_max / experts;
+  const double spread = experts > 1 ? sqrt(rows) : 0.0;
+  double tiles = 0.0;
+  for (int z = -1; z <= 1; ++z) tiles += ceil((rows + z * spread) / P::kTokens) / 3;
+  const int channels = op == kGated ? kBlock : 2 * kBlock;
+  return ceil(tiles * experts * ((p.N + channels - 1) / channels) / num_sms) * tile;
+}
+
 cudaError_t launch_expert_int8(ExpertOp op, const ExpertArgs& p, const void* a, const void* b,
                                int num_sms, cudaStream_t st) {
-  // By average rows per expert (the host knows no others): an expert's weights are
-  // converted once for each of its tiles, so most should fit one, but what a
-  // tile could hold costs steps. us of Few / Some / Many, uniform routing (gated,
-  // E = 64, H = 7168, F = 2048): 366 / 410 / 472 at 32 rows, 438 / 443 / 494 at 56,
-  // 545 / 446 / 505 at 64, - / 457 / 535 at 96, - / 519 / 543 at 112,
-  // - / 646 / 551 at 128, - / 889 / 571 at 160, - / 1056 / 1122 at 256; 512 rows
-  // each of E = 19: - / 518 / 494.
-  if (p.rows_max <= 56ll * p.E) return launch<Few>(op, p, a, b, num_sms, st);
-  if (p.rows_max <= 112ll * p.E) return launch<Some>(op, p, a, b, num_sms, st);
-  return launch<Many>(op, p, a, b, num_sms, st);
+  const double few = plan_cost<Few>(op, p, num_sms, 29), some = plan_cost<Some>(op, p, num_sms, 33),
+               many = plan_cost<Many>(op, p, num_sms, 42);
+  if (few <= some && few <= many) return launch<Few>(op, p, a, b, num_sms, st);
+  return some <= many ? launch<Some>(op, p, a, b, num_sms, st)
+                      : launch<Many>(op, p, a, b, num_sms, st);
 }
 
 }  // namespace moe
