@@ -4,6 +4,8 @@
 
 serve: FP8. Routes a decode batch and a single token, dispatches e4m3 rows,
 runs the gated experts on e4m3 weights with 128 x 128 block scales and combines.
+serve_int8: the same with int8 rows (a scale for each token) and int8 weights (a
+scale for each output channel).
 train: bf16. Fits a small layer to a fixed random target: forward, the gradients
 of combine, experts and dispatch, the router's softmax in plain torch, and plain
 SGD. Prints the loss, which falls.
@@ -33,12 +35,19 @@ def init_experts(E, H, F, seed=0):
             new(E, H, F).normal_(0, F ** -0.5, generator=g))
 
 
-def serve(P=8, E=64, k=8, H=2048, F=1024):
+def quantise_channels(w):
+    """int8 codes and fp32 scales of each output channel (row) of w [E, n, m]."""
+    scale = (w.float().abs().amax(2) / 127.0).clamp_min(1e-30)
+    return torch.round(w.float() / scale[..., None]).to(torch.int8), scale
+
+
+def serve(dtype=moe.MOE_FP8_E4M3, quantise=quantise_weights, most=0.1, P=8, E=64, k=8, H=2048,
+          F=1024):
     w13, w2 = init_experts(E, H, F)
-    (q13, s13), (q2, s2) = quantise_weights(w13), quantise_weights(w2)
+    (q13, s13), (q2, s2) = quantise(w13), quantise(w2)
     g = torch.Generator(device="cuda").manual_seed(1)
     for ranks, tokens in ((P, 16), (1, 1)):  # a batch over P ranks, then one token
-        layer = moe.MoeLayer(ranks, tokens, E, k, H, moe.MOE_FP8_E4M3)
+        layer = moe.MoeLayer(ranks, tokens, E, k, H, dtype)
         layer.set_experts(q13, q2, s13, s2)
         x = torch.empty(layer.T, H, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
         logits = torch.randn(layer.T, E, device="cuda", generator=g)
@@ -53,7 +62,13 @@ def serve(P=8, E=64, k=8, H=2048, F=1024):
                 want.index_add_(0, t, layer.w[t, j, None] * (h @ w2[e].float().T))
         err = ((out.float() - want).norm() / want.norm()).item()
         print(f"serve {layer.T} tokens: relative distance from the bf16 layer {err:.4f}", flush=True)
-        assert err < 0.1 and layer.status() == 0 and layer.experts.status() == 0
+        assert err < most and layer.status() == 0 and layer.experts.status() == 0
+
+
+def serve_int8():
+    # of normal values whose amax is some four deviations, half a step is 1 / 64 of a deviation
+    # at most: of x, h and both weights, no more than 4 / 64 together
+    serve(moe.MOE_INT8, quantise_channels, most=4 / 64)
 
 
 def train(P=4, Tr=64, E=8, k=2, H=256, F=128, steps=60, lr=0.05):
@@ -86,4 +101,5 @@ def train(P=4, Tr=64, E=8, k=2, H=256, F=128, steps=60, lr=0.05):
 
 if __name__ == "__main__":
     serve()
+    serve_int8()
     train()

@@ -3,6 +3,8 @@ quantiser, code for code, in every form it has; the experts' products and the
 quantised h against 64 bits; whole layers, captured ones, other streams; what is
 not touched and what is refused."""
 import ctypes
+import importlib.util
+import os
 
 import pytest
 import torch
@@ -67,13 +69,12 @@ def check_dispatch(layer, x, ids, w, recv, scale, meta):
     assert layer.status() == 0
 
 
-@pytest.mark.parametrize("form", ["dispatch", "two_stage", "fixed_slots", "tokens"])
-@pytest.mark.parametrize("case", list(DISPATCH))
+@pytest.mark.parametrize("case, form", [
+    (case, form) for form in ("dispatch", "two_stage", "fixed_slots", "tokens") for case in DISPATCH
+    if form != "fixed_slots" or not DISPATCH[case][5]])  # fixed slots have no capacity
 def test_dispatch(gpu, case, form):
     from combine_top_histogram_gb300 import MoeLayer
     P, Tr, E, k, H, cap, at = DISPATCH[case]
-    if form == "fixed_slots" and cap:
-        pytest.skip("fixed slots have no capacity")
     T = P * Tr
     layer = MoeLayer(P, Tr, E, k, H, B.MOE_INT8, cap)
     x, (ids, w) = tokens(T, H, offset=at), routed(T, E, k)
@@ -300,6 +301,15 @@ def test_two_handles_on_two_streams(gpu):
     torch.cuda.synchronize()
     for h, x, xs, w13, ws, hid, hs, st in jobs:
         Q.check_quantised(hid, hs, *Q.gated(x, xs, w13, ws, counts))
+
+
+def test_example(gpu):
+    spec = importlib.util.spec_from_file_location(
+        "moe_layer_example", os.path.join(os.path.dirname(__file__), "..", "examples",
+                                          "moe_layer.py"))
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    m.serve_int8()
 
 
 def test_refusals(gpu, cuda_lib):
