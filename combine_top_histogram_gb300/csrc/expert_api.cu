@@ -44,22 +44,33 @@ int validate(const moe_expert_config_t* c) {
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
 // INT8 with many rows an expert: the codes of rows and weights are widened to
-// fp16 in memory for the products (see forward()). By the rows a configuration
+// fp16 in memory for the product, which then runs at the paired fp16 rate and
+// not at that of the conversions on the way to it (expert_int8.cu). us, converted /
+// widened: down, H = 7168, F = 2048, E = 8, 1536 rows each 278 / 324, 2048 361 / 350,
+// 4096 665 / 583, E = 1, 4096 rows 103 / 81; gated 2048 646 / 722, 4096 1247 / 1244,
+// H = 4096, F = 1408, 8192 1044 / 997; small products lose the extra launches
+// (down, E = 1, H = 2048, F = 1024, 4096 rows 24.8 / 25.3). By the rows a configuration
 // can have: a call of fewer takes the same way.
-bool widens(const moe_expert_config_t* c) {
-  return c->dtype == MOE_INT8 && c->rows_max >= 1280ll * c->num_experts &&
-         (double)c->rows_max * c->hidden * c->inter >= 0x1p32;
+bool widens(const moe_expert_config_t* c, moe::ExpertOp op) {
+  return c->dtype == MOE_INT8 &&
+         c->rows_max >= (op == moe::kGated ? 4096ll : 2048ll) * c->num_experts &&
+         (double)c->rows_max * c->hidden * c->inter >= 0x1p34;
 }
+// What that takes, at most: the rows' and the weights' fp16.
 size_t x16_bytes(const moe_expert_config_t* c) {
-  return align_up((size_t)c->rows_max * (c->hidden > c->inter ? c->hidden : c->inter) * 2);
+  const size_t k = widens(c, moe::kGated) && c->hidden > c->inter ? c->hidden
+                   : widens(c, moe::kDown)                         ? c->inter
+                                                                   : 0;
+  return align_up((size_t)c->rows_max * k * 2);
 }
 size_t w16_bytes(const moe_expert_config_t* c) {
-  return (size_t)c->num_experts * c->inter * c->hidden * 4;
+  const size_t n = widens(c, moe::kGated) ? 2 : widens(c, moe::kDown) ? 1 : 0;
+  return n * c->num_experts * c->inter * c->hidden * 2;
 }
 
 size_t workspace_bytes(const moe_expert_config_t* c) {
   size_t n = kAlign + (c->train || c->dtype == MOE_INT8 ? (size_t)c->rows_max * c->inter * 4 : 0);
-  if (widens(c)) n = align_up(n) + x16_bytes(c) + w16_bytes(c);
+  if (w16_bytes(c)) n = align_up(n) + x16_bytes(c) + w16_bytes(c);
   return n;
 }
 
@@ -94,8 +105,7 @@ cudaError_t forward(moe_expert_t x, moe::ExpertOp op, const moe::ExpertArgs& a, 
   const moe::ExpertType type = static_cast<moe::ExpertType>(x->cfg.dtype);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (use_rows(x, op)) return moe::launch_expert_rows(op, type, a, in, w, x->num_sms, st);
-  if (type == moe::kInt8 && !x->x16) return moe::launch_expert_int8(op, a, in, w, x->num_sms, st);
-  if (type == moe::kInt8) {
+  if (type == moe::kInt8 && widens(&x->cfg, op)) {
     const bool gated = op == moe::kGated;
     cudaError_t e = moe::launch_widen_rows(a, in, x->x16, x->num_sms, st);
     if (e == cudaSuccess)
@@ -104,6 +114,7 @@ cudaError_t forward(moe_expert_t x, moe::ExpertOp op, const moe::ExpertArgs& a, 
                             : moe::launch_expert_gemm(gated ? moe::kGatedCodes : moe::kDownCodes,
                                                       false, a, x->x16, x->w16, x->num_sms, st);
   }
+  if (type == moe::kInt8) return moe::launch_expert_int8(op, a, in, w, x->num_sms, st);
   return moe::launch_expert_gemm(op, type == moe::kE4m3, a, in, w, x->num_sms, st);
 }
 
@@ -141,7 +152,7 @@ int moe_expert_create(const moe_expert_config_t* cfg, void* d_workspace, size_t 
   x->h32 = cfg->dtype == MOE_INT8
                ? reinterpret_cast<float*>(static_cast<char*>(d_workspace) + kAlign)
                : nullptr;
-  if (widens(cfg)) {
+  if (w16_bytes(cfg)) {
     char* at = static_cast<char*>(d_workspace) +
                align_up(kAlign + (size_t)cfg->rows_max * cfg->inter * 4);
     x->x16 = reinterpret_cast<uint16_t*>(at);

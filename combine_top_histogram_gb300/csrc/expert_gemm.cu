@@ -1024,18 +1024,19 @@ EncodeTiled encode_tiled() {
 }  // namespace
 
 cudaError_t make_map(CUtensorMap* m, const void* base, bool fp8, long long cols, long long rows,
-                     long long planes, int box_rows) {
+                     long long planes, int box_rows, int row_bytes) {
   const EncodeTiled enc = encode_tiled();
   if (!enc) return cudaErrorNotSupported;
   const long long elt = fp8 ? 1 : 2;
   const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
   const cuuint64_t strides[2] = {(cuuint64_t)(cols * elt), (cuuint64_t)(cols * elt * rows)};
-  const cuuint32_t box[3] = {(cuuint32_t)(128 / elt), (cuuint32_t)box_rows, 1};
+  const cuuint32_t box[3] = {(cuuint32_t)(row_bytes / elt), (cuuint32_t)box_rows, 1};
   const cuuint32_t ones[3] = {1, 1, 1};
   const CUresult rc =
       enc(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
           planes > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, ones,
-          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+          CU_TENSOR_MAP_INTERLEAVE_NONE,
+          row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return rc == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }

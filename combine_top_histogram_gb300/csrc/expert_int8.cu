@@ -57,54 +57,61 @@ namespace moe {
 namespace {
 
 constexpr int kBlock = 128;            // channels of a block: lanes of an accumulator
-constexpr int kBoxTokens = 32;         // tokens of one copy
 constexpr int kConvWarp0 = 4, kConvWarps = 16, kEpiWarp0 = 20, kEpiWarps = 8;
 constexpr int kThreads = 896;
-constexpr int kStageK = 128;           // k of a stage, 128 bytes a row
+constexpr int kStageK = 128;           // k of a stage of weights, 128 bytes a row
+constexpr int kStepK = 64;             // k of a step and of a stage of tokens, 64 bytes a row
 constexpr int kWBytes = 2 * kBlock * kStageK;
-constexpr int kMaxTokens = 192, kMaxStages = 4, kMaxSteps = 6;
+constexpr uint32_t kBlockColumns = kStepK / 2, kStepColumns = 2 * kBlockColumns;
+constexpr int kMaxTokens = 192, kMaxRing = 6;
 
-// TOKENS of a tile, k of a step, steps that are converted and not yet
-// multiplied, and stages of weights and of tokens.
-template <int TOKENS, int STEP_K, int STEPS, int W_STAGES, int X_STAGES>
+// TOKENS of a tile; SLOTS of the tensor memory for a step's fp16 weights;
+// stages of codes of weights and tokens; BUFFERS of a step's fp16 tokens; BOX:
+// tokens of one copy.
+template <int TOKENS, int SLOTS, int W_STAGES, int X_STAGES, int BUFFERS, int BOX>
 struct Plan {
-  static constexpr int kTokens = TOKENS, kStepK = STEP_K, kSteps = STEPS;
+  // of the largest tiles, shared memory has room for no more experts' segments
+  static constexpr int kExperts = TOKENS == 192 ? 768 : MOE_MAX_EXPERTS;
+  // the second half of a step's weights is converted after the slot is free: a few
+  // more cycles there, but registers for the rest where a thread has two tokens or three
+  static constexpr bool kSplit = TOKENS > 64;
+  static constexpr int kTokens = TOKENS, kSlots = SLOTS, kBuffers = BUFFERS, kBox = BOX;
   static constexpr int kWStages = W_STAGES, kXStages = X_STAGES;
-  static constexpr int kXBytes = kTokens * kStageK;
-  // fp16 of the tokens: 64 k, 128 bytes a token
-  static constexpr int kPerBuffer = 64 / kStepK, kBufferBytes = kTokens * 128;
+  static constexpr int kXBytes = kTokens * kStepK, kBufferBytes = kTokens * 2 * kStepK;
   static constexpr uint32_t kAcc = kTokens;       // tensor-memory columns of an accumulator
   static constexpr uint32_t kOperand = 2 * kAcc;  // first column of the fp16 weights
-  static constexpr uint32_t kBlockColumns = kStepK / 2, kStepColumns = 2 * kBlockColumns;
   static constexpr int kRingBytes =
-      kWStages * kWBytes + kXStages * kXBytes + kSteps / kPerBuffer * kBufferBytes;
-  static_assert(kOperand + kSteps * kStepColumns <= 512, "tensor memory");
-  static_assert(kWStages <= kMaxStages && kXStages <= kMaxStages && kSteps <= kMaxSteps, "");
-  static_assert(kSteps % kPerBuffer == 0 && kTokens <= kMaxTokens && kTokens % 64 == 0, "");
+      kWStages * kWBytes + kXStages * kXBytes + kBuffers * kBufferBytes;
+  static_assert(kOperand + kSlots * kStepColumns <= 512, "tensor memory");
+  static_assert(kWStages <= kMaxRing && kXStages <= kMaxRing && kSlots <= kMaxRing &&
+                kBuffers <= kMaxRing, "");
+  static_assert(kTokens <= kMaxTokens && kTokens % 64 == 0 && kTokens % kBox == 0 &&
+                kXBytes % 1024 == 0, "");
 };
-using Many = Plan<192, 32, 4, 3, 2>;
-using Some = Plan<128, 64, 4, 3, 2>;
-using Few = Plan<64, 64, 6, 3, 3>;
+using Many = Plan<192, 2, 3, 4, 3, 64>;
+using Some = Plan<128, 4, 3, 6, 3, 64>;
+using Few = Plan<64, 6, 4, 4, 4, 32>;
 
 // Registers of a thread: the launch's 28 warps x 72, split between the copying
 // and issuing warps (4), the converting (16) and the epilogue's (8), which hold
 // 64 sums at a time: 4 * 40 + 16 * 64 + 8 * 104 = 28 * 72.
 constexpr int kRegisters = 72;
 
+template <class P>
 struct Shared {
-  uint64_t wfull[kMaxStages], wempty[kMaxStages], xfull[kMaxStages], xempty[kMaxStages];
-  uint64_t ready[kMaxSteps], used[kMaxSteps];
+  uint64_t wfull[kMaxRing], wempty[kMaxRing], xfull[kMaxRing], xempty[kMaxRing];
+  uint64_t ready[kMaxRing], used[kMaxRing], xused[kMaxRing];
   uint64_t dfull, dempty, drain;
-  float scale[kEpiWarps][kMaxTokens / 2];  // of an epilogue warp's tokens
+  float scale[kEpiWarps][P::kTokens / 2];  // of an epilogue warp's tokens
   uint32_t tmem;
   int abort;
-  int off[MOE_MAX_EXPERTS + 1];
-  int pre[MOE_MAX_EXPERTS + 1];        // row tiles before expert e
+  int off[P::kExperts + 1];
+  int pre[P::kExperts + 1];            // row tiles before expert e
 };
 
 template <class P>
 constexpr int smem_bytes() {
-  constexpr int bytes = 1024 + P::kRingBytes + (int)sizeof(Shared);
+  constexpr int bytes = 1024 + P::kRingBytes + (int)sizeof(Shared<P>);
   static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
   // more than half of an SM's: a second CTA, and with it a second allocation
   // of the tensor memory, never shares it
@@ -112,11 +119,16 @@ constexpr int smem_bytes() {
   return bytes;
 }
 
-// Tokens of a tile that are copied, converted and multiplied: the segment's, up
-// to a whole number of copies.
+// Tokens of a tile that are converted and multiplied.
 template <class P>
 __device__ __forceinline__ int tile_tokens(int rows) {
-  return (min(rows, P::kTokens) + kBoxTokens - 1) / kBoxTokens * kBoxTokens;
+  return (min(rows, P::kTokens) + 31) / 32 * 32;
+}
+
+// All lanes wait for the phase of the given parity; false when a wait gave up.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtl& ctl) {
+  if (__all_sync(~0u, mbar_test(bar, parity))) return true;
+  return __all_sync(~0u, mbar_wait<false>(bar, parity, ctl));
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -157,6 +169,13 @@ struct Ring {
       phase ^= 1;
     }
   }
+  __device__ __forceinline__ void skip() {  // to the next but one
+    i += 2;
+    if (i >= N) {
+      i -= N;
+      phase ^= 1;
+    }
+  }
   __device__ __forceinline__ void back() {
     if (--i < 0) {
       i = N - 1;
@@ -181,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* wring = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* xring = wring + P::kWStages * kWBytes;
   uint8_t* buffers = xring + P::kXStages * P::kXBytes;
-  Shared& s = *reinterpret_cast<Shared*>(wring + P::kRingBytes);
+  Shared<P>& s = *reinterpret_cast<Shared<P>*>(wring + P::kRingBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (warp == 2) tc_alloc<1>(smem_u32(&s.tmem), 512);
@@ -193,12 +212,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < P::kXStages; ++i) {
       mbar_init(smem_u32(&s.xfull[i]), 1);
-      mbar_init(smem_u32(&s.xempty[i]), kConvWarps);
+      mbar_init(smem_u32(&s.xempty[i]), kConvWarps / 2);
     }
-    for (int i = 0; i < P::kSteps; ++i) {
+    for (int i = 0; i < P::kSlots; ++i) {
       mbar_init(smem_u32(&s.ready[i]), kConvWarps / 2);
       mbar_init(smem_u32(&s.used[i]), 1);
     }
+    for (int i = 0; i < P::kBuffers; ++i) mbar_init(smem_u32(&s.xused[i]), 1);
     mbar_init(smem_u32(&s.dfull), 1);
     mbar_init(smem_u32(&s.dempty), kEpiWarps);
     mbar_init(smem_u32(&s.drain), 1);
@@ -213,8 +233,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = s.tmem;
   const WaitCtl ctl{&s.abort, 0u, p.wait_limit, p.status};
-  Walk<false, P::kTokens, Shared> walk(p, s, kStageK, 0, blockIdx.x, gridDim.x);
-  const int step_count = (p.K + P::kStepK - 1) / P::kStepK;  // of a tile
+  Walk<false, P::kTokens, Shared<P>> walk(p, s, kStageK, 0, blockIdx.x, gridDim.x);
+  const int step_count = (p.K + kStepK - 1) / kStepK;  // of a tile
   constexpr int kChannels = OP == kGated ? kBlock : 2 * kBlock;  // a tile's output channels
 
   if (warp < kConvWarp0) {
@@ -249,15 +269,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       Tile t;
       while (ok && walk.next(t)) {
-        const int blocks = __shfl_sync(~0u, t.kb, 0), row0 = __shfl_sync(~0u, t.row0, 0);
-        const int n = tile_tokens<P>(__shfl_sync(~0u, t.rows, 0));
-        for (int kb = 0; kb < blocks; ++kb) {
+        const int row0 = __shfl_sync(~0u, t.row0, 0);
+        const int n = tile_tokens<P>(__shfl_sync(~0u, t.rows, 0)), copies = (n + P::kBox - 1) / P::kBox;
+        for (int j = 0; j < step_count; ++j) {
           ok = __all_sync(~0u, mbar_wait<false>(smem_u32(&s.xempty[ring.i]), ring.phase ^ 1, ctl));
           if (!ok) break;
           const uint32_t bar = smem_u32(&s.xfull[ring.i]), x = smem_u32(xring) + ring.i * P::kXBytes;
-          mbar_expect_elected(bar, n * kStageK);
-          for (int i = 0; i < n; i += kBoxTokens)
-            tma_load_2d<1>(x + i * kStageK, &map_x, bar, kb * kStageK, row0 + i);
+          mbar_expect_elected(bar, copies * P::kBox * kStepK);
+          for (int i = 0; i < copies; ++i)
+            tma_load_2d<1>(x + i * P::kBox * kStepK, &map_x, bar, j * kStepK, row0 + i * P::kBox);
           ++announced;
           ring.next();
         }
@@ -265,7 +285,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       drain_ring<P::kXStages>(s.xfull, announced);
       __syncwarp();
     } else if (warp == 1) {
-      Ring<P::kSteps> ring;
+      Ring<P::kSlots> slot;
+      Ring<P::kBuffers> buffer;
       uint32_t dphase = 1;
       bool ok = true;
       Tile t;
@@ -276,21 +297,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         dphase ^= 1;
         for (int j = 0; j < step_count; ++j) {
-          ok = __all_sync(~0u, mbar_wait<false>(smem_u32(&s.ready[ring.i]), ring.phase, ctl));
+          ok = __all_sync(~0u, mbar_wait<false>(smem_u32(&s.ready[slot.i]), slot.phase, ctl));
           if (!ok) break;
           tc_fence_after();
-          const uint32_t a = tmem + P::kOperand + ring.i * P::kStepColumns;
-          const uint64_t b =
-              smem_desc(smem_u32(buffers) + ring.i / P::kPerBuffer * P::kBufferBytes +
-                            ring.i % P::kPerBuffer * (2 * P::kStepK),
-                        16, 1024);
+          const uint32_t a = tmem + P::kOperand + slot.i * kStepColumns;
+          const uint64_t b = smem_desc(smem_u32(buffers) + buffer.i * P::kBufferBytes, 16, 1024);
 #pragma unroll
-          for (int k = 0; k < P::kStepK / 16; ++k) {  // 16 k: 8 columns of A, 32 bytes of a row of B
+          for (int k = 0; k < kStepK / 16; ++k) {  // 16 k: 8 columns of A, 32 bytes of a row of B
             tc_mma_ta<1>(tmem, a + 8 * k, b + 2 * k, idesc, j > 0 || k > 0);
-            tc_mma_ta<1>(tmem + P::kAcc, a + P::kBlockColumns + 8 * k, b + 2 * k, idesc, j > 0 || k > 0);
+            tc_mma_ta<1>(tmem + P::kAcc, a + kBlockColumns + 8 * k, b + 2 * k, idesc, j > 0 || k > 0);
           }
-          tc_commit<1>(smem_u32(&s.used[ring.i]));
-          ring.next();
+          tc_commit<1>(smem_u32(&s.used[slot.i]));
+          tc_commit<1>(smem_u32(&s.xused[buffer.i]));
+          slot.next();
+          buffer.next();
         }
         if (ok) tc_commit<1>(smem_u32(&s.dfull));
       }
@@ -304,117 +324,116 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int cw = warp - kConvWarp0, group = cw >> 3, block = (cw >> 2) & 1;
     const int row = (warp & 3) * 32 + lane;  // of the weight block: its lane of tensor memory
     const uint32_t to =
-        tmem + ((uint32_t)((warp & 3) * 32) << 16) + P::kOperand + block * P::kBlockColumns;
+        tmem + ((uint32_t)((warp & 3) * 32) << 16) + P::kOperand + block * kBlockColumns;
     const int ct = (cw & 7) * 32 + lane;     // thread of the group
-    // A step's 16-byte units: kWUnits of this thread's channel, and of the tokens
-    // those numbered ct + 256 i, all first units before all second ones. Unit u
-    // of a row lies at (u ^ row & 7) of its 128 bytes, so that the address of
-    // another unit is that of the first one (of this group's first step) with some bits turned.
-    constexpr int kWUnits = P::kStepK / 16, kXUnits = P::kTokens * kWUnits;
-    constexpr int kPer = (kXUnits + 255) / 256, kOwnSteps = kStageK / P::kStepK / 2;
+    // A step's 16-byte units: four of this thread's channel, and of the tokens those
+    // numbered ct + 256 i, all first units before all second ones and so on. The
+    // copies leave unit u of a weight row at u ^ (row & 7) of its 128 bytes, and of a token at
+    // u ^ (token / 2 & 3) of its 64; the products want unit u of a token's fp16 at u ^ (token & 7).
+    constexpr int kPer = P::kTokens * 4 / 256;
     const uint32_t w0 = smem_u32(wring) + (block * kBlock + row) * kStageK +
-                        (((group * kWUnits) ^ (row & 7)) << 4);
+                        (((group * 4) ^ (row & 7)) << 4);
     uint32_t x0[kPer], o0[kPer];
-    int token[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int unit = (ct + 256 * i) / P::kTokens;
-      token[i] = ct + 256 * i < kXUnits ? (ct + 256 * i) % P::kTokens : P::kTokens;
-      const uint32_t r = token[i] * 128, m = token[i] & 7;
-      x0[i] = smem_u32(xring) + r + (((group * kWUnits + unit) ^ m) << 4);
-      o0[i] = smem_u32(buffers) + r + (((2 * unit) ^ m) << 4);
+      const int unit = (ct + 256 * i) / P::kTokens, token = (ct + 256 * i) % P::kTokens;
+      x0[i] = smem_u32(xring) + token * 64 + ((unit ^ (token >> 1 & 3)) << 4);
+      o0[i] = smem_u32(buffers) + token * 128 + (((2 * unit) ^ (token & 7)) << 4);
     }
     Ring<P::kWStages> wr;
+    // this group's next step
     Ring<P::kXStages> xr;
-    Ring<P::kSteps> step;  // this group's next one
-    if (group == 1) step.next();
-    int pending = -1;      // the step whose stores are under way
-    // its stores are done and the products may read them
-    const auto finish = [&] {
-      if (pending < 0) return;
-      fence_async_smem();
-      tc_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&s.ready[pending]));
-      pending = -1;
-    };
+    Ring<P::kBuffers> buffer;
+    Ring<P::kSlots> slot;
+    if (group == 1) {
+      xr.next();
+      buffer.next();
+      slot.next();
+    }
     bool ok = true;
     Tile t;
     while (ok && walk.next(t)) {
-      const int n = tile_tokens<P>(t.rows);
-      for (int j0 = 0; j0 < step_count; j0 += kStageK / P::kStepK) {
-        const uint32_t wbar = smem_u32(&s.wfull[wr.i]), xbar = smem_u32(&s.xfull[xr.i]);
-        if (!__all_sync(~0u, mbar_test(wbar, wr.phase) && mbar_test(xbar, xr.phase))) {
-          finish();
-          ok = mbar_wait<false>(wbar, wr.phase, ctl) &&
-               mbar_wait<false>(xbar, xr.phase, ctl);
-          ok = __all_sync(~0u, ok);
+      bool mine[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        mine[i] = (ct + 256 * i) % P::kTokens < tile_tokens<P>(t.rows);
+      for (int j0 = 0; j0 < step_count; j0 += 2) {
+        if (j0 + group < step_count) {
+          // 16 k of a token: 32 bytes of fp16
+          ok = warp_wait(smem_u32(&s.xfull[xr.i]), xr.phase, ctl);
           if (!ok) break;
-        }
-        const uint32_t w = w0 + wr.i * kWBytes, x = xr.i * P::kXBytes;
+          uint4 c[kPer];
 #pragma unroll
-        for (int h = 0; h < kOwnSteps; ++h) {
-          if (j0 + 2 * h + group < step_count) {
-            constexpr int kTurn = 2 * kWUnits * 16;  // to the group's next step
-            uint4 c[kPer];
+          for (int i = 0; i < kPer; ++i)
+            if (mine[i]) c[i] = lds128(x0[i] + xr.i * P::kXBytes);
+          ok = warp_wait(smem_u32(&s.xused[buffer.i]), buffer.phase ^ 1, ctl);
+          if (!ok) break;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i)
-              if (token[i] < n) c[i] = lds128((x + x0[i]) ^ (h * kTurn));
-            uint32_t v[kWUnits / 2][16];  // 32 k of a channel each
+          for (int i = 0; i < kPer; ++i) {
+            if (mine[i]) {
+              const uint2 f0 = int8_to_f16(c[i].x), f1 = int8_to_f16(c[i].y),
+                          f2 = int8_to_f16(c[i].z), f3 = int8_to_f16(c[i].w);
+              const uint32_t o = o0[i] + buffer.i * P::kBufferBytes;
+              sts128(o, make_uint4(f0.x, f0.y, f1.x, f1.y));
+              sts128(o ^ 16, make_uint4(f2.x, f2.y, f3.x, f3.y));
+            }
+          }
+          // 64 k of a channel
+          ok = warp_wait(smem_u32(&s.wfull[wr.i]), wr.phase, ctl);
+          if (!ok) break;
+          const uint32_t w = w0 + wr.i * kWBytes;
+          uint32_t v[2][16];
+          const auto widen = [&](int half) {
 #pragma unroll
-            for (int u = 0; u < kWUnits; ++u) {
-              const uint4 q = lds128(w ^ (h * kTurn + 16 * u));
+            for (int u = 0; u < 2; ++u) {
+              const uint4 q = lds128(w ^ (32 * half + 16 * u));
               const uint32_t cc[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
               for (int b = 0; b < 4; ++b) {
                 const uint2 f = int8_to_f16(cc[b]);
-                v[u / 2][u % 2 * 8 + 2 * b] = f.x;
-                v[u / 2][u % 2 * 8 + 2 * b + 1] = f.y;
+                v[half][u * 8 + 2 * b] = f.x;
+                v[half][u * 8 + 2 * b + 1] = f.y;
               }
             }
-            finish();  // the step before, beside whose stores this one's codes were converted
-            if (!__all_sync(~0u, mbar_test(smem_u32(&s.used[step.i]), step.phase ^ 1))) {
-              ok = __all_sync(
-                  ~0u, mbar_wait<false>(smem_u32(&s.used[step.i]), step.phase ^ 1, ctl));
-              if (!ok) break;
-            }
-            tc_fence_after();
-#pragma unroll
-            for (int i = 0; i < kWUnits / 2; ++i)
-              tc_st16(to + step.i * P::kStepColumns + 16 * i, v[i]);
-            const uint32_t buffer = step.i / P::kPerBuffer * P::kBufferBytes,
-                           turn = step.i % P::kPerBuffer * (2 * P::kStepK);
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {  // 16 k of a token: 32 bytes of fp16
-              if (token[i] < n) {
-                const uint2 f0 = int8_to_f16(c[i].x), f1 = int8_to_f16(c[i].y),
-                            f2 = int8_to_f16(c[i].z), f3 = int8_to_f16(c[i].w);
-                const uint32_t o = (buffer + o0[i]) ^ turn;
-                sts128(o, make_uint4(f0.x, f0.y, f1.x, f1.y));
-                sts128(o ^ 16, make_uint4(f2.x, f2.y, f3.x, f3.y));
-              }
-            }
-            pending = step.i;
-            step.next();
-            step.next();
+          };
+          widen(0);
+          if (!P::kSplit) widen(1);
+          ok = warp_wait(smem_u32(&s.used[slot.i]), slot.phase ^ 1, ctl);
+          if (!ok) break;
+          tc_fence_after();
+          tc_st16(to + slot.i * kStepColumns, v[0]);
+          if (P::kSplit) widen(1);
+          tc_st16(to + slot.i * kStepColumns + 16, v[1]);
+          fence_async_smem();
+          tc_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&s.ready[slot.i]));
+            mbar_arrive(smem_u32(&s.xempty[xr.i]));
           }
+          xr.skip();
+          buffer.skip();
+          slot.skip();
+        } else {  // an odd last step: the other group's
+          ok = warp_wait(smem_u32(&s.wfull[wr.i]), wr.phase, ctl);
+          if (!ok) break;
         }
-        if (!ok) break;
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(smem_u32(&s.wempty[wr.i]));
-          mbar_arrive(smem_u32(&s.xempty[xr.i]));
-        }
+        if (lane == 0) mbar_arrive(smem_u32(&s.wempty[wr.i]));
         wr.next();
-        xr.next();
       }
-      finish();
       // an odd number of steps: each group took every other one up to the last, so the first one's
       // next is one too far and the second's one short
       if (step_count & 1) {
-        if (group == 0) step.back();
-        else step.next();
+        if (group == 0) {
+          xr.back();
+          buffer.back();
+          slot.back();
+        } else {
+          xr.next();
+          buffer.next();
+          slot.next();
+        }
       }
     }
   } else {
@@ -512,7 +531,7 @@ cudaError_t launch(const ExpertArgs& args, const void* a, const void* b, int num
   constexpr int channels = OP == kGated ? kBlock : 2 * kBlock;
   p.nt = (p.N + channels - 1) / channels;
   CUtensorMap mx, mw;
-  cudaError_t e = make_map(&mx, a, true, p.K, p.rows_max, 0, kBoxTokens);
+  cudaError_t e = make_map(&mx, a, true, p.K, p.rows_max, 0, P::kBox, kStepK);
   if (e == cudaSuccess)
     e = make_map(&mw, b, true, p.K, OP == kGated ? 2ll * p.F : p.N, p.E, kBlock);
   if (e != cudaSuccess) return e;
@@ -553,31 +572,36 @@ cudaError_t expert_int8_prepare() {
   return e;
 }
 
-// The plan with the least waves x time of a tile (single waves of gated, E = 1,
-// H = 4096, F = 2048, at 64 / 128 / 192 tokens a tile: 38 / 42 / 51 us, of which 9
-// are not the tile's). An expert's weights are converted once for each of its tiles, so a
-// tile should hold most experts' rows; where tiles are few, small ones spread
-// over more SMs. The host knows the rows and the experts, and takes the rows of
-// one to be within a standard deviation of a random choice of the experts. us of
-// Few / Some / Many, gated, H = 7168, F = 2048, random: E = 64, 32 rows 366 / 410 /
-// 472, 56 rows 438 / 443 / 494, 96 rows 757 / 457 / 535, 160 rows 1102 / 889 / 571,
-// 256 rows 1641 / 1056 / 1122; down, E = 1, 1024 rows 51 / 41 / 52; gated, E = 8,
-// H = 1024, F = 512, 512 rows 27 / 22 / 24. What it gives away: experts of
-// very unlike rows, and 256 rows each of E = 4, H = 2048, F = 1024 (24 / 27 / 31).
+// The plan with the least waves x time of a full tile (64 k of one at 64 / 128 /
+// 192 tokens: 0.43 / 0.47 / 0.51 us). An expert's weights are converted once for
+// each of its tiles, so a tile should hold most experts' rows; where tiles are
+// few, small ones spread over more SMs. The host knows the rows and the experts,
+// and takes the rows of one to be within two standard deviations of a random
+// choice of the experts. us of Few / Some / Many, gated, H = 7168, F = 2048,
+// random rows of E = 64: 56 on average 417 / 390 / 401, 96 719 / 408 / 433, 112
+// 720 / 475 / 444, 160 1060 / 791 / 486, 256 1567 / 957 / 911, 512 2947 / 1747 /
+// 1337, E = 256: 32 1359 / 1429 / 1494; down, E = 1, 1024 rows 50 / 41 / 46; gated, E = 8,
+// H = 1024, F = 512, 512 rows 27 / 21 / 23. What it gives away: experts of very
+// unlike rows.
 template <class P>
 static double plan_cost(ExpertOp op, const ExpertArgs& p, int num_sms, double tile) {
+  if (p.E > P::kExperts) return HUGE_VAL;
   const double experts = p.E < p.rows_max ? p.E : (double)p.rows_max, rows = p.rows_max / experts;
   const double spread = experts > 1 ? sqrt(rows) : 0.0;
   double tiles = 0.0;
-  for (int z = -1; z <= 1; ++z) tiles += ceil((rows + z * spread) / P::kTokens) / 3;
+  for (int z = -2; z <= 2; ++z) {
+    const double some = ceil((rows + z * spread) / P::kTokens);
+    tiles += (some > 1 ? some : 1) / 5;
+  }
   const int channels = op == kGated ? kBlock : 2 * kBlock;
   return ceil(tiles * experts * ((p.N + channels - 1) / channels) / num_sms) * tile;
 }
 
 cudaError_t launch_expert_int8(ExpertOp op, const ExpertArgs& p, const void* a, const void* b,
                                int num_sms, cudaStream_t st) {
-  const double few = plan_cost<Few>(op, p, num_sms, 29), some = plan_cost<Some>(op, p, num_sms, 33),
-               many = plan_cost<Many>(op, p, num_sms, 42);
+  const double few = plan_cost<Few>(op, p, num_sms, 0.43),
+               some = plan_cost<Some>(op, p, num_sms, 0.47),
+               many = plan_cost<Many>(op, p, num_sms, 0.51);
   if (few <= some && few <= many) return launch<Few>(op, p, a, b, num_sms, st);
   return some <= many ? launch<Some>(op, p, a, b, num_sms, st)
                       : launch<Many>(op, p, a, b, num_sms, st);

@@ -68,10 +68,10 @@ cudaError_t launch_expert_int8(ExpertOp op, const ExpertArgs& args, const void* 
 cudaError_t expert_gemm_prepare();
 cudaError_t expert_int8_prepare();
 
-// TMA map of a row-major tensor [planes][rows][cols] of bf16, or of bytes; copies of
-// box_rows rows x 128 bytes, 128-byte swizzle, zeros outside. planes = 0: two-dimensional.
+// TMA map of a row-major tensor [planes][rows][cols] of 16-bit values, or of bytes; copies of
+// box_rows rows x 128 (or 64) bytes, swizzled over as many, zeros outside. planes = 0: two-dimensional.
 cudaError_t make_map(CUtensorMap* m, const void* base, bool bytes, long long cols, long long rows,
-                     long long planes, int box_rows);
+                     long long planes, int box_rows, int row_bytes = 128);
 
 }  // namespace moe
 

@@ -27,19 +27,19 @@ def uneven(E, rows, seed=0):
 # op: form: (E, rows, H, F). The form follows from the rows a configuration can
 # have, the experts and how many tiles there are: tiles of 64 tokens where those
 # fill no more than a turn of the SMs, of 128 or 192 where the rows of an expert
-# mostly fit one or where fewer weight conversions pay for it, and widened codes
-# from 1280 rows an expert.
+# mostly fit one or where fewer weight conversions pay for it (up to 768
+# experts), and widened codes from 2048 rows an expert, gated from 4096.
 FORMS = {
     "gated": {"rows": (24, 60, 208, 272), "few": (6, 500, 336, 144), "few_turns": (256, 8000, 48, 400),
               "some": (32, 3200, 144, 656), "some_odd": (48, 4608, 208, 400),
               "many": (30, 5100, 208, 656), "many_short": (256, 40960, 16, 144),
-              "many_even": (40, 6000, 128, 528), "widened": (2, 3000, 2048, 720),
-              "widened_ragged": (3, 4101, 1040, 1040)},
+              "many_even": (40, 6000, 128, 528), "many_experts": (1000, 160000, 48, 144),
+              "widened": (2, 9000, 2048, 960), "widened_ragged": (3, 16001, 1040, 1040)},
     "down": {"rows": (24, 60, 272, 208), "few": (6, 500, 400, 336), "few_turns": (256, 8000, 400, 48),
              "some": (32, 3200, 1296, 80), "some_odd": (48, 4608, 784, 208),
              "many": (30, 5100, 1296, 208), "many_short": (256, 40960, 272, 16),
-             "many_even": (40, 6000, 1040, 128), "widened": (2, 3000, 2048, 720),
-             "widened_ragged": (3, 4101, 1040, 1040)},
+             "many_even": (40, 6000, 1040, 128), "many_experts": (1000, 160000, 272, 48),
+             "widened": (2, 9000, 2048, 960), "widened_ragged": (3, 16001, 1040, 1040)},
 }
 CASES = [(op, form) for op in FORMS for form in FORMS[op]]
 
@@ -102,7 +102,7 @@ def test_forms_agree(gpu, op):
     a, s = codes_of(rows, K, seed=1), torch.rand(rows, device="cuda", generator=gen(2)) / 30
     w, ws = weights(E, 2 * F if op == "gated" else H, K, 3)
     got = []
-    for room in (rows, 64 * E, 4096 * E):  # few, and widened last
+    for room in (rows, 64 * E, 4096 * E):  # single rows, tiles, widened
         ar = torch.zeros(room, K, dtype=torch.int8, device="cuda")
         sr, ar[:rows] = torch.zeros(room, device="cuda"), a
         sr[:rows] = s
