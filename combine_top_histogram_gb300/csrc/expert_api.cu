@@ -93,11 +93,16 @@ moe::ExpertArgs expert_args(moe_expert_t x, const int32_t* offset) {
 // at 64; down e4m3, with little to read per row of weights, 47 / 37 at 8,
 // 113 / 92 at 32, 154 / 166 at 64. E = 8, H = 4096, F = 1408, gated bf16:
 // 48 / 42 at 32, 49 / 61 at 128. Above 64 rows the gain is a few per cent and
-// one expert with all of them would cost many passes.
+// one expert with all of them would cost many passes. int8, whose tiles convert
+// what they read: gated 68 / 51 at 8 rows, 360 / 289 at 64, down 178 / 143 at 64;
+// E = 8, gated 41 / 29 at 24, 41 / 49 at 64, down 20.5 / 16.4 at 24; E = 1 (H =
+// 7168, F = 2048), gated 57 / 18 at 8 rows, 57 / 39 at 32, down 22.5 / 14.4 at
+// 16: there up to 32 rows, whatever E is.
 bool use_rows(moe_expert_t x, moe::ExpertOp op) {
   const long long E3 = 3ll * x->cfg.num_experts, rows = x->cfg.rows_max;
   const bool fp8_down = op == moe::kDown && x->cfg.dtype == MOE_FP8_E4M3;
-  return rows <= (E3 > 8 ? E3 : 8) && rows <= (fp8_down ? 48 : 64);
+  const int least = x->cfg.dtype == MOE_INT8 ? 32 : 8;
+  return rows <= (E3 > least ? E3 : least) && rows <= (fp8_down ? 48 : 64);
 }
 
 cudaError_t forward(moe_expert_t x, moe::ExpertOp op, const moe::ExpertArgs& a, const void* in,

@@ -9,36 +9,39 @@
 // below 2^24: the codes stay 8 bits wide in memory and on their way to the SM,
 // and become fp16 there.
 //
-// What that costs is the 128 bytes a cycle between an SM's warps, its shared
-// memory and its tensor memory: stores to tensor memory count like those to
-// shared memory, and so do the products' reads of B (measured by leaving parts
-// out: the times follow the sum of the bytes to 5 %). For 64 k and n tokens,
-// whose products with 256 channels take 4 n cycles, that is
-//   weights (A)  16 KB in, 16 out to be converted, 32 of fp16 to tensor memory
-//   tokens (B)   64 n in, 64 n out, 128 n of fp16 to shared memory, 256 n for the
-//                products of two blocks of 128 channels
-// so tokens are many: 192, with 384 columns of accumulators and 128 of fp16
-// weights the tensor memory is full. 160 KB then stand beside 768 cycles of
-// products, at 128 tokens 128 KB beside 512. The weights are the A operand
-// because the tensor cores take that one from tensor memory: as fp16 in shared
-// memory they would be read there again. CTA pairs that share a tile of tokens
-// save only half of the tokens' conversion (the products of both SMs read all
-// of B): 452 / 424 us at 128 tokens (gated, E = 16, 512 rows each, H = 7168,
-// F = 2048), for a hand-over between the CTAs at every step.
+// The conversions are what bounds a tile. The weights are the A operand, which the
+// tensor cores take from tensor memory: as fp16 in shared memory they would be
+// stored there and read again. A step of 64 k and n tokens, whose products with 256
+// channels take 4 n cycles, is
+//   weights (A)  16 KB of codes in and out of shared memory, 32 KB of fp16 to tensor memory
+//   tokens (B)   64 n bytes in and out, 128 n of fp16 to shared memory
+// beside the 256 n that the products read. The weights' part is the same for any n,
+// so n is as large as tensor memory allows: 192, where 384 columns of accumulators
+// and 128 of weights fill it. Their 768 cycles of products then take about 1100; the
+// vector pipes are 60-70 % busy by then, instruction issue 50-67 %, and the warps wait
+// on stores to tensor and shared memory in turn. Gated, E = 64, 512 rows each, H = 7168,
+// F = 2048: 1340 us, 1.44 PFLOP/s, 0.77 of the measured fp16 rate; products of many rows
+// an expert are widened in memory first (expert_codes.cu).
 //
 // One persistent CTA per SM. Its tile is two blocks of 128 channels (kGated:
 // gate and up of the same ones, kDown: neighbours) by up to 192 tokens:
-//   warps 0, 3   copy codes with TMA into rings of stages (128 k), of weights and of tokens
-//   warp 1       issues the products
-//   warps 4-19   convert: weights to tensor memory, tokens to shared memory, in
-//                four steps of 32 k; eight warps take every other one, so that one step's
+//   warps 0, 3   copy codes with TMA into rings of stages, of weights (128 k) and of
+//                tokens (64 k)
+//   warp 1       issues the products, a step of 64 k at a time
+//   warps 4-19   convert: weights to slots of tensor memory, tokens to buffers of fp16
+//                in shared memory; eight warps take every other step, so that one step's
 //                loads, conversions and stores run beside the next one's
-//   warps 20-27  read the accumulators, hand them back, and scale and store
-//                the results, the last third beside the next tile's products
+//   warps 20-27  read the accumulators 32 tokens at a time, scale and store them; with
+//                the last of them read the accumulators are handed back
+// Steps of 64 k and not 32 halve the waits and hand-overs of a tile (the case above:
+// 1590 us with 32).
 // Channels lie along the accumulator's lanes and tokens along its columns, so
 // a warp stores 32 neighbouring channels of one token at a time, and a short
 // segment shortens everything but the weights: its tokens are copied,
 // converted, multiplied and stored 32 at a time.
+// Of tiles with fewer tokens, those of 128 convert ahead into four slots, those of 64
+// into six: few rows an expert are bound by the weights' bytes (gated, E = 256, 32 rows
+// each: 1360 us, 0.83 of the copy rate).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
