@@ -48,15 +48,18 @@ __device__ __forceinline__ float2 quotient(float2 v, float s, float y) {
 }
 
 // |v / s| is at most 127 or so: adding 1.5 * 2^23 rounds it to an integer,
-// ties to even, whose low byte is the code.
+// ties to even, whose low byte is the code. Where s is one of the least numbers there
+// are, it may be rounded so far down that the quotient of the row's largest value passes
+// 127 (190 times the least, s = once that): codes end at 127.
 __device__ __forceinline__ uint32_t codes4(const float4 v, float s, float y) {
   float2 a, b;
   if (y != 0.0f) {
     a = quotient(make_float2(v.x, v.y), s, y);
     b = quotient(make_float2(v.z, v.w), s, y);
   } else {
-    a = make_float2(__fdiv_rn(v.x, s), __fdiv_rn(v.y, s));
-    b = make_float2(__fdiv_rn(v.z, s), __fdiv_rn(v.w, s));
+    const auto q = [&](float x) { return fminf(fmaxf(__fdiv_rn(x, s), -127.0f), 127.0f); };
+    a = make_float2(q(v.x), q(v.y));
+    b = make_float2(q(v.z), q(v.w));
   }
   const float2 big = make_float2(12582912.0f, 12582912.0f);
   a = __fadd2_rn(a, big);

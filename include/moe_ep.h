@@ -453,7 +453,11 @@ typedef struct moe_expert *moe_expert_t;
 
 /* Bytes of device workspace of a handle (0 if *cfg is invalid): control words
  * and, for training, the gradient of the pre-activations [rows_max, 2F], or,
- * for INT8, h before its quantisation (fp32 [rows_max, F]). */
+ * for INT8, h before its quantisation (fp32 [rows_max, F]) and, from 2048 rows
+ * an expert on, copies in fp16 of the rows of a product and of the weights (one
+ * of the w2's size, or from 4096 rows on of w13's). The kernels of a call follow
+ * rows_max and not the rows that it finds in expert_offset: a program that
+ * serves both large batches and single tokens has a handle for each. */
 size_t moe_expert_workspace_bytes(const moe_expert_config_t *cfg);
 
 /* Creates a handle over d_workspace (256-byte aligned, the caller's). As

@@ -30,12 +30,14 @@ def uneven(E, rows, seed=0):
 # mostly fit one or where fewer weight conversions pay for it (up to 768
 # experts), and widened codes from 2048 rows an expert, gated from 4096.
 FORMS = {
-    "gated": {"rows": (24, 60, 208, 272), "few": (6, 500, 336, 144), "few_turns": (256, 8000, 48, 400),
+    "gated": {"rows": (24, 60, 208, 272), "rows_one": (1, 29, 272, 400),
+              "few": (6, 500, 336, 144), "few_turns": (256, 8000, 48, 400),
               "some": (32, 3200, 144, 656), "some_odd": (48, 4608, 208, 400),
               "many": (30, 5100, 208, 656), "many_short": (256, 40960, 16, 144),
               "many_even": (40, 6000, 128, 528), "many_experts": (1000, 160000, 48, 144),
               "widened": (2, 9000, 2048, 960), "widened_ragged": (3, 16001, 1040, 1040)},
-    "down": {"rows": (24, 60, 272, 208), "few": (6, 500, 400, 336), "few_turns": (256, 8000, 400, 48),
+    "down": {"rows": (24, 60, 272, 208), "rows_one": (1, 29, 400, 272),
+             "few": (6, 500, 400, 336), "few_turns": (256, 8000, 400, 48),
              "some": (32, 3200, 1296, 80), "some_odd": (48, 4608, 784, 208),
              "many": (30, 5100, 1296, 208), "many_short": (256, 40960, 272, 16),
              "many_even": (40, 6000, 1040, 128), "many_experts": (1000, 160000, 272, 48),

@@ -217,6 +217,26 @@ def test_special_scales(gpu, rows):
     assert y[:2].isnan().all() and (y[2] == 0).all() and y[3:].isfinite().all()
 
 
+@pytest.mark.parametrize("room", [1, 300])
+def test_least_values_of_h(gpu, room):
+    """s = amax/127 of a few times the least fp32 value rounds to whole multiples of that: with
+    amax 190 of them s is one, and codes end at 127."""
+    H = F = 16
+    x = torch.zeros(room, H, dtype=torch.int8, device="cuda")
+    x[0, 0] = 1
+    w = torch.zeros(1, 2 * F, H, dtype=torch.int8, device="cuda")
+    w[0, :F, 0] = 95  # silu(95) = 95
+    w[0, F:F + 4, 0] = torch.tensor([2, -2, 1, -1], dtype=torch.int8, device="cuda")
+    ws = torch.ones(1, 2 * F, device="cuda")
+    ws.view(torch.int32)[0, F:] = 1  # 2^-149
+    h = B.moe_expert_create(B.make_expert_config(1, H, F, room, B.MOE_INT8))
+    codes = torch.zeros(room, F, dtype=torch.int8, device="cuda")
+    scale = torch.ones(room, device="cuda")
+    B.moe_expert_gated(h, offsets([1]), x, torch.ones(room, device="cuda"), w, ws, codes, scale)
+    assert scale.view(torch.int32)[0].item() == 1
+    assert codes[0].tolist() == [127, -127, 95, -95] + [0] * 12
+
+
 @pytest.mark.parametrize("rows", [6, 900])
 def test_segments_of_the_callers_own(gpu, rows):
     """Offsets past the rows, below zero and descending are held to ascending ones in range; rows
