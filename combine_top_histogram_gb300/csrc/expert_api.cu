@@ -96,12 +96,12 @@ moe::ExpertArgs expert_args(moe_expert_t x, const int32_t* offset) {
 // one expert with all of them would cost many passes. int8, whose tiles convert
 // what they read: gated 68 / 51 at 8 rows, 360 / 289 at 64, down 178 / 143 at 64;
 // E = 8, gated 41 / 29 at 24, 41 / 49 at 64, down 20.5 / 16.4 at 24; E = 1 (H =
-// 7168, F = 2048), gated 57 / 18 at 8 rows, 57 / 39 at 32, down 22.5 / 14.4 at
-// 16: there up to 32 rows, whatever E is.
+// 7168, F = 2048), gated 31 / 18 at 8 rows, 31 / 25 at 16, 31 / 39 at 32, down
+// 18.4 / 14.4 at 16: there up to 24 rows, whatever E is.
 bool use_rows(moe_expert_t x, moe::ExpertOp op) {
   const long long E3 = 3ll * x->cfg.num_experts, rows = x->cfg.rows_max;
   const bool fp8_down = op == moe::kDown && x->cfg.dtype == MOE_FP8_E4M3;
-  const int least = x->cfg.dtype == MOE_INT8 ? 32 : 8;
+  const int least = x->cfg.dtype == MOE_INT8 ? 24 : 8;
   return rows <= (E3 > least ? E3 : least) && rows <= (fp8_down ? 48 : 64);
 }
 

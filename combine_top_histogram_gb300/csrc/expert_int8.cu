@@ -85,6 +85,7 @@ struct Plan {
   static constexpr uint32_t kOperand = 2 * kAcc;  // first column of the fp16 weights
   static constexpr int kRingBytes =
       kWStages * kWBytes + kXStages * kXBytes + kBuffers * kBufferBytes;
+  static_assert(2 * kTokens * kBlock * 4 <= kRingBytes, "a split tile's sums");
   static_assert(kOperand + kSlots * kStepColumns <= 512, "tensor memory");
   static_assert(kWStages <= kMaxRing && kXStages <= kMaxRing && kSlots <= kMaxRing &&
                 kBuffers <= kMaxRing, "");
@@ -195,7 +196,10 @@ __device__ __forceinline__ void drain_ring(const uint64_t* full, uint32_t announ
     mbar_drain(smem_u32(&full[i % N]), (i / N) & 1);
 }
 
-template <int OP, class P>
+// SPLIT: a cluster takes one tile, each of its CTAs a share of the reduction axis. Their sums
+// meet in shared memory and are added up in the order of the ranks, a rank for every so many
+// tokens.
+template <int OP, class P, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     k_expert_int8(const __grid_constant__ CUtensorMap map_x,
                   const __grid_constant__ CUtensorMap map_w, const ExpertArgs p) {
@@ -236,8 +240,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = s.tmem;
   const WaitCtl ctl{&s.abort, 0u, p.wait_limit, p.status};
-  Walk<false, P::kTokens, Shared<P>> walk(p, s, kStageK, 0, blockIdx.x, gridDim.x);
-  const int step_count = (p.K + kStepK - 1) / kStepK;  // of a tile
+  const int ranks = SPLIT ? (int)cluster_size() : 1;
+  const int rank = SPLIT ? (int)blockIdx.x % ranks : 0;
+  Walk<false, P::kTokens, Shared<P>> walk(p, s, kStageK, 0, blockIdx.x / ranks, gridDim.x / ranks);
+  // of a tile, this CTA's stages of weights and steps
+  const int stages = (p.K + kStageK - 1) / kStageK, stage0 = stages * rank / ranks,
+            stage1 = stages * (rank + 1) / ranks;
+  const int step0 = 2 * stage0, step_count = min(2 * stage1, (p.K + kStepK - 1) / kStepK) - step0;
   constexpr int kChannels = OP == kGated ? kBlock : 2 * kBlock;  // a tile's output channels
 
   if (warp < kConvWarp0) {
@@ -249,10 +258,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       Tile t;
       while (ok && walk.next(t)) {
         // uniform, and known to be
-        const int blocks = __shfl_sync(~0u, t.kb, 0), e = __shfl_sync(~0u, t.e, 0);
+        const int e = __shfl_sync(~0u, t.e, 0);
         const int c0 = __shfl_sync(~0u, t.n0, 0) * kChannels;
         const int c1 = OP == kGated ? p.F + c0 : c0 + kBlock;
-        for (int kb = 0; kb < blocks; ++kb) {
+        for (int kb = stage0; kb < stage1; ++kb) {
           ok = __all_sync(~0u, mbar_wait<false>(smem_u32(&s.wempty[ring.i]), ring.phase ^ 1, ctl));
           if (!ok) break;
           const uint32_t bar = smem_u32(&s.wfull[ring.i]), w = smem_u32(wring) + ring.i * kWBytes;
@@ -262,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++announced;
           ring.next();
         }
+        if (SPLIT) break;
       }
       // copies in flight land before the CTA ends, also when a wait gave up
       drain_ring<P::kWStages>(s.wfull, announced);
@@ -280,10 +290,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t bar = smem_u32(&s.xfull[ring.i]), x = smem_u32(xring) + ring.i * P::kXBytes;
           mbar_expect_elected(bar, copies * P::kBox * kStepK);
           for (int i = 0; i < copies; ++i)
-            tma_load_2d<1>(x + i * P::kBox * kStepK, &map_x, bar, j * kStepK, row0 + i * P::kBox);
+            tma_load_2d<1>(x + i * P::kBox * kStepK, &map_x, bar, (step0 + j) * kStepK,
+                           row0 + i * P::kBox);
           ++announced;
           ring.next();
         }
+        if (SPLIT) break;
       }
       drain_ring<P::kXStages>(s.xfull, announced);
       __syncwarp();
@@ -316,12 +328,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           buffer.next();
         }
         if (ok) tc_commit<1>(smem_u32(&s.dfull));
+        if (SPLIT) break;
       }
       __syncwarp();
       tc_commit<1>(smem_u32(&s.drain));  // products in flight end before TMEM is freed
       mbar_drain(smem_u32(&s.drain), 0);
       __syncwarp();
     }
+    if (SPLIT) cluster_sync();  // the sums are written, as for the other warps
   } else if (warp < kEpiWarp0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     const int cw = warp - kConvWarp0, group = cw >> 3, block = (cw >> 2) & 1;
@@ -438,7 +452,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           slot.next();
         }
       }
+      if (SPLIT) break;
     }
+    if (SPLIT) cluster_sync();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     constexpr int kHalf = P::kTokens / 2;  // tokens of a warp
@@ -448,6 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t dphase = 0;
     bool ok = true;
     Tile t;
+    t.rows = 0;
     while (ok && walk.next(t)) {
       const int left = t.rows - half * kHalf;  // tokens of this warp: columns half * kHalf on
       const int c = t.n0 * kChannels + quarter * 32 + lane;  // channel, of the first block
@@ -463,6 +480,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       dphase ^= 1;
       tc_fence_after();
+      if (SPLIT) {
+        // all copies have landed and all products are done: the rings are free
+        float* sums = reinterpret_cast<float*>(wring) + quarter * 32 + lane;
+#pragma unroll 1
+        for (int i = half * kHalf; i < min(t.rows, (half + 1) * kHalf); i += 32) {
+          uint32_t a[32];
+#pragma unroll
+          for (int blk = 0; blk < 2; ++blk) {
+            tc_ld32(a, from - half * kHalf + blk * P::kAcc + i);
+            tc_wait_ld();
+            tc_loaded(a);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              sums[(blk * P::kTokens + i + j) * kBlock] = __uint_as_float(a[j]);
+          }
+        }
+        break;
+      }
       // Rounds of 32 tokens: all values, then all stores. A store before another token's value
       // would hold that one's scale, which the compiler cannot tell from what is stored, until the
       // first is done (gated, E = 19, 576 rows each, H = 1024, F = 2048: 142 / 135 us).
@@ -518,7 +553,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (rounds == 0 && lane == 0) mbar_arrive(smem_u32(&s.dempty));
       __syncwarp();  // read, before the next tile's are written
     }
+    if (SPLIT) {
+      cluster_sync();
+      if (ok && t.rows > 0) {
+        const uint32_t sums = smem_u32(wring) + (quarter * 32 + lane) * 4;
+        const int c = t.n0 * kChannels + quarter * 32 + lane;
+        const int c1 = OP == kGated ? c + p.F : c + kBlock;
+        const int channels = OP == kGated ? 2 * p.F : p.N;
+        const bool in0 = c < p.N, in1 = OP == kGated ? in0 : c1 < p.N;
+        const float* sw = p.sb + (long long)t.e * channels;
+        const float w0 = in0 ? __ldg(sw + c) : 0.0f, w1 = in1 ? __ldg(sw + c1) : 0.0f;
+        for (int i = rank * 2 + half; i < min(t.rows, P::kTokens); i += 2 * ranks) {
+          const float sr = __ldg(p.sa + t.row0 + i);
+          float f = 0.0f, g = 0.0f;
+#pragma unroll 4
+          for (int r = 0; r < ranks; ++r) {
+            const uint32_t at = cluster_addr(sums + i * kBlock * 4, r);
+            f += ld_cluster(at);
+            g += ld_cluster(at + P::kTokens * kBlock * 4);
+          }
+          f = f * sr * w0;
+          g = g * sr * w1;
+          const long long o = ((long long)t.row0 + i) * p.N + c;
+          if constexpr (OP == kGated) {
+            if (in0) static_cast<float*>(p.out)[o] = silu(f) * g;
+          } else {
+            if (in0) static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(f);
+            if (in1) static_cast<__nv_bfloat16*>(p.out)[o + kBlock] = __float2bfloat16_rn(g);
+          }
+        }
+      }
+    }
   }
+  if (SPLIT) cluster_sync();  // the sums have been read
   __syncwarp();
   tc_fence_before();
   __syncthreads();
@@ -528,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---- host side -------------------------------------------------------------
 template <int OP, class P>
-cudaError_t launch(const ExpertArgs& args, const void* a, const void* b, int num_sms,
+cudaError_t launch(const ExpertArgs& args, const void* a, const void* b, int split, int num_sms,
                    cudaStream_t st) {
   ExpertArgs p = args;
   constexpr int channels = OP == kGated ? kBlock : 2 * kBlock;
@@ -540,20 +607,37 @@ cudaError_t launch(const ExpertArgs& args, const void* a, const void* b, int num
   if (e != cudaSuccess) return e;
   const long long segments = p.E < p.rows_max ? p.E : p.rows_max;
   const long long tiles = (p.rows_max / P::kTokens + segments) * p.nt;
-  return launch_pdl(k_expert_int8<OP, P>, dim3((unsigned)(tiles < num_sms ? tiles : num_sms)),
-                    dim3(kThreads), smem_bytes<P>(), st, mx, mw, p);
+  if (split == 1)
+    return launch_pdl(k_expert_int8<OP, P, false>,
+                      dim3((unsigned)(tiles < num_sms ? tiles : num_sms)), dim3(kThreads),
+                      smem_bytes<P>(), st, mx, mw, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * split));  // a cluster for each tile that there can be
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_bytes<P>();
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k_expert_int8<OP, P, true>, mx, mw, p);
 }
 
 template <class P>
-cudaError_t launch(ExpertOp op, const ExpertArgs& p, const void* a, const void* b, int num_sms,
-                   cudaStream_t st) {
-  return op == kGated ? launch<kGated, P>(p, a, b, num_sms, st)
-                      : launch<kDown, P>(p, a, b, num_sms, st);
+cudaError_t launch(ExpertOp op, const ExpertArgs& p, const void* a, const void* b, int split,
+                   int num_sms, cudaStream_t st) {
+  return op == kGated ? launch<kGated, P>(p, a, b, split, num_sms, st)
+                      : launch<kDown, P>(p, a, b, split, num_sms, st);
 }
 
-template <int OP, class P>
+template <int OP, class P, bool SPLIT>
 cudaError_t prepare() {
-  const auto kernel = k_expert_int8<OP, P>;
+  const auto kernel = k_expert_int8<OP, P, SPLIT>;
   cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<P>());
   if (e != cudaSuccess) return e;
@@ -563,20 +647,26 @@ cudaError_t prepare() {
   return attr.numRegs >= kRegisters ? cudaSuccess : cudaErrorInvalidConfiguration;
 }
 
-}  // namespace
-
-cudaError_t expert_int8_prepare() {
-  cudaError_t e = prepare<kGated, Many>();
-  if (e == cudaSuccess) e = prepare<kDown, Many>();
-  if (e == cudaSuccess) e = prepare<kGated, Some>();
-  if (e == cudaSuccess) e = prepare<kDown, Some>();
-  if (e == cudaSuccess) e = prepare<kGated, Few>();
-  if (e == cudaSuccess) e = prepare<kDown, Few>();
+template <class P>
+cudaError_t prepare() {
+  cudaError_t e = prepare<kGated, P, false>();
+  if (e == cudaSuccess) e = prepare<kGated, P, true>();
+  if (e == cudaSuccess) e = prepare<kDown, P, false>();
+  if (e == cudaSuccess) e = prepare<kDown, P, true>();
   return e;
 }
 
-// The plan with the least waves x time of a full tile (64 k of one at 64 / 128 /
-// 192 tokens: 0.43 / 0.47 / 0.51 us). An expert's weights are converted once for
+}  // namespace
+
+cudaError_t expert_int8_prepare() {
+  cudaError_t e = prepare<Many>();
+  if (e == cudaSuccess) e = prepare<Some>();
+  if (e == cudaSuccess) e = prepare<Few>();
+  return e;
+}
+
+// The plan and the split with the least turns of the SMs x time of a full tile (a step of one at
+// 64 / 128 / 192 tokens: 0.43 / 0.47 / 0.51 us). An expert's weights are converted once for
 // each of its tiles, so a tile should hold most experts' rows; where tiles are
 // few, small ones spread over more SMs. The host knows the rows and the experts,
 // and takes the rows of one to be within two standard deviations of a random
@@ -586,9 +676,22 @@ cudaError_t expert_int8_prepare() {
 // 1337, E = 256: 32 1359 / 1429 / 1494; down, E = 1, 1024 rows 50 / 41 / 46; gated, E = 8,
 // H = 1024, F = 512, 512 rows 27 / 21 / 23. What it gives away: experts of very
 // unlike rows.
+// Where tiles leave SMs without work, clusters of 2, 4 or 8 CTAs share the reduction of one;
+// meeting costs them up to 10 us more. us of one CTA / clusters of 2 / 4 / 8, the caches
+// empty: down, E = 1, 64 rows, H = 4096, F = 14336 (16 tiles) 106 / 63 / 39 / 49, H = 7168,
+// F = 2048 (28) 22.6 / 22.5 / 18.4 / 32.8; gated, E = 7, 240 rows, H = 5488, F = 256 (14) 49 /
+// 37 / 27 / 25, E = 8, 200 rows, H = 4096, F = 1408 (88) 43 / 57 / 57 / 84, E = 4, 400 rows,
+// H = 1024, F = 512 (28) 18.4 / 22.5 / 18.4 / 32.8. Clusters of 8 have room on 14 x 8 SMs
+// only, of 4 on 36 x 4: parts of the GPU have other numbers of SMs.
+struct Choice {
+  double us;
+  int split;
+};
+
 template <class P>
-static double plan_cost(ExpertOp op, const ExpertArgs& p, int num_sms, double tile) {
-  if (p.E > P::kExperts) return HUGE_VAL;
+static Choice choose(ExpertOp op, const ExpertArgs& p, int num_sms, double step) {
+  Choice best{HUGE_VAL, 1};
+  if (p.E > P::kExperts) return best;
   const double experts = p.E < p.rows_max ? p.E : (double)p.rows_max, rows = p.rows_max / experts;
   const double spread = experts > 1 ? sqrt(rows) : 0.0;
   double tiles = 0.0;
@@ -597,17 +700,26 @@ static double plan_cost(ExpertOp op, const ExpertArgs& p, int num_sms, double ti
     tiles += (some > 1 ? some : 1) / 5;
   }
   const int channels = op == kGated ? kBlock : 2 * kBlock;
-  return ceil(tiles * experts * ((p.N + channels - 1) / channels) / num_sms) * tile;
+  tiles *= experts * ((p.N + channels - 1) / channels);
+  const int stages = (p.K + kStageK - 1) / kStageK, steps = (p.K + kStepK - 1) / kStepK;
+  for (int split = 1; split <= 8 && (split == 1 || stages >= 2 * split); split *= 2) {
+    const int room = split == 8 ? num_sms * 3 / 4 : split == 4 ? num_sms * 19 / 20 : num_sms;
+    if (split > 1 && tiles * split > room) break;
+    const double us = split == 1 ? ceil(tiles / num_sms) * steps * step
+                                 : 2 * ((stages + split - 1) / split) * step + 10.0;
+    if (us < best.us) best = {us, split};
+  }
+  return best;
 }
 
 cudaError_t launch_expert_int8(ExpertOp op, const ExpertArgs& p, const void* a, const void* b,
                                int num_sms, cudaStream_t st) {
-  const double few = plan_cost<Few>(op, p, num_sms, 0.43),
-               some = plan_cost<Some>(op, p, num_sms, 0.47),
-               many = plan_cost<Many>(op, p, num_sms, 0.51);
-  if (few <= some && few <= many) return launch<Few>(op, p, a, b, num_sms, st);
-  return some <= many ? launch<Some>(op, p, a, b, num_sms, st)
-                      : launch<Many>(op, p, a, b, num_sms, st);
+  const Choice few = choose<Few>(op, p, num_sms, 0.43), some = choose<Some>(op, p, num_sms, 0.47),
+               many = choose<Many>(op, p, num_sms, 0.51);
+  if (few.us <= some.us && few.us <= many.us)
+    return launch<Few>(op, p, a, b, few.split, num_sms, st);
+  return some.us <= many.us ? launch<Some>(op, p, a, b, some.split, num_sms, st)
+                            : launch<Many>(op, p, a, b, many.split, num_sms, st);
 }
 
 }  // namespace moe

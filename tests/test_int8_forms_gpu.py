@@ -28,18 +28,23 @@ def uneven(E, rows, seed=0):
 # have, the experts and how many tiles there are: tiles of 64 tokens where those
 # fill no more than a turn of the SMs, of 128 or 192 where the rows of an expert
 # mostly fit one or where fewer weight conversions pay for it (up to 768
-# experts), and widened codes from 2048 rows an expert, gated from 4096.
+# experts), clusters of 2, 4 or 8 CTAs for a tile where those are few and the
+# reduction is long, and widened codes from 2048 rows an expert, gated from 4096.
 FORMS = {
-    "gated": {"rows": (24, 60, 208, 272), "rows_one": (1, 29, 272, 400),
+    "gated": {"rows": (24, 60, 208, 272), "rows_one": (1, 21, 272, 400),
               "few": (6, 500, 336, 144), "few_turns": (256, 8000, 48, 400),
               "some": (32, 3200, 144, 656), "some_odd": (48, 4608, 208, 400),
               "many": (30, 5100, 208, 656), "many_short": (256, 40960, 16, 144),
+              "few_split8": (1, 40, 2064, 144), "few_split4": (6, 200, 4112, 400),
+              "some_split2": (10, 600, 4112, 656), "many_split8": (3, 450, 4112, 400),
               "many_even": (40, 6000, 128, 528), "many_experts": (1000, 160000, 48, 144),
               "widened": (2, 9000, 2048, 960), "widened_ragged": (3, 16001, 1040, 1040)},
-    "down": {"rows": (24, 60, 272, 208), "rows_one": (1, 29, 400, 272),
+    "down": {"rows": (24, 60, 272, 208), "rows_one": (1, 21, 400, 272),
              "few": (6, 500, 400, 336), "few_turns": (256, 8000, 400, 48),
              "some": (32, 3200, 1296, 80), "some_odd": (48, 4608, 784, 208),
              "many": (30, 5100, 1296, 208), "many_short": (256, 40960, 272, 16),
+             "few_split8": (1, 40, 400, 2064), "few_split4": (6, 200, 1008, 4112),
+             "some_split2": (10, 600, 1424, 4112), "many_split8": (3, 450, 912, 4112),
              "many_even": (40, 6000, 1040, 128), "many_experts": (1000, 160000, 272, 48),
              "widened": (2, 9000, 2048, 960), "widened_ragged": (3, 16001, 1040, 1040)},
 }
@@ -123,8 +128,8 @@ def test_forms_agree(gpu, op):
 
 
 @pytest.mark.parametrize("cycles", [0, 500, 5000, 40000])
-@pytest.mark.parametrize("op, form", [c for c in CASES if c[1] in ("few_turns", "some", "many",
-                                                                   "widened")])
+@pytest.mark.parametrize("op, form", [c for c in CASES if c[1] in (
+    "few_turns", "some", "many", "few_split8", "some_split2", "many_split8", "widened")])
 def test_waits_that_run_out(gpu, op, form, cycles):
     """Whatever wait runs out first, every kernel leaves and says so, and the next call with the
     usual limit is right."""
@@ -140,8 +145,8 @@ def test_waits_that_run_out(gpu, op, form, cycles):
     job.check()
 
 
-@pytest.mark.parametrize("op, form", [c for c in CASES if c[1] in ("rows", "few", "some", "many",
-                                                                   "widened")])
+@pytest.mark.parametrize("op, form", [c for c in CASES if c[1] in (
+    "rows", "few", "some", "many", "few_split4", "many_split8", "widened")])
 def test_in_a_graph(gpu, op, form):
     job = Job(op, *FORMS[op][form])
     job.call()
@@ -153,6 +158,23 @@ def test_in_a_graph(gpu, op, form):
         job.fill(seed)
         g.replay()
         job.check()
+
+
+@pytest.mark.parametrize("form", ["few_split8", "many_split8"])
+@pytest.mark.parametrize("op", ["gated", "down"])
+def test_clusters_without_a_tile(gpu, op, form):
+    """No rows at all, and then rows of one expert only."""
+    job = Job(op, *FORMS[op][form])
+    full, E = job.n, len(job.counts)
+    for job.counts in ([0] * E, [0] * (E - 1) + [1]):
+        job.n = sum(job.counts)
+        job.off.copy_(offsets(job.counts))
+        job.call()
+        assert B.moe_expert_read_status(job.h) == 0
+        if job.n:
+            job.check()
+        else:
+            assert untouched(job.out[:full]) and (op == "down" or untouched(job.outs[:full]))
 
 
 @pytest.mark.parametrize("F", [2064, 4112])
