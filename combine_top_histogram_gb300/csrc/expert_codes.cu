@@ -4,9 +4,9 @@
 // row of the segments s = amax/127 over its F values and codes = RNE(h / s). The
 // scale needs the whole row, whose columns many CTAs computed, so h comes
 // through memory in fp32 (a rounded h would move codes that lie near a tie). One
-// CTA takes a row at a time, holds it in registers (up to 16 values a thread)
-// while its largest magnitude is found, and writes the codes: every value is
-// read once.
+// CTA, or of short rows a warp, takes a row at a time, holds it in registers (up to
+// 16 values a thread) while its largest magnitude is found, and writes the codes:
+// every value of up to 2048 (of a warp's, 512) is read once.
 //
 // k_widen: codes as fp16, for the products of many rows an expert. It moves three
 // bytes a code at HBM's rate; the products that read them then run at the fp16
@@ -128,27 +128,31 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+// WARPS of a row: all of the CTA's, or one, which needs no barrier (short rows).
+template <int WARPS>
 __global__ void __launch_bounds__(kThreads)
     k_expert_quantise(const ExpertArgs p, const float* __restrict__ h, int8_t* __restrict__ codes,
                       float* __restrict__ scale) {
+  constexpr int kRow = WARPS * 32, kRows = kThreads / kRow;
   __shared__ uint32_t buf[3][kWarps];
-  const int tid = threadIdx.x, n = p.F >> 2;
+  const int tid = threadIdx.x % kRow, n = p.F >> 2;
   pdl_wait();
   int first, end, par = 0;
   segment_rows(p, buf[2], first, end);
-  for (long long r = (long long)first + blockIdx.x; r < end; r += gridDim.x, par ^= 1) {
+  for (long long r = (long long)first + blockIdx.x * kRows + threadIdx.x / kRow; r < end;
+       r += (long long)gridDim.x * kRows, par ^= 1) {
     const float4* row = reinterpret_cast<const float4*>(h + r * p.F);
     float4 v[kHeld];
     uint32_t m = 0u;
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
-      const int c = tid + i * kThreads;
+      const int c = tid + i * kRow;
       v[i] = c < n ? __ldcs(row + c) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) m = max4(m, v[i]);
-    for (int c = tid + kHeld * kThreads; c < n; c += kThreads) m = max4(m, __ldg(row + c));
-    m = cta_max(m, buf[par]);
+    for (int c = tid + kHeld * kRow; c < n; c += kRow) m = max4(m, __ldg(row + c));
+    m = WARPS == 1 ? __reduce_max_sync(~0u, m) : cta_max(m, buf[par]);
     const bool finite = m < 0x7f800000u;
     const float s = finite ? __fdiv_rn(__uint_as_float(m), 127.0f) : __uint_as_float(m);
     const bool any = finite && s > 0.0f;
@@ -157,10 +161,10 @@ __global__ void __launch_bounds__(kThreads)
     if (tid == 0) scale[r] = s;
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
-      const int c = tid + i * kThreads;
+      const int c = tid + i * kRow;
       if (c < n) out[c] = any ? codes4(v[i], s, y) : 0u;
     }
-    for (int c = tid + kHeld * kThreads; c < n; c += kThreads)
+    for (int c = tid + kHeld * kRow; c < n; c += kRow)
       out[c] = any ? codes4(__ldg(row + c), s, y) : 0u;
   }
 }
@@ -185,8 +189,17 @@ cudaError_t launch_widen_weights(const ExpertArgs& p, long long weight_rows, con
 cudaError_t launch_expert_quantise(const ExpertArgs& p, const float* h, int8_t* codes,
                                    float* scale, int num_sms, cudaStream_t st) {
   const long long most = 16ll * num_sms;
-  const int grid = (int)(p.rows_max < most ? p.rows_max : most);
-  return launch_pdl(k_expert_quantise, dim3(grid), dim3(kThreads), 0, st, p, h, codes, scale);
+  // one warp / four (us, with the products; H = 256): E = 11, 3507 rows each, F = 464 58.5 / 77.7
+  // (H = 368), E = 8, 4000 rows, F = 640 52.8 / 67.4, F = 896 73.7 / 81.6, 1000 rows, F = 1008
+  // 29.9 / 31.2; longer rows are read twice by one warp, and the same by both
+  if (p.F <= 1024) {
+    const long long ctas = (p.rows_max + kWarps - 1) / kWarps;
+    return launch_pdl(k_expert_quantise<1>, dim3((unsigned)(ctas < most ? ctas : most)),
+                      dim3(kThreads), 0, st, p, h, codes, scale);
+  }
+  const unsigned ctas = (unsigned)(p.rows_max < most ? p.rows_max : most);
+  return launch_pdl(k_expert_quantise<kWarps>, dim3(ctas), dim3(kThreads), 0, st, p, h, codes,
+                    scale);
 }
 
 }  // namespace moe
