@@ -99,17 +99,13 @@ def test_form(gpu, op, form):
     job.check()
 
 
-@pytest.mark.parametrize("op", ["gated", "down"])
-def test_forms_agree(gpu, op):
-    """Sums of codes are exact here, so the forms give the same results, bit for bit: of the
-    same rows, with room for so many more that other tiles are taken."""
-    E, rows, H, F = 8, 60, 512, 1296
-    K, N = (H, F) if op == "gated" else (F, H)
+def agree(op, E, rows, K, N, rooms):
+    H, F = (K, N) if op == "gated" else (N, K)
     counts = uneven(E, rows)
     a, s = codes_of(rows, K, seed=1), torch.rand(rows, device="cuda", generator=gen(2)) / 30
     w, ws = weights(E, 2 * F if op == "gated" else H, K, 3)
     got = []
-    for room in (rows, 64 * E, 4096 * E):  # single rows, tiles, widened
+    for room in rooms:
         ar = torch.zeros(room, K, dtype=torch.int8, device="cuda")
         sr, ar[:rows] = torch.zeros(room, device="cuda"), a
         sr[:rows] = s
@@ -125,6 +121,20 @@ def test_forms_agree(gpu, op):
             got.append((o[:rows].clone(),))
     for other in got[1:]:
         assert all(torch.equal(x, y) for x, y in zip(got[0], other))
+
+
+@pytest.mark.parametrize("op", ["gated", "down"])
+def test_forms_agree(gpu, op):
+    """Sums of codes are exact here, so the forms give the same results, bit for bit: of the
+    same rows, with room for so many more that other tiles are taken."""
+    K, N = (512, 1296) if op == "gated" else (1296, 512)
+    agree(op, 8, 60, K, N, (60, 64 * 8, 4096 * 8))  # single rows, tiles, widened
+
+
+@pytest.mark.parametrize("op", ["gated", "down"])
+def test_clusters_agree(gpu, op):
+    """As above, of single rows, of clusters of 8 that share a tile, and of tiles without clusters."""
+    agree(op, 2, 20, 2064, 144, (20, 80, 20000))
 
 
 @pytest.mark.parametrize("cycles", [0, 500, 5000, 40000])
