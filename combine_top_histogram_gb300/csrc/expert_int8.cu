@@ -23,8 +23,9 @@
 // F = 2048: 1340 us, 1.44 PFLOP/s, 0.77 of the measured fp16 rate; products of many rows
 // an expert are widened in memory first (expert_codes.cu).
 //
-// One persistent CTA per SM. Its tile is two blocks of 128 channels (kGated:
-// gate and up of the same ones, kDown: neighbours) by up to 192 tokens:
+// One persistent CTA per SM, or, where tiles are few and the reduction is long, a
+// cluster of CTAs for each tile (SPLIT, below). A tile is two blocks of 128 channels
+// (kGated: gate and up of the same ones, kDown: neighbours) by up to 192 tokens:
 //   warps 0, 3   copy codes with TMA into rings of stages, of weights (128 k) and of
 //                tokens (64 k)
 //   warp 1       issues the products, a step of 64 k at a time
