@@ -142,7 +142,9 @@ int moe_expert_create(const moe_expert_config_t* cfg, void* d_workspace, size_t 
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-      moe::expert_gemm_prepare() != cudaSuccess || moe::expert_int8_prepare() != cudaSuccess ||
+      moe::expert_gemm_prepare(static_cast<moe::ExpertType>(cfg->dtype), cfg->train) !=
+          cudaSuccess ||
+      (cfg->dtype == MOE_INT8 && moe::expert_int8_prepare() != cudaSuccess) ||
       cudaMemset(d_workspace, 0, kAlign) != cudaSuccess ||
       cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess)  // before work on any stream
     return MOE_ERR_CUDA;

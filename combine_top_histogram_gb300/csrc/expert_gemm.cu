@@ -1172,18 +1172,23 @@ cudaError_t prepare() {
 
 }  // namespace
 
-cudaError_t expert_gemm_prepare() {
-  cudaError_t e = prepare<kGated, false>();
-  if (e == cudaSuccess) e = prepare<kGated, true>();
-  if (e == cudaSuccess) e = prepare<kDown, false>();
-  if (e == cudaSuccess) e = prepare<kDown, true>();
-  if (e == cudaSuccess) e = prepare<kDgate, false>();
-  if (e == cudaSuccess) e = prepare<kDx, false>();
-  if (e == cudaSuccess) e = prepare<kDw, false>();
-  // only of many rows an expert
-  if (e == cudaSuccess) e = prepare<kGatedCodes, false, 2, 256>();
-  if (e == cudaSuccess) e = prepare<kDownCodes, false, 2, 256>();
-  return e;
+cudaError_t expert_gemm_prepare(ExpertType type, bool train) {
+  cudaError_t e;
+  switch (type) {
+    case kE4m3:
+      e = prepare<kGated, true>();
+      return e != cudaSuccess ? e : prepare<kDown, true>();
+    case kInt8:  // only of many rows an expert
+      e = prepare<kGatedCodes, false, 2, 256>();
+      return e != cudaSuccess ? e : prepare<kDownCodes, false, 2, 256>();
+    default:
+      e = prepare<kGated, false>();
+      if (e == cudaSuccess) e = prepare<kDown, false>();
+      if (e == cudaSuccess && train) e = prepare<kDgate, false>();
+      if (e == cudaSuccess && train) e = prepare<kDx, false>();
+      if (e == cudaSuccess && train) e = prepare<kDw, false>();
+      return e;
+  }
 }
 
 cudaError_t launch_expert_gemm(ExpertOp op, bool fp8, const ExpertArgs& args, const void* a,

@@ -64,8 +64,9 @@ cudaError_t launch_expert_quantise(const ExpertArgs& args, const float* h, int8_
 // INT8: kGated (to fp32 h) or kDown on the tensor cores (expert_int8.cu).
 cudaError_t launch_expert_int8(ExpertOp op, const ExpertArgs& args, const void* a, const void* b,
                                int num_sms, cudaStream_t st);
-// Opt the kernels in to their shared memory and check their register split.
-cudaError_t expert_gemm_prepare();
+// Opt the kernels that a type's handles launch (the first: with those of backward, or
+// without) in to their shared memory and check their register split.
+cudaError_t expert_gemm_prepare(ExpertType type, bool train);
 cudaError_t expert_int8_prepare();
 
 // TMA map of a row-major tensor [planes][rows][cols] of 16-bit values, or of bytes; copies of
