@@ -22,6 +22,9 @@ MOE_STATUS_BAD_EXPERT_ID = 0x1
 MOE_STATUS_TIMEOUT = 0x2
 MOE_STATUS_SLOT_OVERFLOW = 0x4
 MOE_STATUS_BOUNDS = 0x8
+MOE_FORM_ROWS = 0
+MOE_FORM_TILES = 1
+MOE_FORM_WIDENED = 2
 MOE_MAX_EXPERTS = 1024
 MOE_MAX_TOPK = 32
 MOE_MAX_RANKS = 1024
@@ -40,6 +43,7 @@ EXPORTED_SYMBOLS = (
     "moe_fixed_slot_rows", "moe_debug_bounds", "moe_expert_workspace_bytes", "moe_expert_create",
     "moe_expert_destroy", "moe_expert_gated", "moe_expert_down", "moe_expert_backward",
     "moe_expert_set_wait_limit", "moe_expert_read_status", "moe_combine_backward",
+    "moe_expert_form",
 )
 
 
@@ -72,6 +76,11 @@ class moe_expert_config_t(ctypes.Structure):
     _fields_ = [("num_experts", ctypes.c_int32), ("hidden", ctypes.c_int32),
                 ("inter", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("rows_max", ctypes.c_int64), ("train", ctypes.c_int32)]
+
+
+class moe_expert_form_t(ctypes.Structure):
+    _fields_ = [("kernels", ctypes.c_int32), ("tokens", ctypes.c_int32),
+                ("split", ctypes.c_int32)]
 
 
 _lib = None
@@ -164,6 +173,9 @@ def load_library():
         xcfgp = ctypes.POINTER(moe_expert_config_t)
         lib.moe_expert_workspace_bytes.restype = sz
         lib.moe_expert_workspace_bytes.argtypes = [xcfgp]
+        lib.moe_expert_form.restype = i32
+        lib.moe_expert_form.argtypes = [xcfgp, ctypes.c_int32, ctypes.c_int32,
+                                        ctypes.POINTER(moe_expert_form_t)]
         lib.moe_expert_create.restype = i32
         lib.moe_expert_create.argtypes = [xcfgp, vp, sz, ctypes.POINTER(vp)]
         lib.moe_expert_destroy.restype = i32
@@ -460,6 +472,14 @@ def make_expert_config(E: int, H: int, F: int, rows_max: int, dtype: int = MOE_B
 
 def moe_expert_workspace_bytes(cfg: moe_expert_config_t) -> int:
     return int(load_library().moe_expert_workspace_bytes(ctypes.byref(cfg)))
+
+
+def moe_expert_form(cfg: moe_expert_config_t, down: bool, num_sms: int) -> tuple:
+    """(kernels, tokens, split) of a handle's gated or down product (see the header)."""
+    out = moe_expert_form_t()
+    _check("moe_expert_form", load_library().moe_expert_form(
+        ctypes.byref(cfg), int(down), num_sms, ctypes.byref(out)))
+    return out.kernels, out.tokens, out.split
 
 
 class ExpertHandle:

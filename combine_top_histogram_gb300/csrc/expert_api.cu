@@ -98,19 +98,26 @@ moe::ExpertArgs expert_args(moe_expert_t x, const int32_t* offset) {
 // E = 8, gated 41 / 29 at 24, 41 / 49 at 64, down 20.5 / 16.4 at 24; E = 1 (H =
 // 7168, F = 2048), gated 31 / 18 at 8 rows, 31 / 25 at 16, 31 / 39 at 32, down
 // 18.4 / 14.4 at 16: there up to 24 rows, whatever E is.
-bool use_rows(moe_expert_t x, moe::ExpertOp op) {
-  const long long E3 = 3ll * x->cfg.num_experts, rows = x->cfg.rows_max;
-  const bool fp8_down = op == moe::kDown && x->cfg.dtype == MOE_FP8_E4M3;
-  const int least = x->cfg.dtype == MOE_INT8 ? 24 : 8;
+bool use_rows(const moe_expert_config_t* c, moe::ExpertOp op) {
+  const long long E3 = 3ll * c->num_experts, rows = c->rows_max;
+  const bool fp8_down = op == moe::kDown && c->dtype == MOE_FP8_E4M3;
+  const int least = c->dtype == MOE_INT8 ? 24 : 8;
   return rows <= (E3 > least ? E3 : least) && rows <= (fp8_down ? 48 : 64);
+}
+
+// The kernels of a product (MOE_FORM_*).
+int form(const moe_expert_config_t* c, moe::ExpertOp op) {
+  return use_rows(c, op) ? MOE_FORM_ROWS : widens(c, op) ? MOE_FORM_WIDENED : MOE_FORM_TILES;
 }
 
 cudaError_t forward(moe_expert_t x, moe::ExpertOp op, const moe::ExpertArgs& a, const void* in,
                     const void* w, void* stream) {
   const moe::ExpertType type = static_cast<moe::ExpertType>(x->cfg.dtype);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (use_rows(x, op)) return moe::launch_expert_rows(op, type, a, in, w, x->num_sms, st);
-  if (type == moe::kInt8 && widens(&x->cfg, op)) {
+  const int kernels = form(&x->cfg, op);
+  if (kernels == MOE_FORM_ROWS)
+    return moe::launch_expert_rows(op, type, a, in, w, x->num_sms, st);
+  if (kernels == MOE_FORM_WIDENED) {
     const bool gated = op == moe::kGated;
     cudaError_t e = moe::launch_widen_rows(a, in, x->x16, x->num_sms, st);
     if (e == cudaSuccess)
@@ -129,6 +136,25 @@ extern "C" {
 
 size_t moe_expert_workspace_bytes(const moe_expert_config_t* cfg) {
   return validate(cfg) == MOE_OK ? workspace_bytes(cfg) : 0;
+}
+
+int moe_expert_form(const moe_expert_config_t* cfg, int32_t down, int32_t num_sms,
+                    moe_expert_form_t* out) {
+  if (!out || (down != 0 && down != 1) || num_sms < 1) return MOE_ERR_INVALID_ARG;
+  const int rc = validate(cfg);
+  if (rc != MOE_OK) return rc;
+  const moe::ExpertOp op = down ? moe::kDown : moe::kGated;
+  *out = {form(cfg, op), 0, 0};
+  if (cfg->dtype != MOE_INT8 || out->kernels != MOE_FORM_TILES) return MOE_OK;
+  moe::ExpertArgs a{};
+  a.E = cfg->num_experts;
+  a.rows_max = cfg->rows_max;
+  a.N = down ? cfg->hidden : cfg->inter;
+  a.K = down ? cfg->inter : cfg->hidden;
+  const moe::Int8Plan plan = moe::expert_int8_plan(op, a, num_sms);
+  out->tokens = plan.tokens;
+  out->split = plan.split;
+  return MOE_OK;
 }
 
 int moe_expert_create(const moe_expert_config_t* cfg, void* d_workspace, size_t bytes,

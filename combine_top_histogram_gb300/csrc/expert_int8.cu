@@ -713,14 +713,22 @@ static Choice choose(ExpertOp op, const ExpertArgs& p, int num_sms, double step)
   return best;
 }
 
-cudaError_t launch_expert_int8(ExpertOp op, const ExpertArgs& p, const void* a, const void* b,
-                               int num_sms, cudaStream_t st) {
+Int8Plan expert_int8_plan(ExpertOp op, const ExpertArgs& p, int num_sms) {
   const Choice few = choose<Few>(op, p, num_sms, 0.43), some = choose<Some>(op, p, num_sms, 0.47),
                many = choose<Many>(op, p, num_sms, 0.51);
-  if (few.us <= some.us && few.us <= many.us)
-    return launch<Few>(op, p, a, b, few.split, num_sms, st);
-  return some.us <= many.us ? launch<Some>(op, p, a, b, some.split, num_sms, st)
-                            : launch<Many>(op, p, a, b, many.split, num_sms, st);
+  if (few.us <= some.us && few.us <= many.us) return {Few::kTokens, few.split};
+  return some.us <= many.us ? Int8Plan{Some::kTokens, some.split}
+                            : Int8Plan{Many::kTokens, many.split};
+}
+
+cudaError_t launch_expert_int8(ExpertOp op, const ExpertArgs& p, const void* a, const void* b,
+                               int num_sms, cudaStream_t st) {
+  const Int8Plan plan = expert_int8_plan(op, p, num_sms);
+  switch (plan.tokens) {
+    case Few::kTokens: return launch<Few>(op, p, a, b, plan.split, num_sms, st);
+    case Some::kTokens: return launch<Some>(op, p, a, b, plan.split, num_sms, st);
+    default: return launch<Many>(op, p, a, b, plan.split, num_sms, st);
+  }
 }
 
 }  // namespace moe

@@ -61,6 +61,11 @@ cudaError_t launch_widen_weights(const ExpertArgs& args, long long weight_rows, 
 // INT8: codes [rows, F] and scales [rows] of the segments' rows of h (expert_codes.cu).
 cudaError_t launch_expert_quantise(const ExpertArgs& args, const float* h, int8_t* codes,
                                    float* scale, int num_sms, cudaStream_t st);
+// INT8: tokens of a tile and CTAs that share one, of kGated (p.N = F) or kDown.
+struct Int8Plan {
+  int tokens, split;
+};
+Int8Plan expert_int8_plan(ExpertOp op, const ExpertArgs& p, int num_sms);
 // INT8: kGated (to fp32 h) or kDown on the tensor cores (expert_int8.cu).
 cudaError_t launch_expert_int8(ExpertOp op, const ExpertArgs& args, const void* a, const void* b,
                                int num_sms, cudaStream_t st);

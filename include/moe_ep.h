@@ -460,6 +460,21 @@ typedef struct moe_expert *moe_expert_t;
  * serves both large batches and single tokens has a handle for each. */
 size_t moe_expert_workspace_bytes(const moe_expert_config_t *cfg);
 
+/* Housekeeping: the kernels that a handle of this configuration runs for
+ * moe_expert_gated (down = 0) or moe_expert_down (1) on a GPU of num_sms SMs.
+ * Host only: for tests, and for a program that chooses its handles' rows_max.
+ * Errors: INVALID_ARG, UNSUPPORTED. */
+#define MOE_FORM_ROWS 0    /* few rows: each expert's weights streamed once for every eight */
+#define MOE_FORM_TILES 1   /* tiles of rows on the tensor cores */
+#define MOE_FORM_WIDENED 2 /* INT8: the same, of codes widened to fp16 in memory */
+typedef struct {
+    int32_t kernels;     /* MOE_FORM_* */
+    int32_t tokens;      /* INT8, MOE_FORM_TILES: rows of a tile, 64, 128 or 192; else 0 */
+    int32_t split;       /* INT8, MOE_FORM_TILES: CTAs that share a tile's reduction; else 0 */
+} moe_expert_form_t;
+int moe_expert_form(const moe_expert_config_t *cfg, int32_t down, int32_t num_sms,
+                    moe_expert_form_t *out);
+
 /* Creates a handle over d_workspace (256-byte aligned, the caller's). As
  * moe_handle_create: a synchronous cudaMemset of the control words on the
  * current device; outside stream capture. Errors: INVALID_ARG, UNSUPPORTED,
