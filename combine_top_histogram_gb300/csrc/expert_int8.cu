@@ -320,8 +320,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t b = smem_desc(smem_u32(buffers) + buffer.i * P::kBufferBytes, 16, 1024);
 #pragma unroll
           for (int k = 0; k < kStepK / 16; ++k) {  // 16 k: 8 columns of A, 32 bytes of a row of B
-            tc_mma_ta<1>(tmem, a + 8 * k, b + 2 * k, idesc, j > 0 || k > 0);
-            tc_mma_ta<1>(tmem + P::kAcc, a + kBlockColumns + 8 * k, b + 2 * k, idesc, j > 0 || k > 0);
+            tc_mma_ta(tmem, a + 8 * k, b + 2 * k, idesc, j > 0 || k > 0);
+            tc_mma_ta(tmem + P::kAcc, a + kBlockColumns + 8 * k, b + 2 * k, idesc, j > 0 || k > 0);
           }
           tc_commit<1>(smem_u32(&s.used[slot.i]));
           tc_commit<1>(smem_u32(&s.xused[buffer.i]));

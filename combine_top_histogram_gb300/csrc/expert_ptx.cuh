@@ -320,17 +320,6 @@ __device__ __forceinline__ void tc_ld32(uint32_t (&v)[32], uint32_t taddr) {
       : "r"(taddr)
       : "memory");
 }
-// 16 of them.
-__device__ __forceinline__ void tc_ld16(uint32_t (&v)[16], uint32_t taddr) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
-        "=r"(v[14]), "=r"(v[15])
-      : "r"(taddr)
-      : "memory");
-}
 __device__ __forceinline__ void tc_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -363,26 +352,14 @@ __device__ __forceinline__ void tc_wait_st() {
 }
 
 // Elected. One product of 16 k with A in tensor memory (fp16, two k a column).
-template <int CG>
 __device__ __forceinline__ void tc_mma_ta(uint32_t d, uint32_t a, uint64_t db, uint32_t idesc,
                                           bool accumulate) {
-#define MOE_TC_MMA_TA(GROUP)                                                                       \
-  asm volatile("{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\t"                        \
-               "setp.ne.b32 p, %4, 0;\n\t"                                                         \
-               "@q tcgen05.mma.cta_group::" GROUP ".kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"( \
-                   d),                                                                             \
-               "r"(a), "l"(db), "r"(idesc), "r"((uint32_t)accumulate)                              \
-               : "memory")
-  if constexpr (CG == 2) MOE_TC_MMA_TA("2");
-  else MOE_TC_MMA_TA("1");
-#undef MOE_TC_MMA_TA
-}
-
-__device__ __forceinline__ void tc_loaded(uint32_t (&v)[16]) {
-  asm volatile(""
-               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
-                 "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
-                 "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]));
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(db), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
 }
 
 // Shared-memory descriptor of an operand tile with 128-byte swizzled rows.
