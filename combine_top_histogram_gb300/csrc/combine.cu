@@ -57,8 +57,9 @@ __global__ void __launch_bounds__(kCombineThreads) k_combine(const CombineArgs p
   const int nvec = p.H >> 3;
   const int tid = threadIdx.x;
   const int k = K > 0 ? K : p.k;
-  pdl_wait();  // y (and inv, when dispatch ran just before) come from earlier kernels
-  pdl_trigger();
+  // y (and inv, when dispatch ran just before) come from earlier kernels. No early trigger: the
+  // result may be the tokens of a dispatch that follows, which loads them before its wait.
+  pdl_wait();
   for (long long g = p.g0 + blockIdx.x; g < p.T; g += gridDim.x) {
     int* rows_s = rows_buf[par];
     float* w_s = w_buf[par];

@@ -238,7 +238,10 @@ __device__ __forceinline__ bool row_ok(long long r, long long limit, uint32_t* s
 // right after that lets its own dependents launch (their CTAs then wait in
 // hardware). Because a kernel triggers only after its own wait, data written
 // two or more launches earlier is complete whenever a kernel starts, so it may
-// be read before the wait. Without the launch attribute the wait is a no-op.
+// be read before the wait. A dispatch also loads its x and w before it, so the kernels
+// that write what can be one of those (combine's result, routed weights without
+// a layout) never trigger: their dependents start when they have ended.
+// Without the launch attribute the wait is a no-op.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

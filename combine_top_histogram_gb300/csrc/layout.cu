@@ -183,8 +183,7 @@ __global__ void __launch_bounds__(256) k_route_only(const float* __restrict__ lo
                                                     int32_t* ids, float* w, long long T, int E,
                                                     int k) {
   const int lane = threadIdx.x & 31;
-  pdl_wait();
-  pdl_trigger();
+  pdl_wait();  // and no early trigger: a dispatch that follows loads w before its wait
   int K2 = 1;
   while (K2 < k) K2 <<= 1;
   const int G = 32 / K2;
