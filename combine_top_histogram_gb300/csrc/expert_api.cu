@@ -46,10 +46,10 @@ size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 // INT8 with many rows an expert: the codes of rows and weights are widened to
 // fp16 in memory for the product, which then runs at the paired fp16 rate and
 // not at that of the conversions on the way to it (expert_int8.cu). us, converted /
-// widened: down, H = 7168, F = 2048, E = 8, 1536 rows each 278 / 324, 2048 361 / 350,
-// 4096 665 / 583, E = 1, 4096 rows 103 / 81; gated 2048 646 / 722, 4096 1247 / 1244,
-// H = 4096, F = 1408, 8192 1044 / 997; small products lose the extra launches
-// (down, E = 1, H = 2048, F = 1024, 4096 rows 24.8 / 25.3). By the rows a configuration
+// widened (calls on their own, means of 20 within 0.2 %): down, H = 7168, F = 2048, E = 8, 1536
+// rows each 248 / 259, 2048 341 / 317, 4096 658 / 552, E = 1, 4096 rows 110 / 83; gated 2048
+// 646 / 674, 4096 1220 / 1187, H = 4096, F = 1408, 8192 1000 / 973; small products lose the
+// extra launches (down, E = 1, H = 2048, F = 1024, 4096 rows 28.6 / 29.1). By the rows a configuration
 // can have: a call of fewer takes the same way.
 bool widens(const moe_expert_config_t* c, moe::ExpertOp op) {
   return c->dtype == MOE_INT8 &&
@@ -94,10 +94,11 @@ moe::ExpertArgs expert_args(moe_expert_t x, const int32_t* offset) {
 // 113 / 92 at 32, 154 / 166 at 64. E = 8, H = 4096, F = 1408, gated bf16:
 // 48 / 42 at 32, 49 / 61 at 128. Above 64 rows the gain is a few per cent and
 // one expert with all of them would cost many passes. int8, whose tiles convert
-// what they read: gated 68 / 51 at 8 rows, 360 / 289 at 64, down 178 / 143 at 64;
-// E = 8, gated 41 / 29 at 24, 41 / 49 at 64, down 20.5 / 16.4 at 24; E = 1 (H =
-// 7168, F = 2048), gated 31 / 18 at 8 rows, 31 / 25 at 16, 31 / 39 at 32, down
-// 18.4 / 14.4 at 16: there up to 24 rows, whatever E is.
+// what they read (the caches empty, means of 60 within 0.2): gated 64.1 / 48.3 at 8 rows, 357 /
+// 290 at 64, down 174 / 141 at 64; E = 8, gated 39.5 / 29.2 at 24, 39.6 / 39.5 at 64, down
+// 20.3 / 16.3 at 24, 20.3 / 23.3 at 64; E = 1 (H = 7168, F = 2048), gated 26.4 / 16.9 at 8 rows,
+// 27.1 / 24.0 at 16, 27.1 / 31.2 at 24, 27.2 / 38.6 at 32, down 16.3 / 14.3 at 16, 16.3 / 17.3
+// at 24: there up to 24 rows, whatever E is, which one expert's 17 to 24 rows pay for.
 bool use_rows(const moe_expert_config_t* c, moe::ExpertOp op) {
   const long long E3 = 3ll * c->num_experts, rows = c->rows_max;
   const bool fp8_down = op == moe::kDown && c->dtype == MOE_FP8_E4M3;

@@ -10,10 +10,11 @@
 //
 // k_widen: codes as fp16, for the products of many rows an expert. It moves three
 // bytes a code at HBM's rate; the products that read them then run at the fp16
-// rate, while the kernel that converts on its way takes 1100 cycles and more
+// rate, while the kernel that converts on its way takes 1010 cycles and more
 // where the products alone take 768 (expert_int8.cu). Gated,
-// 8 experts and 65536 rows, Zipf(1.2), H = 4096, F = 1408: 1232 us converting on the
-// way, 1187 with codes widened first (widening 147 + 51, products 710, quantising 81).
+// 8 experts and 65536 rows, Zipf(1.2), H = 4096, F = 1408: 1022 us converting on the
+// way, 973 with codes widened first, each call on its own (of the launches of the second, under
+// the profiler: widening 147 + 51, products 710, quantising 81); back to back 1232 / 1187.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -189,9 +190,10 @@ cudaError_t launch_widen_weights(const ExpertArgs& p, long long weight_rows, con
 cudaError_t launch_expert_quantise(const ExpertArgs& p, const float* h, int8_t* codes,
                                    float* scale, int num_sms, cudaStream_t st) {
   const long long most = 16ll * num_sms;
-  // one warp / four (us, with the products; H = 256): E = 11, 3507 rows each, F = 464 58.5 / 77.7
-  // (H = 368), E = 8, 4000 rows, F = 640 52.8 / 67.4, F = 896 73.7 / 81.6, 1000 rows, F = 1008
-  // 29.9 / 31.2; longer rows are read twice by one warp, and the same by both
+  // one warp / four (us, with the products, means of 60 calls within 0.1; H = 256): E = 11, 3507
+  // rows each, F = 464 62.3 / 80.8 (H = 368), E = 8, 4000 rows, F = 640 56.2 / 70.4, F = 896
+  // 76.7 / 84.8, 1000 rows, F = 1008 33.4 / 35.1; from some 1200 on both take the same
+  // (F = 1264 39.6 / 39.6), and longer rows are read twice by one warp
   if (p.F <= 1024) {
     const long long ctas = (p.rows_max + kWarps - 1) / kWarps;
     return launch_pdl(k_expert_quantise<1>, dim3((unsigned)(ctas < most ? ctas : most)),

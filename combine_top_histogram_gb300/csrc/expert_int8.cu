@@ -17,10 +17,12 @@
 //   tokens (B)   64 n bytes in and out, 128 n of fp16 to shared memory
 // beside the 256 n that the products read. The weights' part is the same for any n,
 // so n is as large as tensor memory allows: 192, where 384 columns of accumulators
-// and 128 of weights fill it. Their 768 cycles of products then take about 1100; the
+// and 128 of weights fill it. Their 768 cycles of products then take 1010 to 1030 (by the
+// clocks of the issuing warp; 940 at 128 tokens, 830 to 870 at 64); the
 // vector pipes are 60-70 % busy by then, instruction issue 50-67 %, and the warps wait
 // on stores to tensor and shared memory in turn. Gated, E = 64, 512 rows each, H = 7168,
-// F = 2048: 1340 us, 1.44 PFLOP/s, 0.77 of the measured fp16 rate; products of many rows
+// F = 2048: 1310 to 1340 us a call on its own, 1.44 PFLOP/s, 0.77 of the measured fp16 rate, and
+// 1510 back to back, where the power limit lowers the clock; products of many rows
 // an expert are widened in memory first (expert_codes.cu).
 //
 // One persistent CTA per SM, or, where tiles are few and the reduction is long, a
@@ -34,8 +36,8 @@
 //                loads, conversions and stores run beside the next one's
 //   warps 20-27  read the accumulators 32 tokens at a time, scale and store them; with
 //                the last of them read the accumulators are handed back
-// Steps of 64 k and not 32 halve the waits and hand-overs of a tile (the case above:
-// 1590 us with 32).
+// Steps of 64 k and not 32 halve the waits and hand-overs of a tile (the case above, on
+// its own: 1590 us with 32).
 // Channels lie along the accumulator's lanes and tokens along its columns, so
 // a warp stores 32 neighbouring channels of one token at a time, and a short
 // segment shortens everything but the weights: its tokens are copied,
@@ -667,22 +669,29 @@ cudaError_t expert_int8_prepare() {
 }
 
 // The plan and the split with the least turns of the SMs x time of a full tile (a step of one at
-// 64 / 128 / 192 tokens: 0.43 / 0.47 / 0.51 us). An expert's weights are converted once for
-// each of its tiles, so a tile should hold most experts' rows; where tiles are
-// few, small ones spread over more SMs. The host knows the rows and the experts,
+// 64 / 128 / 192 tokens: 0.43 / 0.47 / 0.51 us, 850 / 940 / 1020 cycles at 2 GHz). An
+// expert's weights are converted once for each of its tiles, so a tile should hold most
+// experts' rows; where tiles are few, small ones spread over more SMs. The host knows the rows and the experts,
 // and takes the rows of one to be within two standard deviations of a random
-// choice of the experts. us of Few / Some / Many, gated, H = 7168, F = 2048,
-// random rows of E = 64: 56 on average 417 / 390 / 401, 96 719 / 408 / 433, 112
-// 720 / 475 / 444, 160 1060 / 791 / 486, 256 1567 / 957 / 911, 512 2947 / 1747 /
-// 1337, E = 256: 32 1359 / 1429 / 1494; down, E = 1, 1024 rows 50 / 41 / 46; gated, E = 8,
-// H = 1024, F = 512, 512 rows 27 / 21 / 23. What it gives away: experts of very
+// choice of the experts. us of Few / Some / Many (here and below of calls on their own, the
+// caches empty, means of 20 to 60 of each in turn, standard errors 1.3 us at most), gated,
+// H = 7168, F = 2048,
+// random rows of E = 64: 56 on average 418 / 391 / 398, 96 718 / 407 / 426, 112
+// 720 / 467 / 443, 160 1061 / 794 / 472, 256 1565 / 955 / 892, 512 2922 / 1733 /
+// 1317, E = 256: 32 1365 / 1432 / 1458; down, E = 1, 1024 rows 53 / 45 / 49; gated, E = 8,
+// H = 1024, F = 512, 512 rows 29 / 23 / 25. What it gives away: experts of very
 // unlike rows.
 // Where tiles leave SMs without work, clusters of 2, 4 or 8 CTAs share the reduction of one;
-// meeting costs them up to 10 us more. us of one CTA / clusters of 2 / 4 / 8, the caches
-// empty: down, E = 1, 64 rows, H = 4096, F = 14336 (16 tiles) 106 / 63 / 39 / 49, H = 7168,
-// F = 2048 (28) 22.6 / 22.5 / 18.4 / 32.8; gated, E = 7, 240 rows, H = 5488, F = 256 (14) 49 /
-// 37 / 27 / 25, E = 8, 200 rows, H = 4096, F = 1408 (88) 43 / 57 / 57 / 84, E = 4, 400 rows,
-// H = 1024, F = 512 (28) 18.4 / 22.5 / 18.4 / 32.8. Clusters of 8 have room on 14 x 8 SMs
+// meeting costs them up to 10 us more. us of one CTA / clusters of 2 / 4 / 8, tiles of 64
+// unless said otherwise (standard errors 0.1 at most): down, E = 1, 64 rows, H = 4096,
+// F = 14336 (16 tiles) 106.3 / 63.3 / 38.4 / 46.3, H = 7168, F = 2048 (28) 22.7 / 22.4 / 18.3 /
+// 32.6; gated, E = 1, 64 rows, H = 4096, F = 2048 (16) 39.4 / 32.0 / 23.1 / 31.5, E = 7, 240
+// rows, H = 5488, F = 256 (14) 49.4 / 35.3 / 25.1 / 23.1, E = 8, 200 rows, H = 4096,
+// F = 1408 (88) 39.8 / 51.6 / 51.7 / 81.7; down, E = 2, 300 rows, H = F = 4096, tiles of 192
+// (32) 42.9 / 38.4 / 26.5 / 54.0. Where they come near one another the rule may miss the
+// least: gated, E = 4, 400 rows, H = 1024, F = 512 it takes 18.9 / 21.2 / 18.0 (8 stages: no
+// clusters of 8) without clusters, E = 3, 450 rows, H = 4112, F = 400 tiles of 192 in clusters of
+// 8, 26.9, where tiles of 64 in clusters of 4 take 24.9. Clusters of 8 have room on 14 x 8 SMs
 // only, of 4 on 36 x 4: parts of the GPU have other numbers of SMs.
 struct Choice {
   double us;

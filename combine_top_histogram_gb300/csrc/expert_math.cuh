@@ -21,7 +21,8 @@ __device__ __forceinline__ float sigmoid(float g) {
 
 __device__ __forceinline__ float silu(float g) { return g * sigmoid(g); }
 
-// Four int8 codes as fp16, exactly: with the sign bit turned over a byte is
+// Four int8 codes as fp16, exactly, by the well-known way of putting an integer into the low bits
+// of a constant's significand and subtracting the constant: with the sign bit turned over a byte is
 // code + 128, as the low byte of an fp16 of 1024 it makes 1152 + code, and one
 // subtraction leaves the code. In order, .x the first two.
 __device__ __forceinline__ uint2 int8_to_f16(uint32_t codes) {

@@ -225,8 +225,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     };
     if constexpr (INT8) {
       // The conversions keep a warp busy for long, so the next piece is loaded into
-      // a place as soon as that is free (down of one token, E = 256, top-8, H = 7168,
-      // F = 2048: 37.9 / 24.5 us; the other types lose by it, gated e4m3 51 / 59 us).
+      // a place as soon as that is free (us of one token, E = 256, top-8, H = 7168, F = 2048, the
+      // caches empty, without / with: gated 84.5 / 48.0, down 56.1 / 28.5; the other types
+      // lose by it, e4m3 49.0 / 55.5 and 28.6 / 29.3).
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) load(u, ks + u * S);
       for (int c = ks; c < pieces; c += S * kAhead) {
@@ -367,8 +368,10 @@ cudaError_t launch(const ExpertArgs& p, const void* a, const void* b, int num_sm
   // two, one token of E = 256, top-8, H = 7168, F = 2048: down e4m3 24.2 / 24.3 /
   // 26.0, gated e4m3 55.8 / 44.4 / 44.2); two where the split's CTAs form clusters, which cost more (E = 64,
   // H = 2048, F = 1024, top-2: 11.7 / 11.2 / 9.6).
-  // int8 warps, which keep loading while they convert, need one (at three / one, L2 cold: gated
-  // 55 / 53, down 33 / 31).
+  // int8 warps, which keep loading while they convert, need one (the caches empty, means of 150 in
+  // turn within 0.1, three / one: gated 51.5 / 48.6, down 30.7 / 28.6; E = 8 of one row each,
+  // H = 4096, F = 1408 29.6 / 29.2 and 19.2 / 16.3; E = 64, H = 2048, F = 1024, top-2 the same;
+  // two tokens of the first, gated 86.7 / 85.6, but down 47.1 / 51.5).
   const long long enough =
       (TYPE == kInt8 ? 1ll : OP == kGated && TYPE == kE4m3 ? 2ll : 3ll) * num_sms;
   int s = 1;

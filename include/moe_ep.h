@@ -46,12 +46,15 @@
  *     g = s*T_r + t; assignment a = g*k + j (slot j of token g).
  *   - Kernels are launched with programmatic dependent launch: each waits for
  *     the previous grid on the stream before reading what that grid may have
- *     written, and lets its successor launch right after that wait.
+ *     written, and lets its successor launch right after that wait (those of
+ *     moe_combine*, moe_route_topk and the experts when they have ended).
  *     The dispatch entry points start loading x and w before their wait, so
  *     x and w must not be written by the immediately preceding kernel on the
  *     stream if that kernel lets its dependents launch before it finishes
- *     (kernels launched without programmatic dependent launch, and this
- *     library's own kernels, are fine).
+ *     (kernels launched without programmatic dependent launch are fine, and so
+ *     is what this library's calls write, but for the receive rows and metadata
+ *     of a dispatch and the stand-in's rows: where one of those is dispatched
+ *     again, a layout call or another kernel goes in between).
  *   - Every call on a handle that launches work is asynchronous and can be
  *     captured in a CUDA graph. Capture a layout call together with the dispatch that
  *     follows it: the layout records on the host that the per-source tables
@@ -268,8 +271,8 @@ int moe_dispatch(moe_handle_t h, const void *x, const float *w, void *recv_x,
  * within a token) is not written, gets inv = -1 and sets
  * MOE_STATUS_SLOT_OVERFLOW. Needs a preceding layout call on a handle
  * without capacity (MOE_ERR_UNSUPPORTED otherwise, or when the rows exceed
- * int32). slot_x: moe_fixed_slot_rows(cfg) rows of H elements (bf16, or e4m3
- * with fp32 slot_scale [rows, H/128]); meta arrays of that many rows. Same
+ * int32). slot_x: moe_fixed_slot_rows(cfg) rows of H elements (bf16, e4m3
+ * with fp32 slot_scale [rows, H/128], or int8 with fp32 slot_scale [rows]); meta arrays of that many rows. Same
  * payload, scales and metadata per assignment as moe_dispatch; inv holds the
  * slot rows, so moe_combine / moe_expert_standin (which then treats the slot
  * layout) work unchanged on the slot buffers. */
@@ -321,7 +324,7 @@ int moe_set_wait_limit(moe_handle_t h, int64_t polls);
  * of each (source, expert) segment into the receive regions. Produces exactly
  * what moe_dispatch produces (same receive rows, metadata and inv), through one
  * more full write + read of the payload. send_x: rows_max rows like recv_x;
- * send_scale: rows_max x H/128 fp32 for FP8 (NULL for BF16). */
+ * send_scale: rows_max x H/128 fp32 for FP8, rows_max for INT8 (NULL for BF16). */
 int moe_dispatch_two_stage(moe_handle_t h, const void *x, const float *w, void *send_x,
                            float *send_scale, void *recv_x, float *recv_scale,
                            const moe_recv_meta_t *meta, void *stream);
@@ -453,9 +456,10 @@ typedef struct moe_expert *moe_expert_t;
 
 /* Bytes of device workspace of a handle (0 if *cfg is invalid): control words
  * and, for training, the gradient of the pre-activations [rows_max, 2F], or,
- * for INT8, h before its quantisation (fp32 [rows_max, F]) and, from 2048 rows
- * an expert on, copies in fp16 of the rows of a product and of the weights (one
- * of the w2's size, or from 4096 rows on of w13's). The kernels of a call follow
+ * for INT8, h before its quantisation (fp32 [rows_max, F]) and, where rows_max
+ * is at least 2048 num_experts and rows_max * H * F at least 2^34, copies in
+ * fp16 of the rows of a product and of the weights (one of w2's size, or from
+ * 4096 num_experts rows on of w13's: MOE_FORM_WIDENED). The kernels of a call follow
  * rows_max and not the rows that it finds in expert_offset: a program that
  * serves both large batches and single tokens has a handle for each. */
 size_t moe_expert_workspace_bytes(const moe_expert_config_t *cfg);
